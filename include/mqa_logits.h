@@ -72,7 +72,8 @@ typedef enum {
  */
 typedef enum {
   MQA_F32 = 0,
-  MQA_BF16 = 1
+  MQA_BF16 = 1,
+  MQA_F16 = 2    /* only paged_attention's q and out, paged_kv_write's x */
 } mqa_float;
 
 /*
@@ -268,6 +269,115 @@ mqa_status paged_mqa_logits(mqa_dtype dt,
                             int32_t clean_logits, mqa_float weights_type,
                             mqa_float logits_type, mqa_precision precision,
                             hipStream_t stream);
+
+/*
+ * Block tables and slot maps of one step, from request lengths.
+ *   context_lens [batch] int32: tokens of each sequence including its new
+ *            ones, clamped to [0, max_context_len]
+ *   new_lens [batch] int32: how many of them are new, clamped to
+ *            [0, context_lens]; a fresh prompt has new_lens = context_lens
+ *   free_blocks [num_free] int32: ids of free blocks, in the order to take them
+ *   block_table [batch, block_table_stride] int32, read and written: with
+ *            old = context - new, sequence b already has its first
+ *            ceil(old / block_size) entries and gets entries up to
+ *            ceil(context / block_size) from free_blocks (sequence after
+ *            sequence).  No other entry is written.
+ *   slots    [max_tokens] int64: the new tokens, sequence after sequence; token
+ *            at position j has slot block_table[b][j / block_size] * block_size
+ *            + j % block_size.  -1 behind the last new token (a padded batch),
+ *            and where the block is missing: the id is outside
+ *            [0, num_blocks), or the free list ran out.  New tokens past
+ *            max_tokens have no slot.
+ *   token_offsets [batch + 1] int32: where each sequence's new tokens start
+ *            among all of them, and their total (it may exceed max_tokens)
+ *   blocks_taken [1] int32: free blocks asked for.  More than num_free: the
+ *            list ran out, and the entries beyond it are -1.
+ * free_blocks is not changed: the next step starts blocks_taken further on.
+ * The same call again writes the same values.  Requires 1 <= batch <= 8192,
+ * block_size in {16, 32, 64}, block_table_stride >= ceil(max_context_len /
+ * block_size), batch * max_context_len < 2^31.  The arrays must not overlap.
+ */
+mqa_status paged_kv_slots(const int32_t* context_lens, const int32_t* new_lens,
+                          const int32_t* free_blocks, int32_t num_free,
+                          int32_t* block_table, int64_t block_table_stride,
+                          int64_t* slots, int32_t* token_offsets, int32_t* blocks_taken,
+                          int32_t batch, int32_t block_size, int32_t num_blocks,
+                          int32_t max_context_len, int32_t max_tokens, hipStream_t stream);
+
+/*
+ * Quantises rows and stores them in a pool that paged_mqa_logits (one head) or
+ * paged_attention (MXFP4) reads.
+ *   x        [rows, heads, D] of x_type (fp32, bf16 or fp16); x_stride and
+ *            x_head_stride in elements from row to row and from head to head
+ *            (whole 16-byte pieces, at least D), elements of a head adjacent
+ *   slots    [rows] int64: pool slot of each row (block * block_size + offset);
+ *            rows with slots outside [0, num_slots) are not stored.  Slots that
+ *            are stored must differ: of two rows with one slot either may stay,
+ *            or parts of both.
+ *   pool     [num_slots, heads, D] bytes (fp4: D/2)
+ *   sf_pool  [num_slots, heads, D/32] e8m0 bytes (MX formats, else NULL)
+ *   scale_pool [num_slots, heads] fp32 (MQA_FP8_E4M3, else NULL)
+ *   values   NULL, or [rows, heads, D] of x_type: what the codes stand for,
+ *            rounded to x_type, for every row (stored or not).  It may be x
+ *            itself when x is contiguous.
+ * Every 32 elements (MX) or all D of a head (FP8) share the smallest
+ * power-of-two scale under which none exceeds the largest code (448 or 6), at
+ * least 2^-127 (FP8: 2^-126), and 1 for zeros; codes are the elements over the
+ * scale rounded to nearest, ties to even.  A group that holds an infinity or
+ * NaN gets code 0 and a NaN scale (e8m0: 255).
+ */
+mqa_status paged_kv_write(mqa_dtype dt, const void* x, mqa_float x_type, int64_t x_stride,
+                          int64_t x_head_stride, const int64_t* slots, uint8_t* pool,
+                          uint8_t* sf_pool, float* scale_pool, void* values,
+                          int64_t num_slots, int32_t rows, int32_t heads, int32_t d,
+                          hipStream_t stream);
+
+/*
+ * Softmax attention over a paged MXFP4 cache, whole contexts or the columns
+ * that mqa_logits_topk selected (the sparse attention that reads `indices` on
+ * the "FlashMLA" page, flash_mla_with_kvcache; next_n query tokens per
+ * sequence as in PR #314, 12cb7c0).
+ *   dt       MQA_MXFP4_E2M1 (the only format)
+ *   q        [batch*next_n, Hq, D] bf16 or fp16 (q_type); row r = b*next_n + t;
+ *            q_stride elements from row to row (a multiple of 8, >= Hq * D)
+ *   k_pool, v_pool [num_blocks, block_size, Hkv, D/2] packed e2m1
+ *   k_sf_pool, v_sf_pool [num_blocks, block_size, Hkv, D/32] e8m0; bytes over
+ *            252 (products beyond fp32) count as NaN
+ *   context_lens, block_table, max_context_len: as paged_mqa_logits; row
+ *            b*next_n + t sees keys
+ *            [0, clamp(ctx_b - next_n + t + 1, 0, min(ctx_b, max_context_len)))
+ *   indices  NULL with topk = 0: every row attends to all keys it sees; or
+ *            [batch*next_n, indices_stride] int32: row r attends to the keys
+ *            among its first topk entries that it sees, any other entry (-1)
+ *            is passed over; a key listed twice counts twice
+ *   scale    finite factor of <q, k>
+ *   out      [batch*next_n, Hq, D] of q_type; head h reads KV head
+ *            h / (Hq / Hkv).  0 for a row without keys.
+ *   lse      NULL or [batch*next_n, Hq] fp32: log(sum exp(scale <q, k>)), -inf
+ *            for a row without keys
+ *   workspace of at least paged_attention_workspace_size bytes for the same
+ *            sizes (NULL if that is 0), 16-byte aligned.  Its contents matter
+ *            only during the call: calls that may run at the same time need
+ *            workspaces of their own.
+ * Keys outside a row's range never reach its result, whatever the cache holds
+ * there.  Requires D in {64, 128}, Hkv <= 256, Hq a multiple of Hkv and at
+ * most 1024, 1 <= batch <= 8192, 1 <= next_n <= 16, block_size in
+ * {16, 32, 64}, num_blocks * block_size < 2^31, topk <= 2^20.
+ */
+int64_t paged_attention_workspace_size(int32_t batch, int32_t next_n, int32_t hq, int32_t hkv,
+                                       int32_t d, int32_t max_context_len,
+                                       int32_t topk);   /* bytes; negative on error */
+mqa_status paged_attention(mqa_dtype dt, const void* q, mqa_float q_type, int64_t q_stride,
+                           const uint8_t* k_pool, const uint8_t* k_sf_pool,
+                           const uint8_t* v_pool, const uint8_t* v_sf_pool,
+                           const int32_t* context_lens,
+                           const int32_t* block_table, int64_t block_table_stride,
+                           const int32_t* indices, int64_t indices_stride, int32_t topk,
+                           float scale, void* out, float* lse,
+                           void* workspace, int64_t workspace_bytes,
+                           int32_t batch, int32_t next_n, int32_t hq, int32_t hkv, int32_t d,
+                           int32_t block_size, int32_t num_blocks, int32_t max_context_len,
+                           hipStream_t stream);
 
 /* Compute units of a device (the get_num_sms analogue of the DeepGEMM
  * article's paged example); negative on error. */

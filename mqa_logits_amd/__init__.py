@@ -14,6 +14,9 @@ Entry points (same names as the C ABI):
   mqa_logits_compressed           packed logits
   paged_mqa_logits_metadata       paged work split
   paged_mqa_logits                paged decode logits
+  paged_kv_slots                  block-table entries and slot map of a step's new tokens
+  paged_kv_write                  quantise rows and store them at their slots
+  paged_attention                 attention over a paged MXFP4 cache, whole or selected keys
   mqa_num_cus, paged_mqa_logits_default_splits
 """
 
@@ -31,6 +34,9 @@ FORMATS = {"fp8": 0, "mxfp8": 1, "mxfp4": 2}
 PRECISIONS = {"default": 0, "exact": 1}
 # mqa_float of the C ABI: element type of the weights and of the logits
 FLOAT_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+ROW_TYPES = {**FLOAT_TYPES, torch.float16: 2}      # paged_kv_write's rows
+QUERY_TYPES = {torch.bfloat16: 1, torch.float16: 2}    # paged_attention's q and output
+BLOCK_SIZES = (16, 32, 64)
 
 
 class MqaError(RuntimeError):
@@ -59,6 +65,10 @@ def _load():
         "paged_mqa_logits_metadata": [P, I32, I32, I32, I32, I32, P, P],
         "paged_mqa_logits": [I32, P, P, P, P, P, P, P, P, I64, P, P, I64,
                              I32, I32, I32, I32, I32, I32, I32, I32, I32, I32, I32, I32, P],
+        "paged_kv_slots": [P, P, P, I32, P, I64, P, P, P, I32, I32, I32, I32, I32, P],
+        "paged_kv_write": [I32, P, I32, I64, I64, P, P, P, P, P, I64, I32, I32, I32, P],
+        "paged_attention": [I32, P, I32, I64, P, P, P, P, P, P, I64, P, I64, I32, ctypes.c_float,
+                            P, P, P, I64, I32, I32, I32, I32, I32, I32, I32, I32, P],
     }
     for name, argtypes in sigs.items():
         fn = getattr(lib, name)
@@ -67,6 +77,8 @@ def _load():
     for name in ("paged_mqa_logits_metadata_size", "mqa_logits_metadata_size"):
         getattr(lib, name).argtypes = [I32]
         getattr(lib, name).restype = I64
+    lib.paged_attention_workspace_size.argtypes = [I32] * 7
+    lib.paged_attention_workspace_size.restype = I64
     lib.mqa_num_cus.argtypes = [I32]
     lib.mqa_num_cus.restype = I32
     lib.paged_mqa_logits_default_splits.argtypes = [I32]
@@ -81,7 +93,8 @@ lib = _load()
 EXPORTED = ("mqa_logits", "mqa_logits_metadata_size", "mqa_logits_metadata", "mqa_logits_topk",
             "mqa_logits_compressed_offsets", "mqa_logits_compressed",
             "paged_mqa_logits_metadata_size", "paged_mqa_logits_metadata",
-            "paged_mqa_logits", "mqa_num_cus", "paged_mqa_logits_default_splits",
+            "paged_mqa_logits", "paged_kv_slots", "paged_kv_write",
+            "paged_attention_workspace_size", "paged_attention", "mqa_num_cus", "paged_mqa_logits_default_splits",
             "mqa_last_error")
 
 
@@ -392,3 +405,183 @@ def paged_mqa_logits(fmt, q, q_sf, kv_pool, kv_sf_pool, kv_scale_pool, weights,
         1 if clean_logits else 0, _float_type(weights.dtype, "weights"),
         _float_type(out.dtype, "logits"), _precision(precision), _stream(q)))
     return out
+
+
+def _call(fn, t, *args):
+    """fn(*args, stream) on the device of t (kernels go to the current device)."""
+    if torch.cuda.current_device() == t.get_device():
+        _check(fn(*args, _stream(t)))
+    else:
+        with torch.cuda.device(t.device):
+            _check(fn(*args, _stream(t)))
+
+
+def _data(t):
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _row_stride(t, width):
+    """Elements from row to row of a tensor whose rows of `width` are contiguous."""
+    return t.stride(0) if t.shape[0] > 1 else max(width, 1)
+
+
+def _block_size(block_size):
+    if block_size not in BLOCK_SIZES:
+        raise ValueError(f"block_size must be one of {BLOCK_SIZES}, got {block_size}")
+
+
+def _table(a, block_table, batch, block_size, max_context_len):
+    """A block table whose rows reach max_context_len; returns its row stride."""
+    a.want(block_table, "block_table", (batch, None), I32_T, rows=True)
+    need = -(-max_context_len // block_size)
+    if block_table.shape[1] < need:
+        raise ValueError(f"block_table rows must hold ceil(max_context_len / block_size) = {need} "
+                         f"blocks, got {block_table.shape[1]}")
+    return _row_stride(block_table, block_table.shape[1])
+
+
+def paged_kv_slots(context_lens, new_lens, free_blocks, block_table, num_blocks, block_size,
+                   max_context_len, max_tokens, out=None):
+    """Block-table entries and slot map of a step's new tokens.
+
+    context_lens counts the new_lens new tokens; block_table (int32, updated in
+    place) gets the blocks they need from free_blocks in order.  Returns (slots
+    int64 [max_tokens], -1 padded; token_offsets int32 [batch + 1];
+    blocks_taken int32 [1], which exceeds len(free_blocks) when the list ran
+    out); `out` may hold these three."""
+    _block_size(block_size)
+    if max_tokens < 0 or max_context_len < 0:
+        raise ValueError("max_tokens and max_context_len must not be negative")
+    a = _Args()
+    batch = context_lens.shape[0]
+    a.want(context_lens, "context_lens", (batch,), I32_T)
+    a.want(new_lens, "new_lens", (batch,), I32_T)
+    a.want(free_blocks, "free_blocks", (None,), I32_T)
+    stride = _table(a, block_table, batch, block_size, max_context_len)
+    if out is None:
+        dev = context_lens.device
+        out = (torch.empty(max_tokens, dtype=torch.int64, device=dev),
+               torch.empty(batch + 1, dtype=torch.int32, device=dev),
+               torch.empty(1, dtype=torch.int32, device=dev))
+    slots, offsets, taken = out
+    a.want(slots, "slots", (max_tokens,), I64_T)
+    a.want(offsets, "token_offsets", (batch + 1,), I32_T)
+    a.want(taken, "blocks_taken", (1,), I32_T)
+    a.on_gpu()
+    _call(lib.paged_kv_slots, context_lens, _data(context_lens), _data(new_lens),
+          _data(free_blocks), free_blocks.shape[0], _data(block_table), stride, _data(slots),
+          _data(offsets), _data(taken), batch, block_size, num_blocks, max_context_len, max_tokens)
+    return slots, offsets, taken
+
+
+def paged_kv_write(fmt, x, slots, kv_pool, kv_sf_pool=None, kv_scale_pool=None, values=None):
+    """Quantise rows x [n, D] or [n, heads, D] (fp32, bf16 or fp16; rows and
+    heads may be strided) and store them at `slots` (int64 [n]; outside the
+    pool: not stored) of kv_pool [num_blocks, block_size(, heads), D or D/2]
+    with kv_sf_pool [.., D/32] (MX formats) or kv_scale_pool (fp8).  Slots that
+    are stored must differ.  values (x's shape and type, contiguous) receives
+    what the codes stand for."""
+    _fmt(fmt)
+    a = _Args()
+    if x.dim() not in (2, 3) or x.dtype not in ROW_TYPES:
+        raise ValueError(f"x must be [n, D] or [n, heads, D] of {sorted(map(str, ROW_TYPES))}, "
+                         f"got {tuple(x.shape)} {x.dtype}")
+    n, d = x.shape[0], x.shape[-1]
+    heads = x.shape[1] if x.dim() == 3 else 1
+    a.want(x, "x", tuple(x.shape), rows=True)
+    a.want(slots, "slots", (n,), I64_T)
+    lead = (None, None) + tuple(x.shape[1:-1])
+    a.want(kv_pool, "kv_pool", (*lead, d // 2 if fmt == "mxfp4" else d), itemsize=1)
+    lead = tuple(kv_pool.shape[:-1])
+    if fmt == "fp8":
+        if kv_sf_pool is not None:
+            raise ValueError("fp8 takes no block scales (kv_sf_pool)")
+        a.want(kv_scale_pool, "kv_scale_pool", lead, (torch.float32,))
+    else:
+        if kv_scale_pool is not None:
+            raise ValueError(f"{fmt} takes no kv_scale_pool")
+        a.want(kv_sf_pool, "kv_sf_pool", (*lead, d // 32), itemsize=1)
+    if values is not None:
+        a.want(values, "values", tuple(x.shape), (x.dtype,))
+    a.on_gpu()
+    _call(lib.paged_kv_write, x, _fmt(fmt), _data(x), ROW_TYPES[x.dtype], _row_stride(x, d),
+          x.stride(1) if heads > 1 else d, _data(slots), _data(kv_pool), _data(kv_sf_pool),
+          _data(kv_scale_pool), _data(values), kv_pool.shape[0] * kv_pool.shape[1], n, heads, d)
+    return values
+
+
+def paged_attention_workspace_size(batch, next_n, q_heads, kv_heads, d, max_context_len, topk=0):
+    """Bytes of workspace of a paged_attention call of these sizes."""
+    n = lib.paged_attention_workspace_size(batch, next_n, q_heads, kv_heads, d, max_context_len,
+                                           topk)
+    if n < 0:
+        raise MqaError(2, lib.mqa_last_error().decode())
+    return n
+
+
+def paged_attention(fmt, q, k_pool, k_sf_pool, v_pool, v_sf_pool, context_lens, block_table,
+                    next_n, max_context_len, scale=None, indices=None, out=None, lse=None,
+                    return_lse=False, workspace=None):
+    """Attention of next_n query tokens a sequence over a paged 4-bit cache.
+
+    fmt "mxfp4"; q [batch * next_n, Hq, D] bf16 or fp16 (rows may be strided),
+    pools [num_blocks, block_size, Hkv, D/2] with e8m0 [.., D/32].  Row
+    b * next_n + t sees the first context_lens[b] - next_n + 1 + t keys; with
+    indices (int32 [rows, topk], as mqa_logits_topk gives them) it attends to
+    the listed ones among them.  scale defaults to D ** -0.5.  Returns out
+    (q's shape and type; zeros for a row without keys), or (out, lse fp32
+    [rows, Hq]) with return_lse or an lse to fill.  workspace: a uint8 tensor
+    of paged_attention_workspace_size bytes to keep between calls on one
+    stream, or None."""
+    if fmt != "mxfp4":
+        _fmt(fmt)
+        raise ValueError(f"paged_attention reads an mxfp4 cache, got {fmt!r}")
+    a = _Args()
+    if q.dim() != 3 or q.dtype not in QUERY_TYPES:
+        raise ValueError(f"q must be [rows, Hq, D] of bfloat16 or float16, got {tuple(q.shape)} {q.dtype}")
+    if k_pool.dim() != 4:
+        raise ValueError(f"k_pool must be [num_blocks, block_size, Hkv, D/2], got {tuple(k_pool.shape)}")
+    rows, hq, d = q.shape
+    batch = context_lens.shape[0]
+    num_blocks, block_size, hkv = k_pool.shape[:3]
+    _block_size(block_size)
+    if max_context_len < 0:
+        raise ValueError("max_context_len must not be negative")
+    if rows != batch * next_n:
+        raise ValueError(f"q must have batch * next_n = {batch * next_n} rows, got {rows}")
+    if q.stride(2) != 1 or (hq > 1 and q.stride(1) != d):
+        raise ValueError("q rows must be contiguous")
+    a.want(q[:0], "q", (0, hq, d))
+    lead = (num_blocks, block_size, hkv)
+    for name, codes, sf in (("k", k_pool, k_sf_pool), ("v", v_pool, v_sf_pool)):
+        a.want(codes, name + "_pool", (*lead, d // 2), itemsize=1)
+        a.want(sf, name + "_sf_pool", (*lead, d // 32), itemsize=1)
+    a.want(context_lens, "context_lens", (batch,), I32_T)
+    stride = _table(a, block_table, batch, block_size, max_context_len)
+    topk = 0
+    if indices is not None:
+        a.want(indices, "indices", (rows, None), I32_T, rows=True)
+        topk = indices.shape[1]
+        if topk < 1:
+            raise ValueError("indices must have at least one column")
+    if out is None:
+        out = torch.empty((rows, hq, d), dtype=q.dtype, device=q.device)
+    a.want(out, "out", (rows, hq, d), (q.dtype,))
+    if lse is None and return_lse:
+        lse = torch.empty((rows, hq), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        a.want(lse, "lse", (rows, hq), (torch.float32,))
+    need = paged_attention_workspace_size(batch, next_n, hq, hkv, d, max_context_len, topk)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace is not None:
+        a.want(workspace, "workspace", (None,), itemsize=1)
+    a.on_gpu()
+    _call(lib.paged_attention, q, _fmt(fmt), _data(q), QUERY_TYPES[q.dtype],
+          _row_stride(q, hq * d), _data(k_pool), _data(k_sf_pool), _data(v_pool), _data(v_sf_pool),
+          _data(context_lens), _data(block_table), stride, _data(indices),
+          0 if indices is None else _row_stride(indices, topk), topk,
+          d ** -0.5 if scale is None else float(scale), _data(out), _data(lse), _data(workspace),
+          0 if workspace is None else workspace.numel(), batch, next_n, hq, hkv, d, block_size,
+          num_blocks, max_context_len)
+    return out if lse is None else (out, lse)

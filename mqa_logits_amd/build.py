@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libmqa_logits.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["dense.hip", "dense_bf16.hip", "dense_sched.hip", "dense_sched_bf16.hip",
-           "topk.hip", "paged.hip", "api.cpp"]
+           "topk.hip", "paged.hip", "attention.hip", "cache.hip", "api.cpp"]
 # measurement aid for bench.py, linked into a library of its own
 PROBE_SOURCES = ["peak.hip"]
 PROBE_LIB = os.path.join(PKG, "libmqa_peak.so")
@@ -32,15 +32,20 @@ COMMON_FLAGS = [
     "-I", os.path.join(ROOT, "include"), "-I", CSRC,
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-function",
-    # Accumulators in VGPRs (the Q operands are pinned to AGPRs), and no NaN
-    # canonicalisation in front of each ReLU max.
-    "-mllvm", "-amdgpu-mfma-vgpr-form=1", "-fno-honor-nans",
+    # Accumulators in VGPRs (in the logits kernels the Q operands are pinned to
+    # AGPRs; attention rescales its accumulators on the vector ALU).
+    "-mllvm", "-amdgpu-mfma-vgpr-form=1",
 ]
+# No NaN canonicalisation in front of each ReLU max; the cache and attention
+# kernels pass NaNs on and are built without it.
+NO_NANS = ["-fno-honor-nans"]
+HONOR_NANS = ("attention.hip", "cache.hip")
 
 
 def _compile(src):
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-    cmd = [HIPCC, *COMMON_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+    flags = COMMON_FLAGS if src in HONOR_NANS else COMMON_FLAGS + NO_NANS
+    cmd = [HIPCC, *flags, "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     noise = "is not a recognized feature for this target"
     err = "\n".join(l for l in r.stderr.splitlines() if noise not in l)

@@ -8,6 +8,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
+#include <cstring>
 #include <string>
 
 #include "launch.hpp"
@@ -42,6 +43,10 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 // buffer resources with 32-bit offsets; every such range must stay below this
 // many bytes (the kernels' out-of-range marker sits just above it).
 constexpr int64_t kMaxRangeBytes = 0x7ff00000;
+
+// Workgroups that paged_attention aims for, and the fewest keys of one.
+constexpr int64_t kAttnTarget = 2048;
+constexpr int64_t kAttnMinChunk = 256;
 
 bool debug_enabled() {
   static const bool on = [] {
@@ -157,6 +162,49 @@ mqa_status run_dense(mqa_dtype dt, const void* q, const uint8_t* q_sf, const voi
             who, (int)dt, h, d, store, (int)weights_type, (int)logits_type, exact, sq, skv,
             p.n_chunks, (long long)grid);
   return hip_status(mqa::launch_dense((int)dt, h, d, store, out_type, p, stream), who);
+}
+
+// How paged_attention splits its work.  A unit is a sequence, or a query token
+// when it has indices of its own; its next_n * group (or group) rows of a KV
+// head go to workgroups of 16 * row_tiles rows, its keys to workgroups of
+// `chunk` keys.
+struct AttnPlan {
+  int32_t units, row_tiles, row_groups, chunk, chunks;
+};
+
+AttnPlan plan_attention(int32_t batch, int32_t next_n, int32_t hq, int32_t hkv,
+                        int32_t max_context_len, int32_t topk) {
+  AttnPlan a{};
+  const int32_t group = hq / hkv;
+  a.units = topk ? batch * next_n : batch;
+  const int32_t tiles = ((topk ? group : next_n * group) + 15) / 16;
+  a.row_tiles = tiles == 1 ? 1 : tiles == 2 ? 2 : 4;
+  a.row_groups = (tiles + a.row_tiles - 1) / a.row_tiles;
+  const int64_t length = topk ? topk : max_context_len;
+  const int64_t base = (int64_t)a.units * hkv * a.row_groups;
+  const int64_t want = (kAttnTarget + base - 1) / base;
+  int64_t chunk = (length + want - 1) / want;
+  chunk = (chunk + 127) / 128 * 128;
+  if (chunk < kAttnMinChunk) chunk = kAttnMinChunk;
+  if (chunk > mqa::kAttnMaxChunk) chunk = mqa::kAttnMaxChunk;
+  a.chunk = (int32_t)chunk;
+  a.chunks = length > chunk ? (int32_t)((length + chunk - 1) / chunk) : 1;
+  return a;
+}
+
+int32_t block_shift(int32_t block_size) { return block_size == 16 ? 4 : block_size == 32 ? 5 : 6; }
+
+mqa_status check_attention_shape(int32_t batch, int32_t next_n, int32_t hq, int32_t hkv, int32_t d,
+                                 int32_t max_context_len, int32_t topk, const char* who) {
+  if (batch < 1 || batch > 8192) return fail(MQA_ERR_UNSUPPORTED, "%s: batch=%d not in [1, 8192]", who, batch);
+  if (next_n < 1 || next_n > 16) return fail(MQA_ERR_UNSUPPORTED, "%s: next_n=%d not in [1, 16]", who, next_n);
+  if (hkv < 1 || hkv > 256 || hq < hkv || hq > 1024 || hq % hkv)
+    return fail(MQA_ERR_UNSUPPORTED, "%s: Hq=%d must be a multiple of Hkv=%d, at most 1024 and 256", who, hq, hkv);
+  if (d != 64 && d != 128) return fail(MQA_ERR_UNSUPPORTED, "%s: D=%d not supported (64, 128)", who, d);
+  if (max_context_len < 0) return fail(MQA_ERR_INVALID_ARG, "%s: negative max_context_len", who);
+  if (max_context_len > (1 << 30)) return fail(MQA_ERR_UNSUPPORTED, "%s: max_context_len=%d too large", who, max_context_len);
+  if (topk < 0 || topk > (1 << 20)) return fail(MQA_ERR_INVALID_ARG, "%s: topk=%d not in [0, 2^20]", who, topk);
+  return MQA_OK;
 }
 
 mqa_status check_precision(mqa_precision precision, const char* who) {
@@ -394,6 +442,186 @@ mqa_status paged_mqa_logits(mqa_dtype dt, const void* q, const uint8_t* q_sf, co
   const int out_type = logits_type == MQA_BF16 ? mqa::kBF16 : mqa::kF32;
   return hip_status(mqa::launch_paged((int)dt, h, d, clean_logits ? 1 : 0, out_type, p, stream),
                     who);
+}
+
+mqa_status paged_kv_slots(const int32_t* context_lens, const int32_t* new_lens,
+                          const int32_t* free_blocks, int32_t num_free, int32_t* block_table,
+                          int64_t block_table_stride, int64_t* slots, int32_t* token_offsets,
+                          int32_t* blocks_taken, int32_t batch, int32_t block_size,
+                          int32_t num_blocks, int32_t max_context_len, int32_t max_tokens,
+                          hipStream_t stream) {
+  const char* who = "paged_kv_slots";
+  if (batch < 1 || batch > 8192) return fail(MQA_ERR_UNSUPPORTED, "%s: batch=%d not in [1, 8192]", who, batch);
+  if (block_size != 16 && block_size != 32 && block_size != 64)
+    return fail(MQA_ERR_UNSUPPORTED, "%s: block_size=%d not in {16, 32, 64}", who, block_size);
+  if (num_blocks < 1 || num_free < 0 || max_context_len < 0 || max_tokens < 0)
+    return fail(MQA_ERR_INVALID_ARG, "%s: negative size or num_blocks < 1", who);
+  if ((int64_t)batch * max_context_len >= 0x7fffffff)
+    return fail(MQA_ERR_UNSUPPORTED, "%s: batch * max_context_len overflows int32", who);
+  if (!context_lens || !new_lens || (max_context_len > 0 && !block_table) || !token_offsets ||
+      !blocks_taken || (num_free > 0 && !free_blocks) || (max_tokens > 0 && !slots))
+    return fail(MQA_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!aligned(context_lens, 4) || !aligned(new_lens, 4) || !aligned(free_blocks, 4) ||
+      !aligned(block_table, 4) || !aligned(slots, 8) || !aligned(token_offsets, 4) ||
+      !aligned(blocks_taken, 4))
+    return fail(MQA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+  if (block_table_stride < ((int64_t)max_context_len + block_size - 1) / block_size)
+    return fail(MQA_ERR_INVALID_ARG, "%s: block_table_stride < ceil(max_context_len / block_size)", who);
+  mqa::SlotParams p{};
+  p.ctx = context_lens;
+  p.new_lens = new_lens;
+  p.free_ids = free_blocks;
+  p.bt = block_table;
+  p.bt_stride = block_table_stride;
+  p.slots = slots;
+  p.offsets = token_offsets;
+  p.taken = blocks_taken;
+  p.batch = batch;
+  p.num_free = num_free;
+  p.num_blocks = num_blocks;
+  p.bs_shift = block_shift(block_size);
+  p.max_ctx = max_context_len;
+  p.max_tokens = max_tokens;
+  return hip_status(mqa::launch_kv_slots(p, stream), who);
+}
+
+mqa_status paged_kv_write(mqa_dtype dt, const void* x, mqa_float x_type, int64_t x_stride,
+                          int64_t x_head_stride, const int64_t* slots, uint8_t* pool,
+                          uint8_t* sf_pool, float* scale_pool, void* values, int64_t num_slots,
+                          int32_t rows, int32_t heads, int32_t d, hipStream_t stream) {
+  const char* who = "paged_kv_write";
+  if (dt != MQA_FP8_E4M3 && dt != MQA_MXFP8_E4M3 && dt != MQA_MXFP4_E2M1)
+    return fail(MQA_ERR_INVALID_ARG, "%s: unknown dtype %d", who, (int)dt);
+  if (x_type != MQA_F32 && x_type != MQA_BF16 && x_type != MQA_F16)
+    return fail(MQA_ERR_INVALID_ARG, "%s: unknown element type %d", who, (int)x_type);
+  if (d != 64 && d != 128) return fail(MQA_ERR_UNSUPPORTED, "%s: D=%d not supported (64, 128)", who, d);
+  if (heads < 1 || heads > 1024) return fail(MQA_ERR_UNSUPPORTED, "%s: heads=%d not in [1, 1024]", who, heads);
+  if (rows < 0 || num_slots < 0) return fail(MQA_ERR_INVALID_ARG, "%s: negative rows or num_slots", who);
+  if ((int64_t)rows * heads > 0x7fffff00)
+    return fail(MQA_ERR_UNSUPPORTED, "%s: rows * heads overflows int32", who);
+  if (rows == 0) return ok();
+  const int64_t per16 = x_type == MQA_F32 ? 4 : 8;   // elements of 16 bytes
+  if ((rows > 1 && x_stride % per16) || (heads > 1 && x_head_stride % per16))
+    return fail(MQA_ERR_INVALID_ARG, "%s: strides must be whole 16-byte pieces", who);
+  if ((heads > 1 && x_head_stride < d) || (rows > 1 && x_stride < d))
+    return fail(MQA_ERR_INVALID_ARG, "%s: strides below the row width", who);
+  if (!x || !slots || !pool) return fail(MQA_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (dt == MQA_FP8_E4M3 ? (!scale_pool || sf_pool) : (scale_pool || !sf_pool))
+    return fail(MQA_ERR_INVALID_ARG, "%s: FP8 takes a scale pool, MX formats a block-scale pool", who);
+  if (!aligned(x, 16) || !aligned(pool, 16) || !aligned(values, 16) || !aligned(slots, 8) ||
+      !aligned(scale_pool, 4))
+    return fail(MQA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+  mqa::WriteParams p{};
+  p.x = x;
+  p.x_stride = x_stride;
+  p.x_head_stride = x_head_stride;
+  p.slots = slots;
+  p.pool = pool;
+  p.sf = sf_pool;
+  p.scale = scale_pool;
+  p.values = values;
+  p.num_slots = num_slots;
+  p.rows = rows;
+  p.heads = heads;
+  const int type = x_type == MQA_F32 ? mqa::kF32 : x_type == MQA_BF16 ? mqa::kBF16 : mqa::kF16;
+  return hip_status(mqa::launch_kv_write((int)dt, d, type, p, stream), who);
+}
+
+int64_t paged_attention_workspace_size(int32_t batch, int32_t next_n, int32_t hq, int32_t hkv,
+                                       int32_t d, int32_t max_context_len, int32_t topk) {
+  mqa_status st = check_attention_shape(batch, next_n, hq, hkv, d, max_context_len, topk,
+                                        "paged_attention_workspace_size");
+  if (st != MQA_OK) return -1;
+  const AttnPlan a = plan_attention(batch, next_n, hq, hkv, max_context_len, topk);
+  return a.chunks == 1 ? 0 : (int64_t)a.chunks * batch * next_n * hq * (d + 2) * 4;
+}
+
+mqa_status paged_attention(mqa_dtype dt, const void* q, mqa_float q_type, int64_t q_stride,
+                           const uint8_t* k_pool, const uint8_t* k_sf_pool, const uint8_t* v_pool,
+                           const uint8_t* v_sf_pool, const int32_t* context_lens,
+                           const int32_t* block_table, int64_t block_table_stride,
+                           const int32_t* indices, int64_t indices_stride, int32_t topk,
+                           float scale, void* out, float* lse, void* workspace,
+                           int64_t workspace_bytes, int32_t batch, int32_t next_n, int32_t hq,
+                           int32_t hkv, int32_t d, int32_t block_size, int32_t num_blocks,
+                           int32_t max_context_len, hipStream_t stream) {
+  const char* who = "paged_attention";
+  if (dt != MQA_MXFP4_E2M1)
+    return fail(dt == MQA_FP8_E4M3 || dt == MQA_MXFP8_E4M3 ? MQA_ERR_UNSUPPORTED : MQA_ERR_INVALID_ARG,
+                "%s: the cache must be MXFP4 (dtype %d)", who, (int)dt);
+  if (q_type != MQA_BF16 && q_type != MQA_F16)
+    return fail(q_type == MQA_F32 ? MQA_ERR_UNSUPPORTED : MQA_ERR_INVALID_ARG,
+                "%s: q must be bf16 or fp16 (type %d)", who, (int)q_type);
+  if ((indices != nullptr) != (topk != 0))
+    return fail(MQA_ERR_INVALID_ARG, "%s: pass indices with topk >= 1 or neither", who);
+  mqa_status st = check_attention_shape(batch, next_n, hq, hkv, d, max_context_len, topk, who);
+  if (st != MQA_OK) return st;
+  if (block_size != 16 && block_size != 32 && block_size != 64)
+    return fail(MQA_ERR_UNSUPPORTED, "%s: block_size=%d not in {16, 32, 64}", who, block_size);
+  if (num_blocks < 1) return fail(MQA_ERR_INVALID_ARG, "%s: num_blocks < 1", who);
+  if ((int64_t)num_blocks * block_size > 0x7fffffff)
+    return fail(MQA_ERR_UNSUPPORTED, "%s: pool of %d blocks too large", who, num_blocks);
+  if (!q || !k_pool || !k_sf_pool || !v_pool || !v_sf_pool || !context_lens ||
+      (max_context_len > 0 && !block_table) || !out)
+    return fail(MQA_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16) ||
+      !aligned(context_lens, 4) || !aligned(block_table, 4) || !aligned(indices, 4) ||
+      !aligned(lse, 4) || !aligned(workspace, 16))
+    return fail(MQA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+  if (q_stride < (int64_t)hq * d || q_stride % 8)
+    return fail(MQA_ERR_INVALID_ARG, "%s: q_stride must be a multiple of 8 and at least Hq * D", who);
+  if (block_table_stride < ((int64_t)max_context_len + block_size - 1) / block_size)
+    return fail(MQA_ERR_INVALID_ARG, "%s: block_table_stride < ceil(max_context_len / block_size)", who);
+  if (indices && indices_stride < topk)
+    return fail(MQA_ERR_INVALID_ARG, "%s: indices_stride < topk", who);
+  uint32_t scale_bits;   // by its bits: this file is built without NaN semantics
+  std::memcpy(&scale_bits, &scale, 4);
+  if ((scale_bits & 0x7f800000u) == 0x7f800000u)
+    return fail(MQA_ERR_INVALID_ARG, "%s: scale is not finite", who);
+  const AttnPlan a = plan_attention(batch, next_n, hq, hkv, max_context_len, topk);
+  const int64_t rows_heads = (int64_t)batch * next_n * hq;
+  const int64_t need = a.chunks == 1 ? 0 : (int64_t)a.chunks * rows_heads * (d + 2) * 4;
+  if (workspace_bytes < need || (need > 0 && !workspace))
+    return fail(MQA_ERR_INVALID_ARG, "%s: workspace of %lld bytes, %lld needed", who,
+                (long long)workspace_bytes, (long long)need);
+  const int64_t groups = ((int64_t)a.units * a.chunks + 7) / 8 * 8;
+  if (groups * a.row_groups * hkv > 0x7fffffff || (rows_heads + 3) / 4 > 0x7fffffff)
+    return fail(MQA_ERR_UNSUPPORTED, "%s: problem too large", who);
+  mqa::AttnParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_stride = q_stride;
+  p.k = k_pool;
+  p.k_sf = k_sf_pool;
+  p.v = v_pool;
+  p.v_sf = v_sf_pool;
+  p.ctx = context_lens;
+  p.bt = block_table;
+  p.bt_stride = block_table_stride;
+  p.indices = indices;
+  p.idx_stride = indices_stride;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + (int64_t)a.chunks * rows_heads * d);
+  p.rows_heads = rows_heads;
+  p.units = a.units;
+  p.kv_heads = hkv;
+  p.group = hq / hkv;
+  p.next_n = next_n;
+  p.num_blocks = num_blocks;
+  p.bs_shift = block_shift(block_size);
+  p.max_ctx = max_context_len;
+  p.topk = topk;
+  p.chunk = a.chunk;
+  p.chunks = a.chunks;
+  p.row_tiles = a.row_tiles;
+  p.row_groups = a.row_groups;
+  p.negate = scale < 0.f;
+  p.c2 = (scale < 0.f ? -scale : scale) * 1.4426950408889634f;
+  if (debug_enabled())
+    fprintf(stderr, "[mqa_logits] %s Hq=%d Hkv=%d D=%d batch=%d next_n=%d bs=%d topk=%d chunk=%d x %d rows=16*%d x %d\n",
+            who, hq, hkv, d, batch, next_n, block_size, topk, a.chunk, a.chunks, a.row_tiles, a.row_groups);
+  return hip_status(mqa::launch_attention(d, q_type == MQA_F16, p, stream), who);
 }
 
 }  // extern "C"

@@ -9,8 +9,8 @@ namespace mqa {
 // Output modes of the dense kernel.
 enum Store : int { kDenseClean = 0, kDenseKeep = 1, kCompressed = 2 };
 
-// Element type of the weights and of the logits (the C ABI's mqa_float).
-enum FloatType : int { kF32 = 0, kBF16 = 1 };
+// Element types (the C ABI's mqa_float; kF16 only for attention and cache writes).
+enum FloatType : int { kF32 = 0, kBF16 = 1, kF16 = 2 };
 
 // Waves per block of the paged kernel.  One: every value a wave needs to be
 // uniform (its schedule slot, its buffer resources) then comes from blockIdx
@@ -84,6 +84,62 @@ struct TopkParams {
   int64_t out_stride;
 };
 
+// Keys per workgroup of the attention kernel, at most (its slots live in LDS).
+constexpr int kAttnMaxChunk = 4096;
+
+struct AttnParams {
+  const uint16_t* q;         // [batch*next_n, Hq, D] bf16 or fp16 bits
+  int64_t q_stride;          // elements from one query token to the next
+  const uint8_t* k;          // [num_blocks, bs, Hkv, D/2] packed e2m1
+  const uint8_t* k_sf;       // [num_blocks, bs, Hkv, D/32] e8m0
+  const uint8_t* v;
+  const uint8_t* v_sf;
+  const int32_t* ctx;        // [batch]
+  const int32_t* bt;         // [batch, bt_stride]
+  int64_t bt_stride;
+  const int32_t* indices;    // [batch*next_n, idx_stride] or null (whole contexts)
+  int64_t idx_stride;
+  uint16_t* out;             // [batch*next_n, Hq, D], q's type
+  float* lse;                // [batch*next_n, Hq] or null
+  float* part_o;             // [chunks, batch*next_n, Hq, D]
+  float2* part_ml;           // [chunks, batch*next_n, Hq] maximum (log2), sum
+  int64_t rows_heads;        // batch*next_n * Hq
+  int32_t units;             // sequences, or query tokens with indices
+  int32_t kv_heads, group;   // Hkv, Hq / Hkv
+  int32_t next_n, num_blocks, bs_shift, max_ctx, topk;
+  int32_t chunk, chunks;     // keys per workgroup; workgroups along the keys
+  int32_t row_tiles, row_groups;   // 16-row tiles per workgroup; workgroups along the rows
+  int32_t negate;            // scale < 0: the queries' signs are flipped
+  float c2;                  // |scale| * log2(e)
+};
+
+struct WriteParams {
+  const void* x;             // rows of heads of D elements
+  int64_t x_stride, x_head_stride;   // elements
+  const int64_t* slots;      // [rows]
+  uint8_t* pool;             // [slots, heads, D] bytes (fp4: D/2)
+  uint8_t* sf;               // [slots, heads, D/32] or null
+  float* scale;              // [slots, heads] or null
+  void* values;              // [rows, heads, D] of x's type, or null
+  int64_t num_slots, rows;
+  int32_t heads;
+};
+
+struct SlotParams {
+  const int32_t* ctx;        // [batch]
+  const int32_t* new_lens;   // [batch]
+  const int32_t* free_ids;   // [num_free]
+  int32_t* bt;               // [batch, bt_stride]
+  int64_t bt_stride;
+  int64_t* slots;            // [max_tokens]
+  int32_t* offsets;          // [batch + 1]
+  int32_t* taken;            // [1]
+  int32_t batch, num_free, num_blocks, bs_shift, max_ctx, max_tokens;
+};
+
+hipError_t launch_attention(int d, int f16, const AttnParams& p, hipStream_t s);
+hipError_t launch_kv_write(int fmt, int d, int in_type, const WriteParams& p, hipStream_t s);
+hipError_t launch_kv_slots(const SlotParams& p, hipStream_t s);
 hipError_t launch_topk(int in_type, const TopkParams& p, hipStream_t s);
 hipError_t launch_dense(int fmt, int h, int d, int store, int out, const DenseParams& p,
                         hipStream_t s);

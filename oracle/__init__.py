@@ -24,12 +24,13 @@ Modules:
   reference  dense, compressed and paged logits plus the per-entry error bound.
   schedule   the paged and dense work splits the metadata entry points produce.
   topk       the top-k column indices of logits rows.
+  cache      slot maps, quantising writes and attention over the paged cache.
   brute      exact rational (fractions.Fraction) evaluation for tiny inputs.
 
 Every function is pinned by tests under ``tests/`` marked ``not gpu``.
 """
 
-from . import codecs, reference, schedule, brute, topk  # noqa: F401
+from . import codecs, reference, schedule, brute, topk, cache  # noqa: F401
 from .reference import (  # noqa: F401
     row_ranges,
     dense_logits,
