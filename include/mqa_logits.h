@@ -362,7 +362,8 @@ mqa_status paged_kv_write(mqa_dtype dt, const void* x, mqa_float x_type, int64_t
  * Keys outside a row's range never reach its result, whatever the cache holds
  * there.  Requires D in {64, 128}, Hkv <= 256, Hq a multiple of Hkv and at
  * most 1024, 1 <= batch <= 8192, 1 <= next_n <= 16, block_size in
- * {16, 32, 64}, num_blocks * block_size < 2^31, topk <= 2^20.
+ * {16, 32, 64}, num_blocks * block_size < 2^31, less than 2^32 blocks of 32
+ * elements in a pool (64 GiB of codes), topk <= 2^20.
  */
 int64_t paged_attention_workspace_size(int32_t batch, int32_t next_n, int32_t hq, int32_t hkv,
                                        int32_t d, int32_t max_context_len,

@@ -21,6 +21,7 @@ Entry points (same names as the C ABI):
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -144,7 +145,7 @@ class _Args:
         self.seen.append((name, t))
 
     def on_gpu(self):
-        # device indices compared as integers (-1 for a CPU tensor)
+        # device indices compared as integers (-1 for a CPU tensor); returns theirs
         first = self.seen[0][1].get_device()
         for name, t in self.seen:
             dev = t.get_device()
@@ -152,6 +153,7 @@ class _Args:
                 raise ValueError(f"{name} must be a GPU tensor (the library reads device memory)")
             if dev != first:
                 raise ValueError(f"{name} must be on cuda:{first}, got {t.device}")
+        return first
 
 
 def _codes(a, fmt, q, kv, q_sf, kv_sf, kv_scale, rows_shape, kv_shape):
@@ -407,17 +409,23 @@ def paged_mqa_logits(fmt, q, q_sf, kv_pool, kv_sf_pool, kv_scale_pool, weights,
     return out
 
 
-def _call(fn, t, *args):
-    """fn(*args, stream) on the device of t (kernels go to the current device)."""
-    if torch.cuda.current_device() == t.get_device():
-        _check(fn(*args, _stream(t)))
+# The calls below run once per layer and step, so their checks are made twice:
+# first one expression over everything a call takes; only where that fails, the
+# checks one by one, which name what does not fit.
+
+def _call(fn, device, *args):
+    """fn(*args, stream) on GPU `device` (kernels go to the current device)."""
+    if torch._C._cuda_getDevice() == device:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
-        with torch.cuda.device(t.device):
-            _check(fn(*args, _stream(t)))
+        with torch.cuda.device(device):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    if status != 0:
+        _check(status)
 
 
 def _data(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _row_stride(t, width):
@@ -430,14 +438,24 @@ def _block_size(block_size):
         raise ValueError(f"block_size must be one of {BLOCK_SIZES}, got {block_size}")
 
 
-def _table(a, block_table, batch, block_size, max_context_len):
-    """A block table whose rows reach max_context_len; returns its row stride."""
+def _fits(t, shape, dtype, device):
+    return (t.shape == shape and t.dtype is dtype and t.get_device() == device
+            and t.is_contiguous())
+
+
+def _table_fits(t, batch, blocks, device):
+    shape = t.shape
+    return (len(shape) == 2 and shape[0] == batch and shape[1] >= blocks
+            and t.dtype is torch.int32 and t.get_device() == device
+            and (t.stride(1) == 1 or shape[1] <= 1))
+
+
+def _want_table(a, block_table, batch, block_size, max_context_len):
     a.want(block_table, "block_table", (batch, None), I32_T, rows=True)
     need = -(-max_context_len // block_size)
     if block_table.shape[1] < need:
         raise ValueError(f"block_table rows must hold ceil(max_context_len / block_size) = {need} "
                          f"blocks, got {block_table.shape[1]}")
-    return _row_stride(block_table, block_table.shape[1])
 
 
 def paged_kv_slots(context_lens, new_lens, free_blocks, block_table, num_blocks, block_size,
@@ -452,26 +470,33 @@ def paged_kv_slots(context_lens, new_lens, free_blocks, block_table, num_blocks,
     _block_size(block_size)
     if max_tokens < 0 or max_context_len < 0:
         raise ValueError("max_tokens and max_context_len must not be negative")
-    a = _Args()
-    batch = context_lens.shape[0]
-    a.want(context_lens, "context_lens", (batch,), I32_T)
-    a.want(new_lens, "new_lens", (batch,), I32_T)
-    a.want(free_blocks, "free_blocks", (None,), I32_T)
-    stride = _table(a, block_table, batch, block_size, max_context_len)
+    batch, dev = context_lens.shape[0], context_lens.get_device()
     if out is None:
-        dev = context_lens.device
-        out = (torch.empty(max_tokens, dtype=torch.int64, device=dev),
-               torch.empty(batch + 1, dtype=torch.int32, device=dev),
-               torch.empty(1, dtype=torch.int32, device=dev))
+        out = (context_lens.new_empty(max_tokens, dtype=torch.int64),
+               context_lens.new_empty(batch + 1, dtype=torch.int32),
+               context_lens.new_empty(1, dtype=torch.int32))
     slots, offsets, taken = out
-    a.want(slots, "slots", (max_tokens,), I64_T)
-    a.want(offsets, "token_offsets", (batch + 1,), I32_T)
-    a.want(taken, "blocks_taken", (1,), I32_T)
-    a.on_gpu()
-    _call(lib.paged_kv_slots, context_lens, _data(context_lens), _data(new_lens),
-          _data(free_blocks), free_blocks.shape[0], _data(block_table), stride, _data(slots),
-          _data(offsets), _data(taken), batch, block_size, num_blocks, max_context_len, max_tokens)
-    return slots, offsets, taken
+    i32 = torch.int32
+    if not (dev >= 0 and _fits(context_lens, (batch,), i32, dev)
+            and _fits(new_lens, (batch,), i32, dev)
+            and _fits(free_blocks, (free_blocks.numel(),), i32, dev)
+            and _table_fits(block_table, batch, -(-max_context_len // block_size), dev)
+            and _fits(slots, (max_tokens,), torch.int64, dev)
+            and _fits(offsets, (batch + 1,), i32, dev) and _fits(taken, (1,), i32, dev)):
+        a = _Args()
+        a.want(context_lens, "context_lens", (batch,), I32_T)
+        a.want(new_lens, "new_lens", (batch,), I32_T)
+        a.want(free_blocks, "free_blocks", (None,), I32_T)
+        _want_table(a, block_table, batch, block_size, max_context_len)
+        a.want(slots, "slots", (max_tokens,), I64_T)
+        a.want(offsets, "token_offsets", (batch + 1,), I32_T)
+        a.want(taken, "blocks_taken", (1,), I32_T)
+        a.on_gpu()
+    _call(lib.paged_kv_slots, dev, context_lens.data_ptr(), new_lens.data_ptr(),
+          free_blocks.data_ptr(), free_blocks.shape[0], block_table.data_ptr(),
+          _row_stride(block_table, block_table.shape[1]), slots.data_ptr(), offsets.data_ptr(),
+          taken.data_ptr(), batch, block_size, num_blocks, max_context_len, max_tokens)
+    return out
 
 
 def paged_kv_write(fmt, x, slots, kv_pool, kv_sf_pool=None, kv_scale_pool=None, values=None):
@@ -481,35 +506,47 @@ def paged_kv_write(fmt, x, slots, kv_pool, kv_sf_pool=None, kv_scale_pool=None, 
     with kv_sf_pool [.., D/32] (MX formats) or kv_scale_pool (fp8).  Slots that
     are stored must differ.  values (x's shape and type, contiguous) receives
     what the codes stand for."""
-    _fmt(fmt)
-    a = _Args()
-    if x.dim() not in (2, 3) or x.dtype not in ROW_TYPES:
+    code = _fmt(fmt)
+    shape = x.shape
+    if len(shape) not in (2, 3) or x.dtype not in ROW_TYPES:
         raise ValueError(f"x must be [n, D] or [n, heads, D] of {sorted(map(str, ROW_TYPES))}, "
-                         f"got {tuple(x.shape)} {x.dtype}")
-    n, d = x.shape[0], x.shape[-1]
-    heads = x.shape[1] if x.dim() == 3 else 1
-    a.want(x, "x", tuple(x.shape), rows=True)
-    a.want(slots, "slots", (n,), I64_T)
-    lead = (None, None) + tuple(x.shape[1:-1])
-    a.want(kv_pool, "kv_pool", (*lead, d // 2 if fmt == "mxfp4" else d), itemsize=1)
-    lead = tuple(kv_pool.shape[:-1])
+                         f"got {tuple(shape)} {x.dtype}")
+    n, d, dev = shape[0], shape[-1], x.get_device()
+    heads = shape[1] if len(shape) == 3 else 1
+    lead = kv_pool.shape[:2] + shape[1:-1]
+    pool_shape = (*lead, d // 2 if fmt == "mxfp4" else d)
     if fmt == "fp8":
-        if kv_sf_pool is not None:
-            raise ValueError("fp8 takes no block scales (kv_sf_pool)")
-        a.want(kv_scale_pool, "kv_scale_pool", lead, (torch.float32,))
+        scales, scale_shape, scale_size = kv_scale_pool, lead, 4
     else:
-        if kv_scale_pool is not None:
-            raise ValueError(f"{fmt} takes no kv_scale_pool")
-        a.want(kv_sf_pool, "kv_sf_pool", (*lead, d // 32), itemsize=1)
-    if values is not None:
-        a.want(values, "values", tuple(x.shape), (x.dtype,))
-    a.on_gpu()
-    _call(lib.paged_kv_write, x, _fmt(fmt), _data(x), ROW_TYPES[x.dtype], _row_stride(x, d),
-          x.stride(1) if heads > 1 else d, _data(slots), _data(kv_pool), _data(kv_sf_pool),
-          _data(kv_scale_pool), _data(values), kv_pool.shape[0] * kv_pool.shape[1], n, heads, d)
+        scales, scale_shape, scale_size = kv_sf_pool, (*lead, d // 32), 1
+    if not (dev >= 0 and scales is not None and (kv_sf_pool is None or kv_scale_pool is None)
+            and x.stride(-1) == 1 and _fits(slots, (n,), torch.int64, dev)
+            and _fits(kv_pool, pool_shape, kv_pool.dtype, dev) and kv_pool.dtype.itemsize == 1
+            and _fits(scales, scale_shape, scales.dtype, dev)
+            and (scales.dtype.itemsize == 1 if scale_size == 1 else scales.dtype is torch.float32)
+            and (values is None or _fits(values, shape, x.dtype, dev))):
+        a = _Args()
+        a.want(x, "x", tuple(shape), rows=True)
+        a.want(slots, "slots", (n,), I64_T)
+        a.want(kv_pool, "kv_pool", (None, None, *pool_shape[2:]), itemsize=1)
+        if fmt == "fp8":
+            if kv_sf_pool is not None:
+                raise ValueError("fp8 takes no block scales (kv_sf_pool)")
+            a.want(kv_scale_pool, "kv_scale_pool", tuple(lead), (torch.float32,))
+        else:
+            if kv_scale_pool is not None:
+                raise ValueError(f"{fmt} takes no kv_scale_pool")
+            a.want(kv_sf_pool, "kv_sf_pool", tuple(scale_shape), itemsize=1)
+        if values is not None:
+            a.want(values, "values", tuple(shape), (x.dtype,))
+        a.on_gpu()
+    _call(lib.paged_kv_write, dev, code, x.data_ptr(), ROW_TYPES[x.dtype], _row_stride(x, d),
+          x.stride(1) if heads > 1 else d, slots.data_ptr(), kv_pool.data_ptr(), _data(kv_sf_pool),
+          _data(kv_scale_pool), _data(values), lead[0] * lead[1], n, heads, d)
     return values
 
 
+@functools.lru_cache(maxsize=None)
 def paged_attention_workspace_size(batch, next_n, q_heads, kv_heads, d, max_context_len, topk=0):
     """Bytes of workspace of a paged_attention call of these sizes."""
     n = lib.paged_attention_workspace_size(batch, next_n, q_heads, kv_heads, d, max_context_len,
@@ -536,52 +573,66 @@ def paged_attention(fmt, q, k_pool, k_sf_pool, v_pool, v_sf_pool, context_lens, 
     if fmt != "mxfp4":
         _fmt(fmt)
         raise ValueError(f"paged_attention reads an mxfp4 cache, got {fmt!r}")
-    a = _Args()
     if q.dim() != 3 or q.dtype not in QUERY_TYPES:
         raise ValueError(f"q must be [rows, Hq, D] of bfloat16 or float16, got {tuple(q.shape)} {q.dtype}")
     if k_pool.dim() != 4:
         raise ValueError(f"k_pool must be [num_blocks, block_size, Hkv, D/2], got {tuple(k_pool.shape)}")
-    rows, hq, d = q.shape
+    q_shape, q_stride, dev = q.shape, q.stride(), q.get_device()
+    rows, hq, d = q_shape
     batch = context_lens.shape[0]
-    num_blocks, block_size, hkv = k_pool.shape[:3]
+    num_blocks, block_size, hkv, _ = k_pool.shape
     _block_size(block_size)
     if max_context_len < 0:
         raise ValueError("max_context_len must not be negative")
     if rows != batch * next_n:
         raise ValueError(f"q must have batch * next_n = {batch * next_n} rows, got {rows}")
-    if q.stride(2) != 1 or (hq > 1 and q.stride(1) != d):
+    if q_stride[2] != 1 or (hq > 1 and q_stride[1] != d):
         raise ValueError("q rows must be contiguous")
-    a.want(q[:0], "q", (0, hq, d))
-    lead = (num_blocks, block_size, hkv)
-    for name, codes, sf in (("k", k_pool, k_sf_pool), ("v", v_pool, v_sf_pool)):
-        a.want(codes, name + "_pool", (*lead, d // 2), itemsize=1)
-        a.want(sf, name + "_sf_pool", (*lead, d // 32), itemsize=1)
-    a.want(context_lens, "context_lens", (batch,), I32_T)
-    stride = _table(a, block_table, batch, block_size, max_context_len)
     topk = 0
     if indices is not None:
-        a.want(indices, "indices", (rows, None), I32_T, rows=True)
-        topk = indices.shape[1]
+        topk = indices.shape[1] if indices.dim() == 2 else 0
         if topk < 1:
-            raise ValueError("indices must have at least one column")
+            raise ValueError("indices must be [rows, topk] with at least one column")
     if out is None:
-        out = torch.empty((rows, hq, d), dtype=q.dtype, device=q.device)
-    a.want(out, "out", (rows, hq, d), (q.dtype,))
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if lse is None and return_lse:
-        lse = torch.empty((rows, hq), dtype=torch.float32, device=q.device)
-    if lse is not None:
-        a.want(lse, "lse", (rows, hq), (torch.float32,))
+        lse = q.new_empty((rows, hq), dtype=torch.float32)
     need = paged_attention_workspace_size(batch, next_n, hq, hkv, d, max_context_len, topk)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    if workspace is not None:
-        a.want(workspace, "workspace", (None,), itemsize=1)
-    a.on_gpu()
-    _call(lib.paged_attention, q, _fmt(fmt), _data(q), QUERY_TYPES[q.dtype],
-          _row_stride(q, hq * d), _data(k_pool), _data(k_sf_pool), _data(v_pool), _data(v_sf_pool),
-          _data(context_lens), _data(block_table), stride, _data(indices),
-          0 if indices is None else _row_stride(indices, topk), topk,
-          d ** -0.5 if scale is None else float(scale), _data(out), _data(lse), _data(workspace),
-          0 if workspace is None else workspace.numel(), batch, next_n, hq, hkv, d, block_size,
-          num_blocks, max_context_len)
+        workspace = q.new_empty(need, dtype=torch.uint8)
+    codes, scales = (num_blocks, block_size, hkv, d // 2), (num_blocks, block_size, hkv, d // 32)
+    byte, i32 = k_pool.dtype, torch.int32
+    if not (dev >= 0 and byte.itemsize == 1 and _fits(k_pool, codes, byte, dev)
+            and _fits(v_pool, codes, byte, dev)
+            and k_sf_pool.dtype.itemsize == 1 and _fits(k_sf_pool, scales, k_sf_pool.dtype, dev)
+            and _fits(v_sf_pool, scales, k_sf_pool.dtype, dev)
+            and _fits(context_lens, (batch,), i32, dev)
+            and _table_fits(block_table, batch, -(-max_context_len // block_size), dev)
+            and (topk == 0 or _table_fits(indices, rows, topk, dev))
+            and _fits(out, q_shape, q.dtype, dev)
+            and (lse is None or _fits(lse, (rows, hq), torch.float32, dev))
+            and (workspace is None or _fits(workspace, (workspace.numel(),), torch.uint8, dev))):
+        a = _Args()
+        a.want(q[:0], "q", (0, hq, d))
+        for name, pool, sf in (("k", k_pool, k_sf_pool), ("v", v_pool, v_sf_pool)):
+            a.want(pool, name + "_pool", codes, itemsize=1)
+            a.want(sf, name + "_sf_pool", scales, itemsize=1)
+        a.want(context_lens, "context_lens", (batch,), I32_T)
+        _want_table(a, block_table, batch, block_size, max_context_len)
+        if topk:
+            a.want(indices, "indices", (rows, topk), I32_T, rows=True)
+        a.want(out, "out", (rows, hq, d), (q.dtype,))
+        if lse is not None:
+            a.want(lse, "lse", (rows, hq), (torch.float32,))
+        if workspace is not None:
+            a.want(workspace, "workspace", (None,), itemsize=1)
+        a.on_gpu()
+    _call(lib.paged_attention, dev, 2, q.data_ptr(), QUERY_TYPES[q.dtype],
+          q_stride[0] if rows > 1 else hq * d, k_pool.data_ptr(), k_sf_pool.data_ptr(),
+          v_pool.data_ptr(), v_sf_pool.data_ptr(), context_lens.data_ptr(), block_table.data_ptr(),
+          _row_stride(block_table, block_table.shape[1]), _data(indices),
+          _row_stride(indices, topk) if topk else 0, topk,
+          d ** -0.5 if scale is None else float(scale), out.data_ptr(), _data(lse),
+          _data(workspace), workspace.numel() if workspace is not None else 0, batch, next_n, hq,
+          hkv, d, block_size, num_blocks, max_context_len)
     return out if lse is None else (out, lse)

@@ -10,6 +10,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <string>
+#include <algorithm>
 
 #include "launch.hpp"
 
@@ -43,10 +44,6 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 // buffer resources with 32-bit offsets; every such range must stay below this
 // many bytes (the kernels' out-of-range marker sits just above it).
 constexpr int64_t kMaxRangeBytes = 0x7ff00000;
-
-// Workgroups that paged_attention aims for, and the fewest keys of one.
-constexpr int64_t kAttnTarget = 2048;
-constexpr int64_t kAttnMinChunk = 256;
 
 bool debug_enabled() {
   static const bool on = [] {
@@ -166,29 +163,29 @@ mqa_status run_dense(mqa_dtype dt, const void* q, const uint8_t* q_sf, const voi
 
 // How paged_attention splits its work.  A unit is a sequence, or a query token
 // when it has indices of its own; its next_n * group (or group) rows of a KV
-// head go to workgroups of 16 * row_tiles rows, its keys to workgroups of
-// `chunk` keys.
+// head go to workgroups of 16 * row_tiles rows, the keys of all units to
+// `workers` workgroups of each (attention.hip, "Work split").
 struct AttnPlan {
-  int32_t units, row_tiles, row_groups, chunk, chunks;
+  int32_t units, row_tiles, row_groups, workers, min_steps;
+  int64_t steps;             // 128-key steps of a KV head, at most
+  int64_t parts, bytes;      // part rows; workspace
 };
 
-AttnPlan plan_attention(int32_t batch, int32_t next_n, int32_t hq, int32_t hkv,
+AttnPlan plan_attention(int32_t batch, int32_t next_n, int32_t hq, int32_t hkv, int32_t d,
                         int32_t max_context_len, int32_t topk) {
   AttnPlan a{};
   const int32_t group = hq / hkv;
   a.units = topk ? batch * next_n : batch;
   const int32_t tiles = ((topk ? group : next_n * group) + 15) / 16;
-  a.row_tiles = tiles == 1 ? 1 : tiles == 2 ? 2 : 4;
+  a.row_tiles = tiles == 1 ? 1 : 2;
   a.row_groups = (tiles + a.row_tiles - 1) / a.row_tiles;
-  const int64_t length = topk ? topk : max_context_len;
-  const int64_t base = (int64_t)a.units * hkv * a.row_groups;
-  const int64_t want = (kAttnTarget + base - 1) / base;
-  int64_t chunk = (length + want - 1) / want;
-  chunk = (chunk + 127) / 128 * 128;
-  if (chunk < kAttnMinChunk) chunk = kAttnMinChunk;
-  if (chunk > mqa::kAttnMaxChunk) chunk = mqa::kAttnMaxChunk;
-  a.chunk = (int32_t)chunk;
-  a.chunks = length > chunk ? (int32_t)((length + chunk - 1) / chunk) : 1;
+  const int64_t members = (int64_t)hkv * a.row_groups;
+  a.steps = a.units * std::max<int64_t>(((topk ? topk : max_context_len) + 127) / 128, 1);
+  a.min_steps = 4;
+  const int64_t want = std::max<int64_t>(mqa::kAttnResident / members, 1);
+  a.workers = (int32_t)std::min(want, std::max<int64_t>(a.steps / a.min_steps, 1));
+  a.parts = a.workers == 1 ? 0 : members * a.workers * 2 * 16 * a.row_tiles;
+  a.bytes = a.workers == 1 ? 0 : a.parts * (d + 2) * 4 + (int64_t)a.units * 8;
   return a;
 }
 
@@ -204,6 +201,8 @@ mqa_status check_attention_shape(int32_t batch, int32_t next_n, int32_t hq, int3
   if (max_context_len < 0) return fail(MQA_ERR_INVALID_ARG, "%s: negative max_context_len", who);
   if (max_context_len > (1 << 30)) return fail(MQA_ERR_UNSUPPORTED, "%s: max_context_len=%d too large", who, max_context_len);
   if (topk < 0 || topk > (1 << 20)) return fail(MQA_ERR_INVALID_ARG, "%s: topk=%d not in [0, 2^20]", who, topk);
+  if ((int64_t)batch * (topk ? next_n : 1) * (((topk ? topk : max_context_len) + 127) / 128 + 1) > 0x7fffffff)
+    return fail(MQA_ERR_UNSUPPORTED, "%s: batch * max_context_len (or rows * topk) too large", who);
   return MQA_OK;
 }
 
@@ -532,8 +531,7 @@ int64_t paged_attention_workspace_size(int32_t batch, int32_t next_n, int32_t hq
   mqa_status st = check_attention_shape(batch, next_n, hq, hkv, d, max_context_len, topk,
                                         "paged_attention_workspace_size");
   if (st != MQA_OK) return -1;
-  const AttnPlan a = plan_attention(batch, next_n, hq, hkv, max_context_len, topk);
-  return a.chunks == 1 ? 0 : (int64_t)a.chunks * batch * next_n * hq * (d + 2) * 4;
+  return plan_attention(batch, next_n, hq, hkv, d, max_context_len, topk).bytes;
 }
 
 mqa_status paged_attention(mqa_dtype dt, const void* q, mqa_float q_type, int64_t q_stride,
@@ -559,12 +557,14 @@ mqa_status paged_attention(mqa_dtype dt, const void* q, mqa_float q_type, int64_
   if (block_size != 16 && block_size != 32 && block_size != 64)
     return fail(MQA_ERR_UNSUPPORTED, "%s: block_size=%d not in {16, 32, 64}", who, block_size);
   if (num_blocks < 1) return fail(MQA_ERR_INVALID_ARG, "%s: num_blocks < 1", who);
-  if ((int64_t)num_blocks * block_size > 0x7fffffff)
+  if ((int64_t)num_blocks * block_size > 0x7fffffff ||
+      (int64_t)num_blocks * block_size * hkv > 0xffffffffll / (d / 32) - 1)
     return fail(MQA_ERR_UNSUPPORTED, "%s: pool of %d blocks too large", who, num_blocks);
   if (!q || !k_pool || !k_sf_pool || !v_pool || !v_sf_pool || !context_lens ||
       (max_context_len > 0 && !block_table) || !out)
     return fail(MQA_ERR_INVALID_ARG, "%s: null pointer", who);
   if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16) ||
+      !aligned(k_sf_pool, 4) || !aligned(v_sf_pool, 4) ||
       !aligned(context_lens, 4) || !aligned(block_table, 4) || !aligned(indices, 4) ||
       !aligned(lse, 4) || !aligned(workspace, 16))
     return fail(MQA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
@@ -578,15 +578,11 @@ mqa_status paged_attention(mqa_dtype dt, const void* q, mqa_float q_type, int64_
   std::memcpy(&scale_bits, &scale, 4);
   if ((scale_bits & 0x7f800000u) == 0x7f800000u)
     return fail(MQA_ERR_INVALID_ARG, "%s: scale is not finite", who);
-  const AttnPlan a = plan_attention(batch, next_n, hq, hkv, max_context_len, topk);
+  const AttnPlan a = plan_attention(batch, next_n, hq, hkv, d, max_context_len, topk);
   const int64_t rows_heads = (int64_t)batch * next_n * hq;
-  const int64_t need = a.chunks == 1 ? 0 : (int64_t)a.chunks * rows_heads * (d + 2) * 4;
-  if (workspace_bytes < need || (need > 0 && !workspace))
+  if (workspace_bytes < a.bytes || (a.bytes > 0 && !workspace))
     return fail(MQA_ERR_INVALID_ARG, "%s: workspace of %lld bytes, %lld needed", who,
-                (long long)workspace_bytes, (long long)need);
-  const int64_t groups = ((int64_t)a.units * a.chunks + 7) / 8 * 8;
-  if (groups * a.row_groups * hkv > 0x7fffffff || (rows_heads + 3) / 4 > 0x7fffffff)
-    return fail(MQA_ERR_UNSUPPORTED, "%s: problem too large", who);
+                (long long)workspace_bytes, (long long)a.bytes);
   mqa::AttnParams p{};
   p.q = static_cast<const uint16_t*>(q);
   p.q_stride = q_stride;
@@ -602,7 +598,8 @@ mqa_status paged_attention(mqa_dtype dt, const void* q, mqa_float q_type, int64_
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
   p.part_o = static_cast<float*>(workspace);
-  p.part_ml = reinterpret_cast<float2*>(p.part_o + (int64_t)a.chunks * rows_heads * d);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + a.parts * d);
+  p.notes = reinterpret_cast<int2*>(p.part_ml + a.parts);
   p.rows_heads = rows_heads;
   p.units = a.units;
   p.kv_heads = hkv;
@@ -612,15 +609,16 @@ mqa_status paged_attention(mqa_dtype dt, const void* q, mqa_float q_type, int64_
   p.bs_shift = block_shift(block_size);
   p.max_ctx = max_context_len;
   p.topk = topk;
-  p.chunk = a.chunk;
-  p.chunks = a.chunks;
+  p.workers = a.workers;
+  p.min_steps = a.min_steps;
   p.row_tiles = a.row_tiles;
   p.row_groups = a.row_groups;
   p.negate = scale < 0.f;
-  p.c2 = (scale < 0.f ? -scale : scale) * 1.4426950408889634f;
+  // scale 0: the least positive factor keeps a masked score (-inf) out of NaN
+  p.c2 = std::max((scale < 0.f ? -scale : scale) * 1.4426950408889634f, 0x1p-126f);
   if (debug_enabled())
-    fprintf(stderr, "[mqa_logits] %s Hq=%d Hkv=%d D=%d batch=%d next_n=%d bs=%d topk=%d chunk=%d x %d rows=16*%d x %d\n",
-            who, hq, hkv, d, batch, next_n, block_size, topk, a.chunk, a.chunks, a.row_tiles, a.row_groups);
+    fprintf(stderr, "[mqa_logits] %s Hq=%d Hkv=%d D=%d batch=%d next_n=%d bs=%d topk=%d workers=%d rows=16*%d x %d\n",
+            who, hq, hkv, d, batch, next_n, block_size, topk, a.workers, a.row_tiles, a.row_groups);
   return hip_status(mqa::launch_attention(d, q_type == MQA_F16, p, stream), who);
 }
 

@@ -84,8 +84,13 @@ struct TopkParams {
   int64_t out_stride;
 };
 
-// Keys per workgroup of the attention kernel, at most (its slots live in LDS).
-constexpr int kAttnMaxChunk = 4096;
+// Keys whose places in the cache an attention workgroup holds in LDS at a time
+// (whole contexts: one place per 16 keys).
+constexpr int kAttnStage = 16384;
+constexpr int kAttnStageSparse = 2048;
+// Attention workgroups the chip holds at a time: two per compute unit (by
+// registers, and by LDS with two row tiles).
+constexpr int kAttnResident = 512;
 
 struct AttnParams {
   const uint16_t* q;         // [batch*next_n, Hq, D] bf16 or fp16 bits
@@ -101,13 +106,14 @@ struct AttnParams {
   int64_t idx_stride;
   uint16_t* out;             // [batch*next_n, Hq, D], q's type
   float* lse;                // [batch*next_n, Hq] or null
-  float* part_o;             // [chunks, batch*next_n, Hq, D]
-  float2* part_ml;           // [chunks, batch*next_n, Hq] maximum (log2), sum
+  float* part_o;             // [members, workers, 2, 16 * row_tiles, D]
+  float2* part_ml;           // [members, workers, 2, 16 * row_tiles] maximum (log2), sum
+  int2* notes;               // [units] first slot and number of a unit's parts
   int64_t rows_heads;        // batch*next_n * Hq
   int32_t units;             // sequences, or query tokens with indices
   int32_t kv_heads, group;   // Hkv, Hq / Hkv
   int32_t next_n, num_blocks, bs_shift, max_ctx, topk;
-  int32_t chunk, chunks;     // keys per workgroup; workgroups along the keys
+  int32_t workers, min_steps;      // workgroups along the keys; fewest 128-key steps of one
   int32_t row_tiles, row_groups;   // 16-row tiles per workgroup; workgroups along the rows
   int32_t negate;            // scale < 0: the queries' signs are flipped
   float c2;                  // |scale| * log2(e)
