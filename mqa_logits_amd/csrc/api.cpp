@@ -163,10 +163,11 @@ mqa_status run_dense(mqa_dtype dt, const void* q, const uint8_t* q_sf, const voi
 
 // How paged_attention splits its work.  A unit is a sequence, or a query token
 // when it has indices of its own; its next_n * group (or group) rows of a KV
-// head go to workgroups of 16 * row_tiles rows, the keys of all units to
+// head go to workgroups of member_rows rows, the keys of all units to
 // `workers` workgroups of each (attention.hip, "Work split").
 struct AttnPlan {
-  int32_t units, row_tiles, row_groups, workers, min_steps;
+  int32_t units, member_heads, member_rows, row_groups, workers, min_steps;
+  bool join;                 // some unit may be cut
   int64_t steps;             // 128-key steps of a KV head, at most
   int64_t parts, bytes;      // part rows; workspace
 };
@@ -176,16 +177,33 @@ AttnPlan plan_attention(int32_t batch, int32_t next_n, int32_t hq, int32_t hkv, 
   AttnPlan a{};
   const int32_t group = hq / hkv;
   a.units = topk ? batch * next_n : batch;
-  const int32_t tiles = ((topk ? group : next_n * group) + 15) / 16;
-  a.row_tiles = tiles == 1 ? 1 : 2;
-  a.row_groups = (tiles + a.row_tiles - 1) / a.row_tiles;
-  const int64_t members = (int64_t)hkv * a.row_groups;
+  const int32_t rows = topk ? group : next_n * group;
   a.steps = a.units * std::max<int64_t>(((topk ? topk : max_context_len) + 127) / 128, 1);
-  a.min_steps = 4;
-  const int64_t want = std::max<int64_t>(mqa::kAttnResident / members, 1);
-  a.workers = (int32_t)std::min(want, std::max<int64_t>(a.steps / a.min_steps, 1));
-  a.parts = a.workers == 1 ? 0 : members * a.workers * 2 * 16 * a.row_tiles;
-  a.bytes = a.workers == 1 ? 0 : a.parts * (d + 2) * 4 + (int64_t)a.units * 8;
+  static const int min_steps = std::getenv("AMS") ? atoi(std::getenv("AMS")) : 4, wide_steps = std::getenv("AWS") ? atoi(std::getenv("AWS")) : 12;
+  a.min_steps = min_steps;
+  int64_t members = 0;
+  const auto split = [&](int32_t member_rows, int32_t member_heads) {
+    a.member_rows = member_rows;
+    a.member_heads = member_heads;
+    a.row_groups = (rows * member_heads + member_rows - 1) / member_rows;
+    members = (int64_t)(hkv / member_heads) * a.row_groups;
+    const int64_t want = std::max<int64_t>(mqa::kAttnResident / members, 1);
+    a.workers = (int32_t)std::min(want, std::max<int64_t>(a.steps / a.min_steps, 1));
+  };
+  static const int hd = std::getenv("AHD") ? atoi(std::getenv("AHD")) : 6;
+  if (rows > 64) split(128, 1);
+  if (rows <= 64 || a.steps < (int64_t)wide_steps * a.workers) {
+    if (rows <= 16 && hkv % 4 == 0) split(64, 4);
+    if (rows > 16 || hkv % 4 || a.steps < (int64_t)hd * a.workers) split(rows <= 16 ? 16 : 32, 1);
+  }
+  // units of one size and whole ones a worker: none is cut
+  if (topk && a.workers < a.units && a.workers > 1) {
+    const int32_t each = (a.units + a.workers - 1) / a.workers;
+    if (a.units % each == 0) a.workers = a.units / each;
+  }
+  a.join = a.workers > 1 && !(topk && a.units % a.workers == 0);
+  a.parts = a.join ? members * a.workers * 2 * a.member_rows : 0;
+  a.bytes = a.join ? a.parts * (d + 2) * 4 + (int64_t)a.units * 8 : 0;
   return a;
 }
 
@@ -564,7 +582,7 @@ mqa_status paged_attention(mqa_dtype dt, const void* q, mqa_float q_type, int64_
       (max_context_len > 0 && !block_table) || !out)
     return fail(MQA_ERR_INVALID_ARG, "%s: null pointer", who);
   if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16) ||
-      !aligned(k_sf_pool, 4) || !aligned(v_sf_pool, 4) ||
+      !aligned(k_sf_pool, 16) || !aligned(v_sf_pool, 16) ||
       !aligned(context_lens, 4) || !aligned(block_table, 4) || !aligned(indices, 4) ||
       !aligned(lse, 4) || !aligned(workspace, 16))
     return fail(MQA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
@@ -611,14 +629,16 @@ mqa_status paged_attention(mqa_dtype dt, const void* q, mqa_float q_type, int64_
   p.topk = topk;
   p.workers = a.workers;
   p.min_steps = a.min_steps;
-  p.row_tiles = a.row_tiles;
+  p.join = a.join;
+  p.member_heads = a.member_heads;
+  p.member_rows = a.member_rows;
   p.row_groups = a.row_groups;
   p.negate = scale < 0.f;
   // scale 0: the least positive factor keeps a masked score (-inf) out of NaN
   p.c2 = std::max((scale < 0.f ? -scale : scale) * 1.4426950408889634f, 0x1p-126f);
   if (debug_enabled())
-    fprintf(stderr, "[mqa_logits] %s Hq=%d Hkv=%d D=%d batch=%d next_n=%d bs=%d topk=%d workers=%d rows=16*%d x %d\n",
-            who, hq, hkv, d, batch, next_n, block_size, topk, a.workers, a.row_tiles, a.row_groups);
+    fprintf(stderr, "[mqa_logits] %s Hq=%d Hkv=%d D=%d batch=%d next_n=%d bs=%d topk=%d workers=%d rows=%d x %d\n",
+            who, hq, hkv, d, batch, next_n, block_size, topk, a.workers, a.member_rows, a.row_groups);
   return hip_status(mqa::launch_attention(d, q_type == MQA_F16, p, stream), who);
 }
 

@@ -132,8 +132,8 @@ struct Raw {
 
 // A 32-element block of the cache is 16 bytes of codes and one scale byte, so
 // one number, the block's index, gives both addresses.  LDS holds the index of
-// the first block (of this KV head) of every key (SPARSE; kNoKey for one to
-// pass over) or of every 16th key.
+// the first block (of KV head 0) of every key (SPARSE; kNoKey for one to pass
+// over) or of every 16th key.
 constexpr uint32_t kNoKey = 0xffffffffu;
 
 template <int D, bool SPARSE>
@@ -143,8 +143,9 @@ struct Tiles {
   uint32_t key_blocks;                       // blocks from one key of the pool to the next
   uint32_t code;                             // the lane's byte offset from its key's first code
 
-  __device__ __forceinline__ Tiles(const AttnParams& p, const uint32_t* at)
-      : k((Bytes)p.k), v((Bytes)p.v), ks((Bytes)p.k_sf), vs((Bytes)p.v_sf), lds(at),
+  __device__ __forceinline__ Tiles(const AttnParams& p, const uint32_t* at, int kv_head)
+      : k((Bytes)p.k + kv_head * (D / 2)), v((Bytes)p.v + kv_head * (D / 2)),
+        ks((Bytes)p.k_sf + kv_head * (D / 32)), vs((Bytes)p.v_sf + kv_head * (D / 32)), lds(at),
         key_blocks(p.kv_heads * (D / 32)) {
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     code = (SPARSE ? 0 : c * key_blocks) * 16 + g * (D / 8);
@@ -156,6 +157,7 @@ struct Tiles {
     return LANES ? p : scalar(p);
   }
 
+  template <bool SCALES = true>
   __device__ __forceinline__ void load(Raw& r, int tile) const {
     const int lane = threadIdx.x & 63, c = lane & 15;
 #pragma unroll
@@ -171,6 +173,7 @@ struct Tiles {
         r.v[half] = u32x4{y[0], y[1], 0u, 0u};
       }
     }
+    if constexpr (!SCALES) return;
     uint32_t first;                          // of key l % 32
     if constexpr (SPARSE) {
       first = key_block(tile * kTile + (lane & 31));
@@ -180,6 +183,12 @@ struct Tiles {
     }
     const Bytes sp = (lane & 32 ? vs : ks) + first;
     r.s = D == 128 ? load_from<uint32_t>(sp) : load_from<uint16_t>(sp);
+  }
+
+  // First block of any one key of the stage.
+  __device__ __forceinline__ uint32_t key_first(int key) const {
+    if constexpr (SPARSE) return key_block(key);
+    return lds[key >> 4] + (key & 15) * key_blocks;
   }
 
   // First block of a key of the stage (SPARSE; any block for one to pass over)
@@ -195,22 +204,23 @@ struct Tiles {
 };
 
 // Rows' state of one wave: queries, running maximum and sum, accumulators.
-template <int D, int RT, bool F16>
+template <int D, int RT, bool F16, bool QUERIES_IN_LDS>
 struct Rows {
   static constexpr int kSteps = D / 32;      // products along D
   static constexpr int kCols = D / 16;       // 16-element column groups of V
   static constexpr int kParts = F16 ? 2 : 1;
-  // staging: 64 scale words, then V's rows of D/2 bytes; the pitch keeps both
-  // the 16-byte writes and the 4-byte reads free of bank conflicts
+  // the pitch of V's rows keeps both the 16-byte writes and the 4-byte reads
+  // free of bank conflicts
   static constexpr int kPitch = D == 128 ? 80 : 40;
   static constexpr int kStageBytes = 256 + kTile * kPitch;
   struct Scores { f32x4 s[RT][2]; };         // [half]: keys 4g .. 4g+3 of row l % 16
   // Queries in LDS, shared by the waves, where registers are short.
-  static constexpr bool kQueriesInLds = RT == 2;
+  static constexpr bool kQueriesInLds = QUERIES_IN_LDS;
   static constexpr int kQueryWords = RT * kParts * kSteps * 64;
   u32x4 q[kQueriesInLds ? 1 : RT][kParts][kSteps];
   u32x4* q_lds;                              // [RT][kParts][kSteps][64 lanes]
-  char* lds;                                 // the wave's staging of a tile (kStageBytes)
+  uint32_t* words;                           // the wave's staging of a tile: 64 scale words,
+  char* values;                              // and V's rows of D/2 bytes
   f32x4 o[RT][kCols];
   float m[RT], l[RT];
   int seen[RT];                              // keys the lane's row sees
@@ -238,10 +248,10 @@ struct Rows {
   // Scale words and V go through LDS to the lanes that need them.
   __device__ __forceinline__ void stage(const Raw& r) const {
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-    reinterpret_cast<uint32_t*>(lds)[lane] = r.s;
+    words[lane] = r.s;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      char* row = lds + 256 + (half * 16 + c) * kPitch + g * (D / 8);
+      char* row = values + (half * 16 + c) * kPitch + g * (D / 8);
       if constexpr (D == 128)
         *reinterpret_cast<u32x4*>(row) = r.v[half];
       else
@@ -259,7 +269,7 @@ struct Rows {
     float ks[2];
 #pragma unroll
     for (int half = 0; half < 2; ++half)
-      ks[half] = byte_scale(reinterpret_cast<const uint32_t*>(lds)[half * 16 + c], g * (D / 4) / 32);
+      ks[half] = byte_scale(words[half * 16 + c], g * (D / 4) / 32);
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) {
       const u32x4 a = cvt_eight(r.k[0][st], ks[0]), b = cvt_eight(r.k[1][st], ks[1]);
@@ -286,27 +296,37 @@ struct Rows {
       const bool any = SPARSE ? places[lane & 31] != kNoKey : first + (lane & 31) < most;
       r.s = any ? r.s : 0u;
     }
-    // some byte of s over 252: some byte of ~s under 3
-    if (__builtin_expect(__any(((~r.s - 0x03030303u) & r.s & 0x80808080u) != 0), 0))
+    if (__builtin_expect(__any(has_nan(r.s)), 0))
       spread_nan<MASKED && !SPARSE>(r.s, first);
   }
 
   template <bool BY_ROW>
   __device__ __forceinline__ void spread_nan(uint32_t& s, int first) {
-    const int lane = threadIdx.x & 63, g = lane >> 4;
-    const int shift = 8 * (g * (D / 4) / 32);            // the block of the lane's results
 #pragma nounroll
-    for (int key = 0; key < kTile; ++key) {
-      const uint32_t b = (__shfl(s, 32 + key) >> shift) & 0xffu;
+    for (int key = 0; key < kTile; ++key) mark_nan<BY_ROW>(__shfl(s, 32 + key), first + key);
+    s = without_nan(s);
+  }
+
+  // A key's V scales mark the rows that see it, by the block of the lane's results.
+  template <bool BY_ROW>
+  __device__ __forceinline__ void mark_nan(uint32_t word, int key) {
+    const uint32_t b = (word >> (8 * ((threadIdx.x & 63) / 16 * (D / 4) / 32))) & 0xffu;
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-        if (b > kLastScale && (!BY_ROW || first + key < seen[rt])) nan_rows |= 1u << rt;
-    }
+    for (int rt = 0; rt < RT; ++rt)
+      if (b > kLastScale && (!BY_ROW || key < seen[rt])) nan_rows |= 1u << rt;
+  }
+
+  __device__ __forceinline__ static bool has_nan(uint32_t s) {
+    // some byte of s over 252: some byte of ~s under 3
+    return ((~s - 0x03030303u) & s & 0x80808080u) != 0;
+  }
+  __device__ __forceinline__ static uint32_t without_nan(uint32_t s) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t byte = 0xffu << (8 * i), b = (s >> (8 * i)) & 0xffu;
-      if (b > kLastScale) s = lane & 32 ? s & ~byte : s | byte;
+      if (b > kLastScale) s = threadIdx.x & 32 ? s & ~byte : s | byte;
     }
+    return s;
   }
 
   // Keys that a row does not see leave its scores.
@@ -376,22 +396,42 @@ struct Rows {
     }
   }
 
-  // The weighted sum of a tile's V.
-  __device__ __forceinline__ void accumulate(const Scores& x, float c2) {
+  // From the staging: D/16 elements of keys 4g .. 4g+3 of both halves, and
+  // their scales.
+  __device__ __forceinline__ void read_values(uint32_t (&v)[8], float (&vs)[8]) const {
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-    uint32_t v[8];                           // D/16 elements of keys 4g .. 4g+3 of both halves
-    float vs[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const char* row = lds + 256 + ((i >> 2) * 16 + 4 * g + (i & 3)) * kPitch + c * (D / 32);
+      const char* row = values + ((i >> 2) * 16 + 4 * g + (i & 3)) * kPitch + c * (D / 32);
       v[i] = D == 128 ? *reinterpret_cast<const uint32_t*>(row) : *reinterpret_cast<const uint16_t*>(row);
     }
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(lds + (32 + half * 16 + 4 * g) * 4);
+      const u32x4 w = *reinterpret_cast<const u32x4*>(words + 32 + half * 16 + 4 * g);
 #pragma unroll
       for (int i = 0; i < 4; ++i) vs[4 * half + i] = byte_scale(w[i], c * (D / 16) / 32);
     }
+  }
+
+  // Operands of elements 2 SEL and 2 SEL + 1 of the lane's D/16.
+  template <int SEL>
+  __device__ __forceinline__ static void value_operands(const uint32_t (&v)[8], const float (&vs)[8],
+                                                        u32x4& even, u32x4& odd) {
+    uint32_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = cvt_pair<SEL>(v[i], vs[i]);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      even[w] = __builtin_amdgcn_perm(e[2 * w + 1], e[2 * w], 0x05040100);
+      odd[w] = __builtin_amdgcn_perm(e[2 * w + 1], e[2 * w], 0x07060302);
+    }
+  }
+
+  // The weighted sum of a tile's V.
+  __device__ __forceinline__ void accumulate(const Scores& x, float c2) {
+    uint32_t v[8];
+    float vs[8];
+    read_values(v, vs);
     u32x4 p[RT][kParts];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) weights(x.s[rt], rt, c2, p[rt]);
@@ -408,19 +448,11 @@ struct Rows {
     }
   }
 
-  // Elements 2 SEL and 2 SEL + 1 of the lane's D/16.
   template <int SEL>
   __device__ __forceinline__ void add_values(const uint32_t (&v)[8], const float (&vs)[8],
                                              const u32x4 (&p)[RT][kParts]) {
-    uint32_t e[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = cvt_pair<SEL>(v[i], vs[i]);
     u32x4 even, odd;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      even[w] = __builtin_amdgcn_perm(e[2 * w + 1], e[2 * w], 0x05040100);
-      odd[w] = __builtin_amdgcn_perm(e[2 * w + 1], e[2 * w], 0x07060302);
-    }
+    value_operands<SEL>(v, vs, even, odd);
 #pragma unroll
     for (int part = 0; part < kParts; ++part)
 #pragma unroll
@@ -429,6 +461,109 @@ struct Rows {
         o[rt][2 * SEL + 1] = mma(odd, p[rt][part], o[rt][2 * SEL + 1]);
       }
   }
+
+  // ---- operands in LDS, shared by the workgroup's waves (the wide kernel) ----
+
+  static constexpr int kKeyOps = 2 * kSteps, kTileOps = kKeyOps + kCols;   // of 64 lanes x 16 bytes
+
+  // The wave's tile into operands: K's [half][step], then V's [column group].
+  __device__ __forceinline__ void convert(const Raw& r, u32x4* ops) {
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    values = reinterpret_cast<char*>(ops + kKeyOps * 64);      // V as loaded, where its operands will be
+    stage(r);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const float ks = byte_scale(words[half * 16 + c], g * (D / 4) / 32);
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st)
+        ops[(half * kSteps + st) * 64 + lane] = cvt_eight(r.k[half][st], ks);
+    }
+    uint32_t v[8];
+    float vs[8];
+    read_values(v, vs);
+    __builtin_amdgcn_wave_barrier();
+    put_values<0>(v, vs, ops);
+    put_values<1>(v, vs, ops);
+    if constexpr (D == 128) {
+      put_values<2>(v, vs, ops);
+      put_values<3>(v, vs, ops);
+    }
+  }
+
+  template <int SEL>
+  __device__ __forceinline__ void put_values(const uint32_t (&v)[8], const float (&vs)[8], u32x4* ops) const {
+    u32x4 even, odd;
+    value_operands<SEL>(v, vs, even, odd);
+    ops[(kKeyOps + 2 * SEL) * 64 + (threadIdx.x & 63)] = even;
+    ops[(kKeyOps + 2 * SEL + 1) * 64 + (threadIdx.x & 63)] = odd;
+  }
+
+  // K's operands of a tile, read while the tile before it is worked on.
+  struct KeyOps { u32x4 a[2][kSteps]; };
+  __device__ __forceinline__ static void read_keys(KeyOps& k, const u32x4* ops) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st)
+        k.a[half][st] = ops[(half * kSteps + st) * 64 + (threadIdx.x & 63)];
+  }
+
+  // One tile from its operands; k: its K's, then the next tile's.
+  template <bool SPARSE>
+  __device__ __forceinline__ void step_shared(KeyOps& k, const u32x4* ops, const u32x4* next, bool masked,
+                                              int first, const uint32_t* places, float c2) {
+    const int lane = threadIdx.x & 63;
+    if constexpr (!kKeysAhead) read_keys(k, ops);
+    Scores s;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) s.s[rt][half] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+      for (int part = 0; part < kParts; ++part)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          s.s[rt][0] = mma(k.a[0][st], q[rt][part][st], s.s[rt][0]);
+          s.s[rt][1] = mma(k.a[1][st], q[rt][part][st], s.s[rt][1]);
+        }
+    if constexpr (kKeysAhead) read_keys(k, next);
+    if constexpr (SPARSE) {
+      mask<SPARSE>(s, first, places);
+    } else {
+      // The compiler was seen to read a product's result right behind a branch,
+      // before it is there; the products end here, ahead of the branch.
+      if constexpr (RT == 1)
+        asm volatile("s_nop 7" : "+v"(s.s[0][0]), "+v"(s.s[0][1]));
+      else
+        asm volatile("s_nop 7" : "+v"(s.s[0][0]), "+v"(s.s[0][1]), "+v"(s.s[RT - 1][0]), "+v"(s.s[RT - 1][1]));
+      if (masked) mask<SPARSE>(s, first, places);
+    }
+    // V's operands, kAhead ahead of their products
+    const u32x4* vops = ops + kKeyOps * 64 + lane;
+    u32x4 a[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) a[j] = vops[j * 64];
+    __builtin_amdgcn_sched_barrier(0);
+    u32x4 p[RT][kParts];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) weights(s.s[rt], rt, c2, p[rt]);
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+#pragma unroll
+      for (int part = 0; part < kParts; ++part)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) o[rt][j] = mma(a[j % kAhead], p[rt][part], o[rt][j]);
+      if (j + kAhead < kCols) {
+        a[j % kAhead] = vops[(j + kAhead) * 64];
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  // (as far as the registers go: fp16's queries take twice as many)
+  static constexpr int kAhead = F16 && RT == 2 ? 2 : 4;
+  static constexpr bool kKeysAhead = !(F16 && RT == 2);
 };
 
 template <bool F16>
@@ -466,10 +601,6 @@ struct Split {
     more = s - each * workers;
   }
   __device__ __forceinline__ int border(int j) const { return j * each + min(j, more); }
-  __device__ __forceinline__ int owner(int step) const {
-    const int head = more * (each + 1);
-    return step < head ? step / (each + 1) : more + (step - head) / each;
-  }
 };
 
 __device__ __forceinline__ int unit_length(const AttnParams& p, int unit) {
@@ -492,6 +623,281 @@ __device__ __forceinline__ int block_sum(int x, int* buf) {
   return x;
 }
 
+// The unit being walked, and what its rows see.
+template <bool SPARSE>
+struct Unit {
+  int raw_ctx, ctx, length;                  // keys of the context; entries to walk
+  __device__ __forceinline__ Unit(const AttnParams& p, int unit) {
+    raw_ctx = max(p.ctx[SPARSE ? unit / p.next_n : unit], 0);
+    ctx = min(raw_ctx, p.max_ctx);
+    length = SPARSE ? p.topk : ctx;
+  }
+  // keys that query token t sees
+  __device__ __forceinline__ int seen(const AttnParams& p, int t) const {
+    return min(max(raw_ctx - p.next_n + 1 + t, 0), ctx);
+  }
+};
+
+// A worker's piece: the steps [at, end) from step unit_begin of `unit` on.
+struct Piece {
+  int begin, end, at;
+  int unit, unit_begin;
+  int steps, workers, each, more;
+
+  // False for a worker that has none.  sums, found: LDS, 4 and 2 words.
+  template <bool SPARSE>
+  __device__ __forceinline__ bool find(const AttnParams& p, int worker, int* sums, int* found) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    // (up to 64 units: every wave by itself, without a barrier)
+    const bool few = SPARSE || p.units <= 64;
+    int total = p.units * unit_steps(p.topk), mine = 0, scan = 0;
+    if constexpr (!SPARSE) {
+      if (few) {
+        scan = mine = lane < p.units ? unit_steps(unit_length(p, lane)) : 0;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+          const int x = __shfl_up(scan, off);
+          if (lane >= off) scan += x;
+        }
+        total = __shfl(scan, 63);
+      } else {
+        total = 0;
+        for (int b = tid; b < p.units; b += kAttnThreads) total += unit_steps(unit_length(p, b));
+        total = block_sum(total, sums);
+      }
+    }
+    const Split split(__builtin_amdgcn_readfirstlane(total), p);
+    if (worker >= split.workers) return false;
+    steps = split.steps;
+    workers = split.workers;
+    each = split.each;
+    more = split.more;
+    begin = at = split.border(worker);
+    end = split.border(worker + 1);
+    if constexpr (SPARSE) {
+      unit = begin / unit_steps(p.topk);
+      unit_begin = unit * unit_steps(p.topk);
+      return true;
+    }
+    if (few) {
+      const uint64_t here = __ballot(scan - mine <= begin && begin < scan);
+      unit = __builtin_ctzll(here);
+      unit_begin = __builtin_amdgcn_readlane(scan - mine, unit);
+      return true;
+    }
+    int base = 0;
+    for (int b0 = 0; base <= begin; b0 += kAttnThreads) {
+      const int b = b0 + tid;
+      mine = b < p.units ? unit_steps(unit_length(p, b)) : 0;
+      scan = mine;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int x = __shfl_up(scan, off);
+        if (lane >= off) scan += x;
+      }
+      if (lane == 63) sums[wave] = scan;
+      __syncthreads();
+      int first = base + scan - mine;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) first += sums[w];
+        base += sums[w];
+      }
+      if (first <= begin && begin < first + mine) {
+        found[0] = b;
+        found[1] = first;
+      }
+      __syncthreads();
+    }
+    unit = __builtin_amdgcn_readfirstlane(found[0]);
+    unit_begin = __builtin_amdgcn_readfirstlane(found[1]);
+    return true;
+  }
+
+  // The kernel that joins the parts learns where a unit begun here has its own.
+  __device__ __forceinline__ void note(const AttnParams& p, int worker, int unit_end) const {
+    int2 n = make_int2(0, 1);                // first slot, parts
+    if (at > unit_begin || unit_end > end) {
+      const int head = more * (each + 1), last = unit_end - 1;
+      const int owner = last < head ? last / (each + 1) : more + (last - head) / each;
+      n = make_int2(2 * worker + (at == begin ? 0 : 1), owner - worker + 1);
+    }
+    p.notes[unit] = n;
+  }
+};
+
+// The first cache blocks of keys [stage, stage_end) of a unit, into LDS.
+template <int D, bool SPARSE>
+__device__ __forceinline__ void fill_places(const AttnParams& p, uint32_t* blocks, int unit,
+                                            int stage, int stage_end, int n_tiles, int seen_sparse) {
+  constexpr int kEach = SPARSE ? 1 : 16;     // keys per entry
+  const int32_t* table = p.bt + (int64_t)(SPARSE ? unit / p.next_n : unit) * p.bt_stride;
+  const int32_t* index = SPARSE ? p.indices + (int64_t)unit * p.idx_stride : nullptr;
+  for (int i = threadIdx.x; i < n_tiles * (kTile / kEach); i += kAttnThreads) {
+    int j = stage + i * kEach;
+    bool use = j < stage_end;
+    if constexpr (SPARSE) {
+      j = use ? index[j] : -1;
+      use = j >= 0 && j < seen_sparse;
+    }
+    uint32_t first = SPARSE ? kNoKey : 0u;
+    if (use) {
+      const int id = min(max(table[j >> p.bs_shift], 0), p.num_blocks - 1);
+      const uint32_t slot = ((uint32_t)id << p.bs_shift) + (j & ((1 << p.bs_shift) - 1));
+      first = slot * p.kv_heads * (D / 32);
+    }
+    blocks[i] = first;
+  }
+}
+
+// Row r of a unit's KV head: its query token of all, and its head.
+struct RowAt {
+  int token, head;
+  template <bool SPARSE>
+  __device__ __forceinline__ static RowAt of(const AttnParams& p, int unit, int kv_head, int r) {
+    const int t = SPARSE ? 0 : r / p.group;
+    return {SPARSE ? unit : unit * p.next_n + t, kv_head * p.group + (SPARSE ? r : r - t * p.group)};
+  }
+  __device__ __forceinline__ int64_t out(const AttnParams& p) const {
+    return (int64_t)token * (p.kv_heads * p.group) + head;
+  }
+};
+
+// The lane's piece st of a query, bf16; with F16 its two exact bf16 parts.
+template <int D, bool F16>
+__device__ __forceinline__ void load_query(const AttnParams& p, RowAt row, int st, u32x4& hi, u32x4& lo) {
+  const int g = (threadIdx.x & 63) >> 4;
+  const uint16_t* src = p.q + (int64_t)row.token * p.q_stride + row.head * D + g * (D / 4);
+  hi = *reinterpret_cast<const u32x4*>(src + st * 8);
+  if (p.negate) hi ^= 0x80008000u;
+  if constexpr (F16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = (float)__builtin_bit_cast(_Float16, (uint16_t)(hi[i] & 0xffff));
+      const float y = (float)__builtin_bit_cast(_Float16, (uint16_t)(hi[i] >> 16));
+      hi[i] = pack_bf16(x, y);
+      // the part below bf16's eight bits; an infinity stays in hi alone
+      const float rx = x - bf16_lo(hi[i]), ry = y - bf16_hi(hi[i]);
+      lo[i] = pack_bf16(__builtin_isfinite(x) ? rx : 0.f, __builtin_isfinite(y) ? ry : 0.f);
+    }
+  }
+}
+
+// Scale words of four adjacent KV heads, one for each wave.  A thread loads the
+// four of one key and pool (one piece instead of four) a step of 128 keys ahead
+// of their use, through LDS to the waves: [step parity][head][pool][key].  The
+// barrier of a step also keeps the waves together, on the same cache lines.
+template <int D, bool SPARSE>
+struct SharedScales {
+  static constexpr int kWords = kWaves * 2 * kStep;      // of a step
+  uint32_t* lds;                             // [2][kWords]
+  const Tiles<D, SPARSE>& tiles;             // at the first of the four heads
+  int n_tiles, wave;
+  u32x4 next;
+
+  __device__ __forceinline__ SharedScales(uint32_t* at, const Tiles<D, SPARSE>& t, int n, int w)
+      : lds(at), tiles(t), n_tiles(n), wave(w) {
+    __syncthreads();                         // the buffers' last use is over
+    load(0);
+    put(0);
+    load(1);
+    __syncthreads();
+  }
+  // At the first tile of a step: the next step's words are put down.
+  __device__ __forceinline__ void turn(int step) {
+    if (step > 0) __syncthreads();
+    put(step + 1);
+    load(step + 2);
+  }
+  __device__ __forceinline__ uint32_t word(int tile) const {
+    const int lane = threadIdx.x & 63;
+    return lds[(tile / kWaves & 1) * kWords + (wave * 2 + (lane >> 5)) * kStep + tile % kWaves * kTile +
+               (lane & 31)];
+  }
+  __device__ __forceinline__ void load(int step) {
+    const int pool = threadIdx.x / kStep;
+    const int key = min(step * kStep + (int)threadIdx.x % kStep, n_tiles * kTile - 1);
+    const uint32_t block = tiles.key_first(key);
+    const Bytes from = (pool ? tiles.vs : tiles.ks) + block;
+    if constexpr (D == 128) {
+      next = load_from<u32x4>(from);
+    } else {
+      const u32x2 x = load_from<u32x2>(from);
+      next = u32x4{x[0] & 0xffffu, x[0] >> 16, x[1] & 0xffffu, x[1] >> 16};
+    }
+  }
+  __device__ __forceinline__ void put(int step) const {
+    const int pool = threadIdx.x / kStep, key = threadIdx.x % kStep;
+#pragma unroll
+    for (int h = 0; h < kWaves; ++h) lds[(step & 1) * kWords + (h * 2 + pool) * kStep + key] = next[h];
+  }
+};
+
+// A wave's tiles, every fourth, loaded two ahead (past the last, the last
+// again, so that every load is unconditional).  Keys that some row does not see
+// lie in the context's last 15 + 32, so only a wave's last tile can hold any.
+template <int D, int RT, bool F16, bool QLDS, bool SPARSE>
+__device__ __forceinline__ void walk(Rows<D, RT, F16, QLDS>& rows, const Tiles<D, SPARSE>& tiles,
+                                     const uint32_t* blocks, int tile, int n_tiles, int stage, float c2) {
+  const int last = tile + (n_tiles - 1 - tile) / kWaves * kWaves;
+  Raw r[3];
+  tiles.load(r[0], tile);
+  tiles.load(r[1], min(tile + kWaves, last));
+  const auto advance = [&](auto turn) {
+    constexpr int i = decltype(turn)::value, ahead = (i + 2) % 3;
+    if (QLDS) asm volatile("" ::: "memory");   // the queries are not kept in registers
+    tiles.load(r[ahead], min(tile + 2 * kWaves, last));
+    rows.template step<SPARSE, SPARSE>(r[i], 0, blocks + tile * kTile, c2);
+    tile += kWaves;
+  };
+  while (tile < last) {
+    advance(std::integral_constant<int, 0>{});
+    if (tile >= last) {
+      r[0] = r[1];
+      break;
+    }
+    advance(std::integral_constant<int, 1>{});
+    if (tile >= last) {
+      r[0] = r[2];
+      break;
+    }
+    advance(std::integral_constant<int, 2>{});
+  }
+  rows.template step<true, SPARSE>(r[0], stage + tile * kTile, blocks + tile * kTile, c2);
+}
+
+// Every tile, for a wave that has a KV head of its own: in steps of four, loaded
+// three ahead, the scales from the workgroup's.  The last tiles, where keys may
+// be hidden from some row (two at most) or a step is not whole, one by one.
+template <int D, bool F16, bool SPARSE>
+__device__ __forceinline__ void walk_all(Rows<D, 1, F16, false>& rows, const Tiles<D, SPARSE>& tiles,
+                                         SharedScales<D, SPARSE>& scales, const uint32_t* blocks,
+                                         int n_tiles, int stage, float c2) {
+  static_assert(kWaves == 4, "a step is four tiles");
+  const int last = n_tiles - 1, whole = (SPARSE ? n_tiles : max(n_tiles - 2, 0)) / 4 * 4;
+  Raw r[4];
+#pragma unroll
+  for (int u = 0; u < 3; ++u) tiles.template load<false>(r[u], min(u, last));
+  int tile = 0;
+  for (; tile < whole; tile += 4) {
+    scales.turn(tile / 4);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      tiles.template load<false>(r[(u + 3) % 4], min(tile + u + 3, last));
+      r[u].s = scales.word(tile + u);
+      rows.template step<SPARSE, SPARSE>(r[u], 0, blocks + (tile + u) * kTile, c2);
+    }
+  }
+  for (; tile <= last; ++tile) {
+    if (tile % 4 == 0) scales.turn(tile / 4);
+    tiles.template load<false>(r[3], min(tile + 3, last));
+    r[0].s = scales.word(tile);
+    rows.template step<true, SPARSE>(r[0], stage + tile * kTile, blocks + tile * kTile, c2);
+#pragma unroll
+    for (int u = 0; u < 3; ++u) r[u] = r[u + 1];
+  }
+}
+
 template <int D, int RT, bool F16, bool SPARSE>
 __global__ void __launch_bounds__(kAttnThreads, 2)
 attention_kernel(const AttnParams p) {
@@ -499,7 +905,7 @@ attention_kernel(const AttnParams p) {
   constexpr int kPitch = D + 4;              // LDS floats per row of the join
   constexpr int kEach = SPARSE ? 1 : 16;     // keys per entry of `blocks`
   constexpr int kStage = SPARSE ? kAttnStageSparse : kAttnStage;   // keys staged at a time
-  using State = Rows<D, RT, F16>;
+  using State = Rows<D, RT, F16, RT == 2>;
   // the join's rows, or (before it) queries, places and scales
   constexpr int kPlaceBytes = kStage / kEach * 4, kQueryBytes = State::kQueriesInLds ? State::kQueryWords * 16 : 0;
   constexpr int kJoinBytes = kWaves * kRows * kPitch * 4, kLoopBytes = kQueryBytes + kPlaceBytes + kWaves * State::kStageBytes;
@@ -520,162 +926,55 @@ attention_kernel(const AttnParams p) {
   const int c = lane & 15, g = lane >> 4;
   const int unit_rows = SPARSE ? p.group : p.next_n * p.group;
 
-  // the worker's piece, and the unit it begins in
-  int unit, unit_begin;                      // unit_begin: its first step
-  int total;
-  if constexpr (SPARSE) {
-    total = p.units * unit_steps(p.topk);
-  } else {
-    int sum = 0;
-    for (int b = tid; b < p.units; b += kAttnThreads) sum += unit_steps(unit_length(p, b));
-    total = block_sum(sum, sums);
-  }
-  const Split split(__builtin_amdgcn_readfirstlane(total), p);
-  if (worker >= split.workers) return;
-  const int piece_begin = split.border(worker), piece_end = split.border(worker + 1);
-  if constexpr (SPARSE) {
-    unit = piece_begin / unit_steps(p.topk);
-    unit_begin = unit * unit_steps(p.topk);
-  } else {
-    int base = 0;
-    for (int b0 = 0; base <= piece_begin; b0 += kAttnThreads) {
-      const int b = b0 + tid;
-      const int mine = b < p.units ? unit_steps(unit_length(p, b)) : 0;
-      int scan = mine;
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int x = __shfl_up(scan, off);
-        if (lane >= off) scan += x;
-      }
-      if (lane == 63) sums[wave] = scan;
-      __syncthreads();
-      int at = base + scan - mine;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        if (w < wave) at += sums[w];
-        base += sums[w];
-      }
-      if (at <= piece_begin && piece_begin < at + mine) {
-        found[0] = b;
-        found[1] = at;
-      }
-      __syncthreads();
-    }
-    unit = __builtin_amdgcn_readfirstlane(found[0]);
-    unit_begin = __builtin_amdgcn_readfirstlane(found[1]);
-  }
+  Piece piece;
+  if (!piece.find<SPARSE>(p, worker, sums, found)) return;
 
-  const Tiles<D, SPARSE> tiles(p, blocks);
+  const Tiles<D, SPARSE> tiles(p, blocks, kv_head);
   State rows;
-  rows.lds = shared + kQueryBytes + kPlaceBytes + wave * State::kStageBytes;
+  rows.words = reinterpret_cast<uint32_t*>(shared + kQueryBytes + kPlaceBytes + wave * State::kStageBytes);
+  rows.values = reinterpret_cast<char*>(rows.words + 64);
   rows.q_lds = queries;
-  for (int at = piece_begin; at < piece_end; ++unit) {
-    const int seq = SPARSE ? unit / p.next_n : unit;
-    const int raw_ctx = max(p.ctx[seq], 0);
-    const int ctx = min(raw_ctx, p.max_ctx);
-    const int length = SPARSE ? p.topk : ctx;
-    const int unit_end = unit_begin + unit_steps(length);
-    const int begin = (at - unit_begin) * kStep;                 // keys of this part
-    const int end = min(length, (min(unit_end, piece_end) - unit_begin) * kStep);
-    const bool whole = at == unit_begin && unit_end <= piece_end;
-    // keys that query token t sees
-    const auto seen_by = [&](int t) { return min(max(raw_ctx - p.next_n + 1 + t, 0), ctx); };
-    const int seen_sparse = SPARSE ? seen_by(unit % p.next_n) : 0;
+  for (; piece.at < piece.end; ++piece.unit) {
+    const int unit = piece.unit;
+    const Unit<SPARSE> u(p, unit);
+    const int unit_end = piece.unit_begin + unit_steps(u.length);
+    const int begin = (piece.at - piece.unit_begin) * kStep;     // keys of this part
+    const int end = min(u.length, (min(unit_end, piece.end) - piece.unit_begin) * kStep);
+    const bool whole = piece.at == piece.unit_begin && unit_end <= piece.end;
+    const int seen_sparse = SPARSE ? u.seen(p, unit % p.next_n) : 0;
 
     rows.clear();
-    rows.most = ctx;
+    rows.most = u.ctx;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       // lanes past the last row repeat it; their results are dropped
       const int r = min(row0 + rt * 16 + c, unit_rows - 1);
-      const int t = SPARSE ? 0 : r / p.group;
-      rows.seen[rt] = SPARSE ? seen_sparse : seen_by(t);
-      const int token = SPARSE ? unit : unit * p.next_n + t;
-      const int head = kv_head * p.group + (SPARSE ? r : r - t * p.group);
-      const uint16_t* src = p.q + (int64_t)token * p.q_stride + head * D + g * (D / 4);
+      rows.seen[rt] = SPARSE ? seen_sparse : u.seen(p, r / p.group);
+      const RowAt row = RowAt::of<SPARSE>(p, unit, kv_head, r);
 #pragma unroll
       for (int st = 0; st < D / 32; ++st) {
-        u32x4 w = *reinterpret_cast<const u32x4*>(src + st * 8), lo;
-        if (p.negate) w ^= 0x80008000u;
-        if constexpr (F16) {
-          u32x4 hi;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x = (float)__builtin_bit_cast(_Float16, (uint16_t)(w[i] & 0xffff));
-            const float y = (float)__builtin_bit_cast(_Float16, (uint16_t)(w[i] >> 16));
-            hi[i] = pack_bf16(x, y);
-            // the part below bf16's eight bits; an infinity stays in hi alone
-            const float rx = x - bf16_lo(hi[i]), ry = y - bf16_hi(hi[i]);
-            lo[i] = pack_bf16(__builtin_isfinite(x) ? rx : 0.f, __builtin_isfinite(y) ? ry : 0.f);
-          }
-          w = hi;
-        }
+        u32x4 hi, lo;
+        load_query<D, F16>(p, row, st, hi, lo);
         if constexpr (State::kQueriesInLds) {
           // (every wave holds all row tiles' lanes; the first RT write one each)
           if (wave == rt) {
-            queries[(rt * State::kParts * State::kSteps + st) * 64 + lane] = w;
+            queries[(rt * State::kParts * State::kSteps + st) * 64 + lane] = hi;
             if (F16) queries[((rt * State::kParts + State::kParts - 1) * State::kSteps + st) * 64 + lane] = lo;
           }
         } else {
-          rows.q[rt][0][st] = w;
+          rows.q[rt][0][st] = hi;
           if (F16) rows.q[rt][State::kParts - 1][st] = lo;
         }
       }
     }
 
-    const int32_t* table = p.bt + (int64_t)seq * p.bt_stride;
-    const int32_t* index = SPARSE ? p.indices + (int64_t)unit * p.idx_stride : nullptr;
     for (int stage = begin; stage < end; stage += kStage) {
       const int stage_end = min(end, stage + kStage);
       const int n_tiles = (stage_end - stage + kTile - 1) / kTile;
       __syncthreads();                       // the last use of `blocks` is over
-      for (int i = tid; i < n_tiles * (kTile / kEach); i += kAttnThreads) {
-        int j = stage + i * kEach;
-        bool use = j < stage_end;
-        if constexpr (SPARSE) {
-          j = use ? index[j] : -1;
-          use = j >= 0 && j < seen_sparse;
-        }
-        uint32_t first = SPARSE ? kNoKey : 0u;
-        if (use) {
-          const int id = min(max(table[j >> p.bs_shift], 0), p.num_blocks - 1);
-          const uint32_t slot = ((uint32_t)id << p.bs_shift) + (j & ((1 << p.bs_shift) - 1));
-          first = (slot * p.kv_heads + kv_head) * (D / 32);
-        }
-        blocks[i] = first;
-      }
+      fill_places<D, SPARSE>(p, blocks, unit, stage, stage_end, n_tiles, seen_sparse);
       __syncthreads();
-      // The wave's tiles, loaded two ahead (past the last, the last again, so that
-      // every load is unconditional).  Keys that some row does not see lie in
-      // the context's last 15 + 32, so only a wave's last tile can hold any.
-      if (wave < n_tiles) {
-        const int last = wave + (n_tiles - 1 - wave) / kWaves * kWaves;
-        Raw r[3];
-        int tile = wave;
-        tiles.load(r[0], tile);
-        tiles.load(r[1], min(tile + kWaves, last));
-        const auto advance = [&](auto turn) {
-          constexpr int i = decltype(turn)::value, ahead = (i + 2) % 3;
-          if (State::kQueriesInLds) asm volatile("" ::: "memory");   // not kept in registers
-          tiles.load(r[ahead], min(tile + 2 * kWaves, last));
-          rows.template step<SPARSE, SPARSE>(r[i], 0, blocks + tile * kTile, p.c2);
-          tile += kWaves;
-        };
-        while (tile < last) {
-          advance(std::integral_constant<int, 0>{});
-          if (tile >= last) {
-            r[0] = r[1];
-            break;
-          }
-          advance(std::integral_constant<int, 1>{});
-          if (tile >= last) {
-            r[0] = r[2];
-            break;
-          }
-          advance(std::integral_constant<int, 2>{});
-        }
-        rows.template step<true, SPARSE>(r[0], stage + tile * kTile, blocks + tile * kTile, p.c2);
-      }
+      if (wave < n_tiles) walk(rows, tiles, blocks, wave, n_tiles, stage, p.c2);
     }
 
     // join the four waves
@@ -704,7 +1003,7 @@ attention_kernel(const AttnParams p) {
     }
     __syncthreads();
     const int64_t part_slot =
-        ((int64_t)member * p.workers + worker) * 2 + (at == piece_begin ? 0 : 1);
+        ((int64_t)member * p.workers + worker) * 2 + (piece.at == piece.begin ? 0 : 1);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       // thread: D/16 adjacent elements of row tid / 16
@@ -725,10 +1024,7 @@ attention_kernel(const AttnParams p) {
           for (int w = 0; w < kWaves; ++w) x[j] += join[(w * kRows + rt * 16 + jr) * kPitch + jc + j];
         }
         if (whole) {
-          const int t = SPARSE ? 0 : r / p.group;
-          const int64_t token = SPARSE ? unit : unit * p.next_n + t;
-          const int head = kv_head * p.group + (SPARSE ? r : r - t * p.group);
-          const int64_t out_row = token * (p.kv_heads * p.group) + head;
+          const int64_t out_row = RowAt::of<SPARSE>(p, unit, kv_head, r).out(p);
           const float inv = lj == 0.f ? 0.f : 1.f / lj;
           uint32_t w[D / 32];
 #pragma unroll
@@ -751,92 +1047,352 @@ attention_kernel(const AttnParams p) {
       }
     }
     __syncthreads();                         // the join's LDS is read
-    if (p.workers > 1 && member == 0 && tid == 0 && at == unit_begin) {
-      int2 note = make_int2(0, 1);           // first slot, parts
-      if (!whole) note = make_int2(2 * worker + (at == piece_begin ? 0 : 1),
-                                   split.owner(unit_end - 1) - worker + 1);
-      p.notes[unit] = note;
-    }
-    at = unit_end;
-    unit_begin = unit_end;
+    if (p.join && member == 0 && tid == 0 && piece.at == piece.unit_begin)
+      piece.note(p, worker, unit_end);
+    piece.at = piece.unit_begin = unit_end;
   }
 }
 
-// Joins the parts of the units that were cut: WAVES waves per (query token,
-// head).  Part 0 is in the noted slot, the next in slot 2j of the workers that
-// follow.
-template <int D, bool F16, int WAVES>
+// The results of a wave that has rows of its own, from row `first` of the KV
+// head on: a lane has D/4 adjacent elements of row l % 16 of each row tile.
+// part0: where its rows' parts go if the unit is cut.
+template <bool SPARSE, int D, int RT, bool F16, bool QLDS>
+__device__ __forceinline__ void store_rows(const AttnParams& p, const Rows<D, RT, F16, QLDS>& rows,
+                                           bool whole, int unit, int kv_head, int unit_rows, int first,
+                                           int64_t part0) {
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const float m = rows.m[rt], l = row_sum(rows.l[rt]);
+    const bool is_nan = (rows.nan_rows >> rt) & 1;
+    int r = first + rt * 16 + c;
+    asm volatile("" : "+v"(r));              // nothing derived from it is kept through the loops
+    if (r < unit_rows) {
+      if (whole) {
+        const int64_t out_row = RowAt::of<SPARSE>(p, unit, kv_head, r).out(p);
+        const float inv = is_nan ? __builtin_nanf("") : l == 0.f ? 0.f : 1.f / l;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + out_row * D + g * (D / 4));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[D / 32];
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j)
+            w[j] = pack_out<F16>(rows.o[rt][2 * j][i] * inv, rows.o[rt][2 * j + 1][i] * inv);
+          if constexpr (D == 128)
+            *reinterpret_cast<u32x4*>(dst + i * 4) = u32x4{w[0], w[1], w[2], w[3]};
+          else
+            *reinterpret_cast<u32x2*>(dst + i * 2) = u32x2{w[0], w[1]};
+        }
+        if (p.lse && g == 0)
+          p.lse[out_row] = l == 0.f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
+      } else {
+        const int64_t part = part0 + (r - first);
+        f32x4* dst = reinterpret_cast<f32x4*>(p.part_o + part * D + g * (D / 4));
+        const float one = is_nan ? __builtin_nanf("") : 1.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j)
+            dst[i * (D / 64) + j] =
+                f32x4{rows.o[rt][4 * j][i] * one, rows.o[rt][4 * j + 1][i] * one,
+                      rows.o[rt][4 * j + 2][i] * one, rows.o[rt][4 * j + 3][i] * one};
+        if (g == 0) p.part_ml[part] = make_float2(m, l);
+      }
+    }
+  }
+}
+
+// Several KV heads: the four waves take a KV head each and walk the same keys,
+// so that a token's adjacent heads are read at about the same time and the
+// cache lines and DRAM pages they share are fetched once.  (With a workgroup per
+// KV head, 64 bytes of every token's row at a time, the loads alone ran at
+// 3.7 TB/s on 8 heads, 32 sequences of 1024..32768 tokens; whole blocks are
+// read at about 6.)  Every wave has rows of its own; nothing is joined.
+template <int D, int RT, bool F16, bool SPARSE>
+__global__ void __launch_bounds__(kAttnThreads, 2)
+attention_heads_kernel(const AttnParams p) {
+  constexpr int kRows = 16 * RT * kWaves;    // of a member: 16 * RT of each of its four heads
+  constexpr int kEach = SPARSE ? 1 : 16;
+  constexpr int kStage = SPARSE ? kAttnStageSparse : kAttnStage;
+  using State = Rows<D, RT, F16, false>;
+  __shared__ __attribute__((aligned(16))) uint32_t blocks[kStage / kEach];
+  __shared__ __attribute__((aligned(16))) char staging[kWaves][State::kStageBytes];
+  __shared__ uint32_t scales[2 * SharedScales<D, SPARSE>::kWords];
+  __shared__ int sums[kWaves], found[2];
+
+  const int members = p.row_groups * (p.kv_heads / kWaves);
+  const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
+  const int worker = idx / members * 8 + xcd, member = idx % members;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kv_head = member / p.row_groups * kWaves + wave;   // (Hkv is a multiple of four)
+  const int row0 = member % p.row_groups * 16 * RT;
+  const int c = lane & 15;
+  const int unit_rows = SPARSE ? p.group : p.next_n * p.group;
+
+  Piece piece;
+  if (!piece.find<SPARSE>(p, worker, sums, found)) return;
+
+  const Tiles<D, SPARSE> tiles(p, blocks, kv_head), heads(p, blocks, kv_head - wave);
+  State rows;
+  rows.words = reinterpret_cast<uint32_t*>(staging[wave]);
+  rows.values = staging[wave] + 256;
+  for (; piece.at < piece.end; ++piece.unit) {
+    const int unit = piece.unit;
+    const Unit<SPARSE> u(p, unit);
+    const int unit_end = piece.unit_begin + unit_steps(u.length);
+    const int begin = (piece.at - piece.unit_begin) * kStep;
+    const int end = min(u.length, (min(unit_end, piece.end) - piece.unit_begin) * kStep);
+    const bool whole = piece.at == piece.unit_begin && unit_end <= piece.end;
+    const int seen_sparse = SPARSE ? u.seen(p, unit % p.next_n) : 0;
+
+    rows.clear();
+    rows.most = u.ctx;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      int r = min(row0 + rt * 16 + c, unit_rows - 1);
+      asm volatile("" : "+v"(r));
+      rows.seen[rt] = SPARSE ? seen_sparse : u.seen(p, r / p.group);
+      const RowAt row = RowAt::of<SPARSE>(p, unit, kv_head, r);
+#pragma unroll
+      for (int st = 0; st < D / 32; ++st)
+        load_query<D, F16>(p, row, st, rows.q[rt][0][st], rows.q[rt][State::kParts - 1][st]);
+    }
+    for (int stage = begin; stage < end; stage += kStage) {
+      const int stage_end = min(end, stage + kStage);
+      const int n_tiles = (stage_end - stage + kTile - 1) / kTile;
+      __syncthreads();                       // the last use of `blocks` is over
+      fill_places<D, SPARSE>(p, blocks, unit, stage, stage_end, n_tiles, seen_sparse);
+      __syncthreads();
+      SharedScales<D, SPARSE> shared(scales, heads, n_tiles, wave);
+      walk_all(rows, tiles, shared, blocks, n_tiles, stage, p.c2);
+    }
+
+    const int64_t part_slot =
+        ((int64_t)member * p.workers + worker) * 2 + (piece.at == piece.begin ? 0 : 1);
+    store_rows<SPARSE>(p, rows, whole, unit, kv_head, unit_rows, row0,
+                       part_slot * kRows + wave * 16 * RT);
+    if (p.join && member == 0 && tid == 0 && piece.at == piece.unit_begin)
+      piece.note(p, worker, unit_end);
+    piece.at = piece.unit_begin = unit_end;
+  }
+}
+
+// Many rows on a KV head: each wave has 16 * RT rows of its own, and the four
+// share the keys.  The matrix cores and the vector ALU hardly overlap, and with
+// every wave converting the keys that it multiplies, the conversions take as
+// long as the products of 32 rows.  Here a wave converts one of a step's four
+// tiles for all four, into operands in LDS (16 KB a tile), and reads the others'
+// from there.  No row is split over waves, so nothing is joined at the end.
+template <int D, int RT, bool F16, bool SPARSE>
+__global__ void __launch_bounds__(kAttnThreads, 2)
+attention_wide_kernel(const AttnParams p) {
+  constexpr int kRows = 16 * RT * kWaves;
+  constexpr int kEach = SPARSE ? 1 : 16;
+  constexpr int kStage = SPARSE ? kAttnStageSparse : kAttnStage;
+  using State = Rows<D, RT, F16, false>;
+  __shared__ u32x4 ops[kWaves][State::kTileOps * 64];
+  __shared__ __attribute__((aligned(16))) uint32_t blocks[kStage / kEach];
+  __shared__ __attribute__((aligned(16))) uint32_t words[kWaves][64];
+  __shared__ uint32_t nan_words[kWaves][kTile], nan_flags[kWaves];
+  __shared__ int sums[kWaves], found[2];
+
+  const int members = p.row_groups * p.kv_heads;
+  const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
+  const int worker = idx / members * 8 + xcd, member = idx % members;
+  const int kv_head = member / p.row_groups, row0 = member % p.row_groups * kRows;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int unit_rows = SPARSE ? p.group : p.next_n * p.group;
+  const int wave_row = row0 + wave * 16 * RT;
+
+  Piece piece;
+  if (!piece.find<SPARSE>(p, worker, sums, found)) return;
+
+  const Tiles<D, SPARSE> tiles(p, blocks, kv_head);
+  State rows;
+  rows.words = words[wave];
+  for (; piece.at < piece.end; ++piece.unit) {
+    const int unit = piece.unit;
+    const Unit<SPARSE> u(p, unit);
+    const int unit_end = piece.unit_begin + unit_steps(u.length);
+    const int begin = (piece.at - piece.unit_begin) * kStep;
+    const int end = min(u.length, (min(unit_end, piece.end) - piece.unit_begin) * kStep);
+    const bool whole = piece.at == piece.unit_begin && unit_end <= piece.end;
+    const int seen_sparse = SPARSE ? u.seen(p, unit % p.next_n) : 0;
+    // keys that all rows of the workgroup see (rows in order of t)
+    const int least = SPARSE ? 0 : u.seen(p, row0 / p.group);
+
+    rows.clear();
+    rows.most = u.ctx;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      int r = min(wave_row + rt * 16 + c, unit_rows - 1);
+      asm volatile("" : "+v"(r));            // nothing derived from it is kept through the loops
+      rows.seen[rt] = SPARSE ? seen_sparse : u.seen(p, r / p.group);
+      const RowAt row = RowAt::of<SPARSE>(p, unit, kv_head, r);
+#pragma unroll
+      for (int st = 0; st < D / 32; ++st)
+        load_query<D, F16>(p, row, st, rows.q[rt][0][st], rows.q[rt][State::kParts - 1][st]);
+    }
+
+    for (int stage = begin; stage < end; stage += kStage) {
+      const int stage_end = min(end, stage + kStage);
+      const int n_tiles = (stage_end - stage + kTile - 1) / kTile;
+      __syncthreads();                       // the last use of `blocks` is over
+      fill_places<D, SPARSE>(p, blocks, unit, stage, stage_end, n_tiles, seen_sparse);
+      __syncthreads();
+      // a wave without a tile of its own in the last step repeats the last one
+      Raw r;
+      tiles.load(r, min(wave, n_tiles - 1));
+      for (int tile0 = 0; tile0 < n_tiles; tile0 += kWaves) {
+        const int own = min(tile0 + wave, n_tiles - 1);
+        int half_lane = lane & 31;
+        asm volatile("" : "+v"(half_lane));
+        const bool any = SPARSE ? blocks[own * kTile + half_lane] != kNoKey
+                                : stage + own * kTile + half_lane < rows.most;
+        r.s = any ? r.s : 0u;
+        __syncthreads();                     // the operands are read
+        const bool bad = __any(State::has_nan(r.s));
+        if (lane == 0) nan_flags[wave] = bad;
+        if (__builtin_expect(bad, 0)) {
+          if (lane & 32) nan_words[wave][half_lane] = r.s;
+          r.s = State::without_nan(r.s);
+        }
+        rows.convert(r, ops[wave]);
+        tiles.load(r, min(tile0 + kWaves + wave, n_tiles - 1));
+        __syncthreads();
+        const int n = min(n_tiles - tile0, kWaves);
+        if (__builtin_expect(__any((lane < n ? nan_flags[lane & (kWaves - 1)] : 0u) != 0), 0)) {
+          for (int w = 0; w < n; ++w)
+            if (nan_flags[w])
+              for (int key = 0; key < kTile; ++key)
+                rows.template mark_nan<!SPARSE>(nan_words[w][key], stage + (tile0 + w) * kTile + key);
+        }
+        const bool masked = stage + (tile0 + kWaves) * kTile > least;
+        typename State::KeyOps k;
+        if constexpr (State::kKeysAhead) State::read_keys(k, ops[0]);
+#pragma nounroll
+        for (int w = 0; w < n; ++w)
+          rows.template step_shared<SPARSE>(k, ops[w], ops[min(w + 1, n - 1)], masked,
+                                            stage + (tile0 + w) * kTile,
+                                            blocks + (tile0 + w) * kTile, p.c2);
+      }
+    }
+
+    const int64_t part_slot =
+        ((int64_t)member * p.workers + worker) * 2 + (piece.at == piece.begin ? 0 : 1);
+    store_rows<SPARSE>(p, rows, whole, unit, kv_head, unit_rows, wave_row, part_slot * kRows + wave * 16 * RT);
+    if (p.join && member == 0 && tid == 0 && piece.at == piece.unit_begin)
+      piece.note(p, worker, unit_end);
+    piece.at = piece.unit_begin = unit_end;
+  }
+}
+
+// Joins the parts of the units that were cut: GROUPS groups of D/4 lanes (16
+// bytes of a row each) per (query token, head).  Part 0 is in the noted slot,
+// the next in slot 2j of the workers that follow.  Bound by the latency of its
+// three loads in a row (note, maxima, rows), so a group keeps four parts in
+// flight, and a block of one item covers 32 parts at a time.
+template <int D, bool F16, int GROUPS>
 __global__ void __launch_bounds__(256)
 attention_join_kernel(const AttnParams p, int sparse) {
-  constexpr int kItems = 4 / WAVES, kPer = D / 64;
-  __shared__ float part_x[WAVES > 1 ? 4 : 1][D], part_l[4];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t item = (int64_t)blockIdx.x * kItems + wave / WAVES;
-  const int mine = wave % WAVES;
-  if (item >= p.rows_heads) return;            // (whole blocks when WAVES > 1)
+  constexpr int kLanes = D / 4, kBlockGroups = 256 / kLanes;
+  static_assert(GROUPS == 1 || GROUPS == kBlockGroups, "one item per group or per block");
+  __shared__ f32x4 part_x[GROUPS > 1 ? kBlockGroups : 1][kLanes];
+  __shared__ float part_ml[GROUPS > 1 ? kBlockGroups : 1][2];
+  const int group = threadIdx.x / kLanes, i = threadIdx.x % kLanes;
+  const int64_t item = GROUPS > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * kBlockGroups + group;
+  if (item >= p.rows_heads) return;            // (no block of one item is partly out)
   const int heads = p.kv_heads * p.group;
-  const int token = (int)(item / heads), head = (int)(item % heads);
-  const int unit = sparse ? token : token / p.next_n;
-  const int2 note = p.notes[unit];
+  const int token = (int)(item / heads), head = (int)(item - (int64_t)token * heads);
+  const int2 note = p.notes[sparse ? token : token / p.next_n];
   const int n = note.y;
   if (n <= 1) return;                          // written by its only worker
   const int kv_head = head / p.group;
   const int r = head % p.group + (sparse ? 0 : token % p.next_n * p.group);
-  const int rows = 16 * p.row_tiles;
-  const int64_t member = kv_head * p.row_groups + r / rows;
-  const int64_t base = member * p.workers * 2;
-  const auto part = [&](int i) {
-    const int64_t slot = base + (i == 0 ? note.x : ((note.x >> 1) + i) * 2);
-    return slot * rows + r % rows;
-  };
-  float m = kLowest;
-  for (int i = lane; i < n; i += 64) m = fmaxf(m, p.part_ml[part(i)].x);
+  // a member's rows: of one KV head, or of member_heads of them
+  const int rows = p.member_rows, rows_each = rows / p.member_heads;
+  const int64_t base = (kv_head / p.member_heads * p.row_groups + r / rows_each) * (int64_t)p.workers * 2;
+  const int row = kv_head % p.member_heads * rows_each + r % rows_each;
+  const int first = GROUPS > 1 ? group : 0;
+  constexpr int kStride = GROUPS;
+  float m = kLowest, l = 0.f;
+  f32x4 x{0.f, 0.f, 0.f, 0.f};
+  for (int j0 = first; j0 < n; j0 += 4 * kStride) {
+    float2 ml[4];
+    f32x4 y[4];
 #pragma unroll
-  for (int off = 1; off < 64; off <<= 1) m = fmaxf(m, __shfl_xor(m, off));
-  float l = 0.f, x[kPer] = {};
-#pragma unroll 4
-  for (int i = mine; i < n; i += WAVES) {
-    const int64_t at = part(i);
-    const float2 ml = p.part_ml[at];
-    const float f = __builtin_amdgcn_exp2f(ml.x - m);
-    l += ml.y * f;
-    const float* src = p.part_o + at * D + lane * kPer;
+    for (int u = 0; u < 4; ++u) {
+      const int j = min(j0 + u * kStride, n - 1);
+      const int64_t at = (base + (j == 0 ? note.x : ((note.x >> 1) + j) * 2)) * rows + row;
+      ml[u] = p.part_ml[at];
+      y[u] = reinterpret_cast<const f32x4*>(p.part_o + at * D)[i];
+    }
+    float top = m;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) x[j] += src[j] * f;
+    for (int u = 0; u < 4; ++u) top = fmaxf(top, j0 + u * kStride < n ? ml[u].x : kLowest);
+    const float f = __builtin_amdgcn_exp2f(m - top);
+    m = top;
+    l *= f;
+    x *= f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (j0 + u * kStride < n) {
+        const float g = __builtin_amdgcn_exp2f(ml[u].x - m);
+        l += ml[u].y * g;
+        x += y[u] * g;
+      }
+    }
   }
-  if constexpr (WAVES > 1) {
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) part_x[wave][lane * kPer + j] = x[j];
-    if (lane == 0) part_l[wave] = l;
+  if constexpr (GROUPS > 1) {
+    part_x[group][i] = x;
+    if (i == 0) {
+      part_ml[group][0] = m;
+      part_ml[group][1] = l;
+    }
     __syncthreads();
-    if (wave > 0) return;
-    for (int w = 1; w < WAVES; ++w) {
-      l += part_l[w];
+    if (group > 0) return;
+    float top = kLowest;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) x[j] += part_x[w][lane * kPer + j];
+    for (int w = 0; w < kBlockGroups; ++w) top = fmaxf(top, part_ml[w][0]);
+    m = top;
+    l = 0.f;
+    x = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kBlockGroups; ++w) {
+      const float g = __builtin_amdgcn_exp2f(part_ml[w][0] - m);
+      l += part_ml[w][1] * g;
+      x += part_x[w][i] * g;
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  if constexpr (D == 128)
-    reinterpret_cast<uint32_t*>(p.out + item * D)[lane] = pack_out<F16>(x[0] * inv, x[1] * inv);
-  else
-    p.out[item * D + lane] = (uint16_t)pack_out<F16>(x[0] * inv, 0.f);
-  if (p.lse && lane == 0) p.lse[item] = l == 0.f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
+  reinterpret_cast<u32x2*>(p.out + item * D)[i] =
+      u32x2{pack_out<F16>(x[0] * inv, x[1] * inv), pack_out<F16>(x[2] * inv, x[3] * inv)};
+  if (p.lse && i == 0) p.lse[item] = l == 0.f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
 }
 
 template <int D, bool F16, bool SPARSE>
 hipError_t launch_rt(const AttnParams& p, hipStream_t s) {
-  const uint32_t grid = (uint32_t)((p.workers + 7) / 8 * 8 * p.row_groups * p.kv_heads);
-  if (p.row_tiles == 1)
+  const int members = p.row_groups * (p.kv_heads / p.member_heads);
+  const uint32_t grid = (uint32_t)((p.workers + 7) / 8 * 8 * members);
+  if (p.member_heads > 1)
+    attention_heads_kernel<D, 1, F16, SPARSE><<<grid, kAttnThreads, 0, s>>>(p);
+  else if (p.member_rows == 16)
     attention_kernel<D, 1, F16, SPARSE><<<grid, kAttnThreads, 0, s>>>(p);
-  else
+  else if (p.member_rows == 32)
     attention_kernel<D, 2, F16, SPARSE><<<grid, kAttnThreads, 0, s>>>(p);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.workers == 1) return e;
-  if (p.rows_heads <= 2048)
-    attention_join_kernel<D, F16, 4><<<(uint32_t)p.rows_heads, 256, 0, s>>>(p, SPARSE);
   else
-    attention_join_kernel<D, F16, 1><<<(uint32_t)((p.rows_heads + 3) / 4), 256, 0, s>>>(p, SPARSE);
+    attention_wide_kernel<D, 2, F16, SPARSE><<<grid, kAttnThreads, 0, s>>>(p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !p.join) return e;
+  constexpr int kPer = 256 / (D / 4);
+  // few items: a block each, so that long contexts' many parts are read at once
+  if (p.rows_heads <= 1024)
+    attention_join_kernel<D, F16, kPer><<<(uint32_t)p.rows_heads, 256, 0, s>>>(p, SPARSE);
+  else
+    attention_join_kernel<D, F16, 1><<<(uint32_t)((p.rows_heads + kPer - 1) / kPer), 256, 0, s>>>(p, SPARSE);
   return hipGetLastError();
 }
 

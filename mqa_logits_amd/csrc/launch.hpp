@@ -106,15 +106,17 @@ struct AttnParams {
   int64_t idx_stride;
   uint16_t* out;             // [batch*next_n, Hq, D], q's type
   float* lse;                // [batch*next_n, Hq] or null
-  float* part_o;             // [members, workers, 2, 16 * row_tiles, D]
-  float2* part_ml;           // [members, workers, 2, 16 * row_tiles] maximum (log2), sum
+  float* part_o;             // [members, workers, 2, member_rows, D]
+  float2* part_ml;           // [members, workers, 2, member_rows] maximum (log2), sum
   int2* notes;               // [units] first slot and number of a unit's parts
   int64_t rows_heads;        // batch*next_n * Hq
   int32_t units;             // sequences, or query tokens with indices
   int32_t kv_heads, group;   // Hkv, Hq / Hkv
   int32_t next_n, num_blocks, bs_shift, max_ctx, topk;
   int32_t workers, min_steps;      // workgroups along the keys; fewest 128-key steps of one
-  int32_t row_tiles, row_groups;   // 16-row tiles per workgroup; workgroups along the rows
+  int32_t member_heads;            // KV heads per workgroup (1, or one for each of its waves)
+  int32_t member_rows, row_groups; // rows per workgroup; workgroups along the rows of a head
+  int32_t join;              // some unit may be cut: its parts are joined
   int32_t negate;            // scale < 0: the queries' signs are flipped
   float c2;                  // |scale| * log2(e)
 };
