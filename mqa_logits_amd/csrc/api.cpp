@@ -163,10 +163,10 @@ mqa_status run_dense(mqa_dtype dt, const void* q, const uint8_t* q_sf, const voi
 
 // How paged_attention splits its work.  A unit is a sequence, or a query token
 // when it has indices of its own; its next_n * group (or group) rows of a KV
-// head go to workgroups of member_rows rows, the keys of all units to
-// `workers` workgroups of each (attention.hip, "Work split").
+// head (of member_heads KV heads) go to workgroups of member_rows rows, the keys
+// of all units to `workers` workgroups of each (attention.hip, "Work split").
 struct AttnPlan {
-  int32_t units, member_heads, member_rows, row_groups, workers, min_steps;
+  int32_t units, member_heads, member_rows, row_groups, workers;
   bool join;                 // some unit may be cut
   int64_t steps;             // 128-key steps of a KV head, at most
   int64_t parts, bytes;      // part rows; workspace
@@ -175,33 +175,38 @@ struct AttnPlan {
 AttnPlan plan_attention(int32_t batch, int32_t next_n, int32_t hq, int32_t hkv, int32_t d,
                         int32_t max_context_len, int32_t topk) {
   AttnPlan a{};
-  const int32_t group = hq / hkv;
   a.units = topk ? batch * next_n : batch;
-  const int32_t rows = topk ? group : next_n * group;
+  const int32_t rows = (topk ? 1 : next_n) * (hq / hkv);      // of a unit and KV head
   a.steps = a.units * std::max<int64_t>(((topk ? topk : max_context_len) + 127) / 128, 1);
-  static const int min_steps = std::getenv("AMS") ? atoi(std::getenv("AMS")) : 4, wide_steps = std::getenv("AWS") ? atoi(std::getenv("AWS")) : 12;
-  a.min_steps = min_steps;
   int64_t members = 0;
   const auto split = [&](int32_t member_rows, int32_t member_heads) {
     a.member_rows = member_rows;
     a.member_heads = member_heads;
     a.row_groups = (rows * member_heads + member_rows - 1) / member_rows;
     members = (int64_t)(hkv / member_heads) * a.row_groups;
-    const int64_t want = std::max<int64_t>(mqa::kAttnResident / members, 1);
-    a.workers = (int32_t)std::min(want, std::max<int64_t>(a.steps / a.min_steps, 1));
+    a.workers = (int32_t)std::min<int64_t>(std::max<int64_t>(mqa::kAttnResident / members, 1), a.steps);
   };
-  static const int hd = std::getenv("AHD") ? atoi(std::getenv("AHD")) : 6;
+  // The kernels whose waves have rows of their own leave four times the parts,
+  // so they need pieces long enough to outweigh that.
+  // Over 64 rows, 128 at a time: 64 sequences of 1024..32768 keys, 256 rows, take
+  // 182 us, 221 with 32 rows at a time; 32 of 8192 keys, 128 rows (4 steps a
+  // piece), 45 against 39.
   if (rows > 64) split(128, 1);
-  if (rows <= 64 || a.steps < (int64_t)wide_steps * a.workers) {
+  if (rows <= 64 || a.steps < 12 * (int64_t)a.workers) {
+    // Up to 16 rows, a KV head per wave: 32 sequences of 1024..32768 keys, 8 KV
+    // heads, 139 us against 158; one of 131072 keys, 4 KV heads (2 steps a
+    // piece), 32 against 26.
     if (rows <= 16 && hkv % 4 == 0) split(64, 4);
-    if (rows > 16 || hkv % 4 || a.steps < (int64_t)hd * a.workers) split(rows <= 16 ? 16 : 32, 1);
+    if (rows > 16 || hkv % 4 || a.steps < 6 * (int64_t)a.workers) split(rows <= 16 ? 16 : 32, 1);
   }
-  // units of one size and whole ones a worker: none is cut
-  if (topk && a.workers < a.units && a.workers > 1) {
+  // selected columns are units of one size: whole ones for every worker, where
+  // that divides evenly, leave nothing to join
+  if (topk && a.workers < a.units) {
     const int32_t each = (a.units + a.workers - 1) / a.workers;
     if (a.units % each == 0) a.workers = a.units / each;
   }
-  a.join = a.workers > 1 && !(topk && a.units % a.workers == 0);
+  // (nor do units of a single step)
+  a.join = a.workers > 1 && a.steps > a.units && !(topk && a.units % a.workers == 0);
   a.parts = a.join ? members * a.workers * 2 * a.member_rows : 0;
   a.bytes = a.join ? a.parts * (d + 2) * 4 + (int64_t)a.units * 8 : 0;
   return a;
@@ -628,7 +633,6 @@ mqa_status paged_attention(mqa_dtype dt, const void* q, mqa_float q_type, int64_
   p.max_ctx = max_context_len;
   p.topk = topk;
   p.workers = a.workers;
-  p.min_steps = a.min_steps;
   p.join = a.join;
   p.member_heads = a.member_heads;
   p.member_rows = a.member_rows;

@@ -7,11 +7,18 @@
 // of a sequence and a KV head: all next_n * group of them share the KV head's
 // tokens (with selected columns: the group heads of one query token).
 //
-// One pass over the cache with a running maximum and sum.  A workgroup of four
-// waves takes 16 * RT rows and a chunk of keys; wave w walks the 32-key tiles
-// w, w + 4, ... of the chunk with its own maximum, sum and accumulators, and
-// the four join through LDS at the end.  Both products are computed transposed
-// so that nothing leaves the registers between them:
+// One pass over the cache with a running maximum and sum, 32 keys and 16 * RT
+// rows at a time per wave.  How a workgroup's four waves divide the work gives
+// three kernels:
+//   attention_kernel        16 or 32 rows of a KV head: the waves take the tiles
+//                           in turn, and join their maxima, sums and
+//                           accumulators through LDS at the end;
+//   attention_heads_kernel  16 rows of each of four KV heads, one per wave, over
+//                           the same keys;
+//   attention_wide_kernel   128 rows of a KV head, 32 per wave, over the same
+//                           keys, which each wave converts a quarter of.
+// Both products are computed transposed so that nothing leaves the registers
+// between them:
 //
 //   S^T[key, row] = K Q^T   A = 16 keys x 32 of D, B = 32 of D x 16 rows
 //   O^T[d, row]  += V^T P^T A = 16 of D x 32 keys, B = 32 keys x 16 rows
@@ -34,6 +41,15 @@
 // for the second product (relative 2^-8 at most, the size of the bf16 result's
 // own rounding); with fp16 q it is split into two bf16 parts, because fp16
 // results keep eleven bits.  The sum of p, the maximum and all accumulators are fp32.
+//
+// What bounds it.  With few rows the cache's bytes: (D/2 + D/32) * 2 per key and
+// KV head.  With many the matrix cores and the vector ALU one after the other,
+// which hardly overlap on this chip: 32 keys x 32 rows are 32 products (512
+// cycles) and, with the keys converted by every wave, about 240 vector
+// instructions (1000 cycles).  Measured: 64 x 4 query
+// tokens of 64 heads over 1024..32768 keys 180 us, 0.79 PFLOP/s; 32 sequences of
+// those lengths, 8 KV heads of 8 fp16 rows each, 139 us, 4.1 TB/s; one context of
+// 131072 keys, 4 KV heads, 26 us.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -270,16 +286,25 @@ struct Rows {
 #pragma unroll
     for (int half = 0; half < 2; ++half)
       ks[half] = byte_scale(words[half * 16 + c], g * (D / 4) / 32);
+    u32x4 y[2][kParts][RT];                  // queries of this step and the next
+    const auto fetch = [&](int st) {
+#pragma unroll
+      for (int part = 0; part < kParts; ++part)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) y[st & 1][part][rt] = query(rt, part, st);
+    };
+    fetch(0);
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) {
+      if (st + 1 < kSteps) fetch(st + 1);
+      if (kQueriesInLds) __builtin_amdgcn_sched_barrier(0);
       const u32x4 a = cvt_eight(r.k[0][st], ks[0]), b = cvt_eight(r.k[1][st], ks[1]);
 #pragma unroll
       for (int part = 0; part < kParts; ++part)
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-          const u32x4 y = query(rt, part, st);
-          x.s[rt][0] = mma(a, y, x.s[rt][0]);
-          x.s[rt][1] = mma(b, y, x.s[rt][1]);
+          x.s[rt][0] = mma(a, y[st & 1][part][rt], x.s[rt][0]);
+          x.s[rt][1] = mma(b, y[st & 1][part][rt], x.s[rt][1]);
         }
     }
   }
@@ -288,16 +313,28 @@ struct Rows {
   // as finite.  Others that are NaN spread: K's bytes over kLastScale become
   // the NaN byte, V's mark the rows that see their key and become 0.  first:
   // position of the tile's first key; places: the LDS entries of its keys
-  // (SPARSE).
+  // (SPARSE).  Returns whether some key may be hidden from some row.
   template <bool MASKED, bool SPARSE>
-  __device__ __forceinline__ void check_scales(Raw& r, int first, const uint32_t* places) {
+  __device__ __forceinline__ bool check_scales(Raw& r, int first, const uint32_t* places) {
     const int lane = threadIdx.x & 63;
+    bool hidden = MASKED;
     if constexpr (MASKED) {
       const bool any = SPARSE ? places[lane & 31] != kNoKey : first + (lane & 31) < most;
       r.s = any ? r.s : 0u;
+      if (SPARSE) hidden = !__all(any);
     }
     if (__builtin_expect(__any(has_nan(r.s)), 0))
       spread_nan<MASKED && !SPARSE>(r.s, first);
+    return hidden;
+  }
+
+  // The compiler was seen to read a product's result right behind a branch,
+  // before it is there; ahead of a branch, the products end here.
+  __device__ __forceinline__ static void end_products(Scores& s) {
+    if constexpr (RT == 1)
+      asm volatile("s_nop 7" : "+v"(s.s[0][0]), "+v"(s.s[0][1]));
+    else
+      asm volatile("s_nop 7" : "+v"(s.s[0][0]), "+v"(s.s[0][1]), "+v"(s.s[RT - 1][0]), "+v"(s.s[RT - 1][1]));
   }
 
   template <bool BY_ROW>
@@ -351,10 +388,13 @@ struct Rows {
   template <bool MASKED, bool SPARSE>
   __device__ __forceinline__ void step(Raw& r, int first, const uint32_t* places, float c2) {
     Scores s;
-    check_scales<MASKED, SPARSE>(r, first, places);
+    const bool hidden = check_scales<MASKED, SPARSE>(r, first, places);
     stage(r);
     scores(r, s);
-    if constexpr (MASKED) mask<SPARSE>(s, first, places);
+    if constexpr (MASKED) {
+      end_products(s);
+      if (hidden) mask<SPARSE>(s, first, places);
+    }
     accumulate(s, c2);
     __builtin_amdgcn_wave_barrier();         // the staging is read
   }
@@ -529,17 +569,8 @@ struct Rows {
           s.s[rt][1] = mma(k.a[1][st], q[rt][part][st], s.s[rt][1]);
         }
     if constexpr (kKeysAhead) read_keys(k, next);
-    if constexpr (SPARSE) {
-      mask<SPARSE>(s, first, places);
-    } else {
-      // The compiler was seen to read a product's result right behind a branch,
-      // before it is there; the products end here, ahead of the branch.
-      if constexpr (RT == 1)
-        asm volatile("s_nop 7" : "+v"(s.s[0][0]), "+v"(s.s[0][1]));
-      else
-        asm volatile("s_nop 7" : "+v"(s.s[0][0]), "+v"(s.s[0][1]), "+v"(s.s[RT - 1][0]), "+v"(s.s[RT - 1][1]));
-      if (masked) mask<SPARSE>(s, first, places);
-    }
+    end_products(s);
+    if (masked) mask<SPARSE>(s, first, places);
     // V's operands, kAhead ahead of their products
     const u32x4* vops = ops + kKeyOps * 64 + lane;
     u32x4 a[kAhead];
@@ -581,11 +612,12 @@ __device__ __forceinline__ uint32_t pack_out(float a, float b) {
 // Work split
 // ---------------------------------------------------------------------------
 //
-// A member is a KV head and a group of 16 * RT rows.  For every member the
+// A member is a group of rows of one KV head, or of four.  For every member the
 // units (sequences; with selected columns, query tokens) are laid end to end in
-// steps of 128 keys (one tile per wave; at least one step a unit), and the S
-// steps are cut into equal pieces, one per worker, as many as the chip holds at
-// a time but none below min_steps.  A worker walks its piece unit by unit.  A
+// steps of 128 keys (four tiles; at least one step a unit), and the S steps are
+// cut into equal pieces, one per worker, as many as the chip holds at a time (a
+// worker per chunk of a unit left it idle for 40% of the time on contexts of
+// 1024..32768 keys).  A worker walks its piece unit by unit.  A
 // unit inside one piece is finished there; one cut by piece borders leaves a
 // part in each: worker j writes the part that begins its piece to slot 2j, the
 // one that ends it to slot 2j + 1.  The worker that begins a unit notes the
@@ -596,7 +628,7 @@ struct Split {
   int steps, workers;     // S; workers in use, of p.workers
   int each, more;         // steps per piece; the first `more` pieces have one more
   __device__ __forceinline__ Split(int s, const AttnParams& p) : steps(s) {
-    workers = min(p.workers, max(s / p.min_steps, 1));
+    workers = min(p.workers, s);
     each = s / workers;
     more = s - each * workers;
   }
@@ -621,6 +653,14 @@ __device__ __forceinline__ int block_sum(int x, int* buf) {
   for (int w = 0; w < kWaves; ++w) x += buf[w];
   __syncthreads();
   return x;
+}
+
+// Members of one piece read the same tokens: they follow each other on one XCD.
+// Pieces go round the XCDs; with selected columns each XCD has a run of them,
+// because neighbouring query tokens select many of the same columns.
+template <bool SPARSE>
+__device__ __forceinline__ int worker_of(const AttnParams& p, int xcd, int turn) {
+  return SPARSE ? xcd * ((p.workers + 7) / 8) + turn : turn * 8 + xcd;
 }
 
 // The unit being walked, and what its rows see.
@@ -917,9 +957,8 @@ attention_kernel(const AttnParams p) {
   __shared__ int sums[kWaves], found[2];
 
   const int members = p.row_groups * p.kv_heads;
-  // members of one piece read the same tokens: on one XCD, one after the other
   const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
-  const int worker = idx / members * 8 + xcd, member = idx % members;
+  const int worker = worker_of<SPARSE>(p, xcd, idx / members), member = idx % members;
   const int kv_head = member / p.row_groups, row0 = member % p.row_groups * kRows;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // uniform, so its branches are too
@@ -1122,7 +1161,7 @@ attention_heads_kernel(const AttnParams p) {
 
   const int members = p.row_groups * (p.kv_heads / kWaves);
   const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
-  const int worker = idx / members * 8 + xcd, member = idx % members;
+  const int worker = worker_of<SPARSE>(p, xcd, idx / members), member = idx % members;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int kv_head = member / p.row_groups * kWaves + wave;   // (Hkv is a multiple of four)
@@ -1199,11 +1238,11 @@ attention_wide_kernel(const AttnParams p) {
 
   const int members = p.row_groups * p.kv_heads;
   const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3;
-  const int worker = idx / members * 8 + xcd, member = idx % members;
+  const int worker = worker_of<SPARSE>(p, xcd, idx / members), member = idx % members;
   const int kv_head = member / p.row_groups, row0 = member % p.row_groups * kRows;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int c = lane & 15, g = lane >> 4;
+  const int c = lane & 15;
   const int unit_rows = SPARSE ? p.group : p.next_n * p.group;
   const int wave_row = row0 + wave * 16 * RT;
 
@@ -1270,7 +1309,7 @@ attention_wide_kernel(const AttnParams p) {
               for (int key = 0; key < kTile; ++key)
                 rows.template mark_nan<!SPARSE>(nan_words[w][key], stage + (tile0 + w) * kTile + key);
         }
-        const bool masked = stage + (tile0 + kWaves) * kTile > least;
+        const bool masked = SPARSE || stage + (tile0 + kWaves) * kTile > least;
         typename State::KeyOps k;
         if constexpr (State::kKeysAhead) State::read_keys(k, ops[0]);
 #pragma nounroll

@@ -113,7 +113,7 @@ struct AttnParams {
   int32_t units;             // sequences, or query tokens with indices
   int32_t kv_heads, group;   // Hkv, Hq / Hkv
   int32_t next_n, num_blocks, bs_shift, max_ctx, topk;
-  int32_t workers, min_steps;      // workgroups along the keys; fewest 128-key steps of one
+  int32_t workers;           // workgroups along the keys
   int32_t member_heads;            // KV heads per workgroup (1, or one for each of its waves)
   int32_t member_rows, row_groups; // rows per workgroup; workgroups along the rows of a head
   int32_t join;              // some unit may be cut: its parts are joined
