@@ -350,7 +350,8 @@ mqa_status paged_kv_write(mqa_dtype dt, const void* x, mqa_float x_type, int64_t
  *            [batch*next_n, indices_stride] int32: row r attends to the keys
  *            among its first topk entries that it sees, any other entry (-1)
  *            is passed over; a key listed twice counts twice
- *   scale    finite factor of <q, k>
+ *   scale    finite factor of <q, k>; scores times log2(e) are fp32 and must
+ *            stay within +-2^127
  *   out      [batch*next_n, Hq, D] of q_type; head h reads KV head
  *            h / (Hq / Hkv).  0 for a row without keys.
  *   lse      NULL or [batch*next_n, Hq] fp32: log(sum exp(scale <q, k>)), -inf
@@ -360,10 +361,11 @@ mqa_status paged_kv_write(mqa_dtype dt, const void* x, mqa_float x_type, int64_t
  *            only during the call: calls that may run at the same time need
  *            workspaces of their own.
  * Keys outside a row's range never reach its result, whatever the cache holds
- * there.  Requires D in {64, 128}, Hkv <= 256, Hq a multiple of Hkv and at
- * most 1024, 1 <= batch <= 8192, 1 <= next_n <= 16, block_size in
- * {16, 32, 64}, num_blocks * block_size < 2^31, less than 2^32 blocks of 32
- * elements in a pool (64 GiB of codes), topk <= 2^20.
+ * there.  Outputs and workspace must not overlap anything else.  Requires
+ * D in {64, 128}, Hkv <= 256, Hq a multiple of Hkv and at most 1024,
+ * 1 <= batch <= 8192, 1 <= next_n <= 16, block_size in {16, 32, 64},
+ * max_context_len <= 2^30, num_blocks * block_size < 2^31, less than 2^32
+ * blocks of 32 elements in a pool (64 GiB of codes), topk <= 2^20.
  */
 int64_t paged_attention_workspace_size(int32_t batch, int32_t next_n, int32_t hq, int32_t hkv,
                                        int32_t d, int32_t max_context_len,

@@ -546,7 +546,7 @@ def paged_kv_write(fmt, x, slots, kv_pool, kv_sf_pool=None, kv_scale_pool=None, 
     return values
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=1024)
 def paged_attention_workspace_size(batch, next_n, q_heads, kv_heads, d, max_context_len, topk=0):
     """Bytes of workspace of a paged_attention call of these sizes."""
     n = lib.paged_attention_workspace_size(batch, next_n, q_heads, kv_heads, d, max_context_len,

@@ -73,7 +73,7 @@ constexpr uint32_t kLastScale = 252;
 // The running maximum follows a new one only when that leaves a weight above
 // this; most tiles rescale nothing.
 constexpr float kMostWeight = 256.f;
-constexpr float kLowest = -3.0e38f;          // a maximum before any key
+constexpr float kLowest = -0x1.fffffep127f;  // a maximum before any key (finite: no inf - inf)
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ bf16x8 as_bf16(u32x4 x) { return __builtin_bit_cast(bf16x8, x); }

@@ -277,3 +277,13 @@ def test_units_of_one_step(batch, hq, hkv, topk):
     lens = np.random.default_rng(batch).integers(0, 129, batch)
     assert mq.paged_attention_workspace_size(batch, 1, hq, hkv, 64, 128, topk) == 0
     Case(lens, hq=hq, hkv=hkv, d=64, bs=16, max_ctx=128, topk=topk, seed=batch).check("one step")
+
+
+@pytest.mark.parametrize("hq,hkv,max_ctx", [(8, 4, 65536), (128, 1, 262144), (8, 2, 300)])
+def test_largest_scales(hq, hkv, max_ctx):
+    # a factor whose product with log2(e) is beyond fp32: scores of 0 weigh the same
+    c = Case([300, 0, 40], hq=hq, hkv=hkv, bs=16, max_ctx=max_ctx, seed=6)
+    c.q.zero_()
+    for c.scale in (3.4e38, -3.4e38):
+        out, lse = c.check("largest scale")
+        assert bool(torch.isfinite(out).all())
