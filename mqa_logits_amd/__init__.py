@@ -413,13 +413,17 @@ def paged_mqa_logits(fmt, q, q_sf, kv_pool, kv_sf_pool, kv_scale_pool, weights,
 # first one expression over everything a call takes; only where that fails, the
 # checks one by one, which name what does not fit.
 
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _call(fn, device, *args):
     """fn(*args, stream) on GPU `device` (kernels go to the current device)."""
-    if torch._C._cuda_getDevice() == device:
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    if _current_device() == device:
+        status = fn(*args, _current_stream(device))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+            status = fn(*args, _current_stream(device))
     if status != 0:
         _check(status)
 
@@ -471,18 +475,18 @@ def paged_kv_slots(context_lens, new_lens, free_blocks, block_table, num_blocks,
     if max_tokens < 0 or max_context_len < 0:
         raise ValueError("max_tokens and max_context_len must not be negative")
     batch, dev = context_lens.shape[0], context_lens.get_device()
-    if out is None:
+    i32, given = torch.int32, out is not None
+    if not given:
         out = (context_lens.new_empty(max_tokens, dtype=torch.int64),
-               context_lens.new_empty(batch + 1, dtype=torch.int32),
-               context_lens.new_empty(1, dtype=torch.int32))
+               context_lens.new_empty(batch + 1, dtype=i32), context_lens.new_empty(1, dtype=i32))
     slots, offsets, taken = out
-    i32 = torch.int32
     if not (dev >= 0 and _fits(context_lens, (batch,), i32, dev)
             and _fits(new_lens, (batch,), i32, dev)
             and _fits(free_blocks, (free_blocks.numel(),), i32, dev)
             and _table_fits(block_table, batch, -(-max_context_len // block_size), dev)
-            and _fits(slots, (max_tokens,), torch.int64, dev)
-            and _fits(offsets, (batch + 1,), i32, dev) and _fits(taken, (1,), i32, dev)):
+            and (not given or (_fits(slots, (max_tokens,), torch.int64, dev)
+                               and _fits(offsets, (batch + 1,), i32, dev)
+                               and _fits(taken, (1,), i32, dev)))):
         a = _Args()
         a.want(context_lens, "context_lens", (batch,), I32_T)
         a.want(new_lens, "new_lens", (batch,), I32_T)
@@ -593,13 +597,17 @@ def paged_attention(fmt, q, k_pool, k_sf_pool, v_pool, v_sf_pool, context_lens, 
         topk = indices.shape[1] if indices.dim() == 2 else 0
         if topk < 1:
             raise ValueError("indices must be [rows, topk] with at least one column")
-    if out is None:
+    # (what is made here needs no check)
+    given_out, given_lse, given_workspace = out is not None, lse is not None, workspace is not None
+    if not given_out:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    if lse is None and return_lse:
+    if not given_lse and return_lse:
         lse = q.new_empty((rows, hq), dtype=torch.float32)
     need = paged_attention_workspace_size(batch, next_n, hq, hkv, d, max_context_len, topk)
-    if workspace is None and need:
-        workspace = q.new_empty(need, dtype=torch.uint8)
+    if not given_workspace:
+        workspace, size = (q.new_empty(need, dtype=torch.uint8), need) if need else (None, 0)
+    else:
+        size = workspace.numel()
     codes, scales = (num_blocks, block_size, hkv, d // 2), (num_blocks, block_size, hkv, d // 32)
     byte, i32 = k_pool.dtype, torch.int32
     if not (dev >= 0 and byte.itemsize == 1 and _fits(k_pool, codes, byte, dev)
@@ -609,9 +617,9 @@ def paged_attention(fmt, q, k_pool, k_sf_pool, v_pool, v_sf_pool, context_lens, 
             and _fits(context_lens, (batch,), i32, dev)
             and _table_fits(block_table, batch, -(-max_context_len // block_size), dev)
             and (topk == 0 or _table_fits(indices, rows, topk, dev))
-            and _fits(out, q_shape, q.dtype, dev)
-            and (lse is None or _fits(lse, (rows, hq), torch.float32, dev))
-            and (workspace is None or _fits(workspace, (workspace.numel(),), torch.uint8, dev))):
+            and (not given_out or _fits(out, q_shape, q.dtype, dev))
+            and (not given_lse or _fits(lse, (rows, hq), torch.float32, dev))
+            and (not given_workspace or _fits(workspace, (size,), torch.uint8, dev))):
         a = _Args()
         a.want(q[:0], "q", (0, hq, d))
         for name, pool, sf in (("k", k_pool, k_sf_pool), ("v", v_pool, v_sf_pool)):
@@ -633,6 +641,5 @@ def paged_attention(fmt, q, k_pool, k_sf_pool, v_pool, v_sf_pool, context_lens, 
           _row_stride(block_table, block_table.shape[1]), _data(indices),
           _row_stride(indices, topk) if topk else 0, topk,
           d ** -0.5 if scale is None else float(scale), out.data_ptr(), _data(lse),
-          _data(workspace), workspace.numel() if workspace is not None else 0, batch, next_n, hq,
-          hkv, d, block_size, num_blocks, max_context_len)
+          _data(workspace), size, batch, next_n, hq, hkv, d, block_size, num_blocks, max_context_len)
     return out if lse is None else (out, lse)
