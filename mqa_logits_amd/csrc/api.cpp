@@ -190,12 +190,12 @@ AttnPlan plan_attention(int32_t batch, int32_t next_n, int32_t hq, int32_t hkv, 
   // The kernels whose waves have rows of their own leave four times the parts,
   // so they need pieces long enough to outweigh that.
   // Over 64 rows, 128 at a time: 64 sequences of 1024..32768 keys, 256 rows, take
-  // 182 us, 221 with 32 rows at a time; 32 of 8192 keys, 128 rows (4 steps a
+  // 176 us, 221 with 32 rows at a time; 32 of 8192 keys, 128 rows (4 steps a
   // piece), 45 against 39.
   if (rows > 64) split(128, 1);
   if (rows <= 64 || a.steps < 12 * (int64_t)a.workers) {
     // Up to 16 rows, a KV head per wave: 32 sequences of 1024..32768 keys, 8 KV
-    // heads, 139 us against 158; one of 131072 keys, 4 KV heads (2 steps a
+    // heads, 138 us against 158; one of 131072 keys, 4 KV heads (2 steps a
     // piece), 32 against 26.
     if (rows <= 16 && hkv % 4 == 0) split(64, 4);
     if (rows > 16 || hkv % 4 || a.steps < 6 * (int64_t)a.workers) split(rows <= 16 ? 16 : 32, 1);

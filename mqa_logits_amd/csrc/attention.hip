@@ -47,9 +47,10 @@
 // which hardly overlap on this chip: 32 keys x 32 rows are 32 products (512
 // cycles) and, with the keys converted by every wave, about 240 vector
 // instructions (1000 cycles).  Measured: 64 x 4 query
-// tokens of 64 heads over 1024..32768 keys 180 us, 0.79 PFLOP/s; 32 sequences of
-// those lengths, 8 KV heads of 8 fp16 rows each, 139 us, 4.1 TB/s; one context of
-// 131072 keys, 4 KV heads, 26 us.
+// tokens of 64 heads over 1024..32768 keys 176 us, 0.81 PFLOP/s (matrix cores
+// busy 35% of the time); 32 sequences of those lengths, 8 KV heads of 8 fp16 rows
+// each, 138 us, 4.2 TB/s (busy 23%); one context of 131072 keys, 4 KV heads,
+// 26 us; 2048 selected keys of 64 heads for 256 query tokens 42 us, for one 10.5.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

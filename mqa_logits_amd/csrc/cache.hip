@@ -27,7 +27,9 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 // over both formats' ties, subnormals and scale range).  A thread holds eight
 // elements of one group; a group's maximum goes through 4 (MX) or D/8 (FP8)
 // neighbouring lanes.  Reads and writes are whole 16-byte and 4- or 8-byte
-// pieces of adjacent lanes; the kernel is bound by them.
+// pieces of adjacent lanes; the kernel is bound by them: 32768 rows of 8 heads of
+// 128 bf16 into MXFP4, with their values written back, take 25 us, 6.1 TB/s of
+// 152 MB moved; 256 rows of 128 take the launch (3.5 us).
 
 template <int TYPE>
 __device__ __forceinline__ void load8(const void* p, int64_t at, float (&x)[8]) {
@@ -203,9 +205,10 @@ hipError_t launch_write_dim(int d, int type, const WriteParams& p, hipStream_t s
 // table entries.  Slots in blocks of this step come straight from the free
 // list, slots in older blocks from table entries that no block of this launch
 // writes.  One launch, bound by the latency of its chain: lengths, sums, a
-// binary search in LDS, one id.  A thread takes four slots at a time so that
-// their searches and loads overlap (513 prompts, 480 thousand slots: 12.9 us
-// with eight slots one after the other).
+// binary search in LDS, one id: 5 us for 64 sequences, 7.9 us for 513 prompts of
+// 480 thousand tokens.  A thread takes four slots at a time so that
+// their searches and loads overlap (12.9 us for those prompts with eight slots one
+// after the other).
 
 constexpr int kSlotThreads = 512;
 constexpr int kSlotMaxBatch = 8192;
