@@ -472,8 +472,8 @@ def paged_kv_slots(context_lens, new_lens, free_blocks, block_table, num_blocks,
     blocks_taken int32 [1], which exceeds len(free_blocks) when the list ran
     out); `out` may hold these three."""
     _block_size(block_size)
-    if max_tokens < 0 or max_context_len < 0:
-        raise ValueError("max_tokens and max_context_len must not be negative")
+    if not (0 <= max_tokens < 2 ** 31 and 0 <= max_context_len < 2 ** 31 and 0 < num_blocks < 2 ** 31):
+        raise ValueError("max_tokens, max_context_len and num_blocks must be int32 and not negative")
     batch, dev = context_lens.shape[0], context_lens.get_device()
     i32, given = torch.int32, out is not None
     if not given:
@@ -586,8 +586,8 @@ def paged_attention(fmt, q, k_pool, k_sf_pool, v_pool, v_sf_pool, context_lens, 
     batch = context_lens.shape[0]
     num_blocks, block_size, hkv, _ = k_pool.shape
     _block_size(block_size)
-    if max_context_len < 0:
-        raise ValueError("max_context_len must not be negative")
+    if not 0 <= max_context_len < 2 ** 31:
+        raise ValueError("max_context_len must be int32 and not negative")
     if rows != batch * next_n:
         raise ValueError(f"q must have batch * next_n = {batch * next_n} rows, got {rows}")
     if q_stride[2] != 1 or (hq > 1 and q_stride[1] != d):

@@ -146,3 +146,19 @@ def test_binding_refuses_what_does_not_fit():
     for f in bad:
         with pytest.raises(ValueError):
             f()
+
+
+@pytest.mark.parametrize("change", [dict(max_tokens=2 ** 32), dict(max_context_len=2 ** 32 + 16),
+                                    dict(num_blocks=2 ** 32 + 5), dict(num_blocks=0),
+                                    dict(max_tokens=-1), dict(max_context_len=-1)])
+def test_binding_refuses_sizes_beyond_int32(change):
+    # (they would reach the library cut to their low 32 bits)
+    sizes = dict(num_blocks=9, block_size=16, max_context_len=16, max_tokens=4)
+    sizes.update(change)
+    with pytest.raises(ValueError, match="int32"):
+        mq.paged_kv_slots(i32(2), i32(2), i32(3), i32(2, 4), **sizes)
+    if "max_context_len" in change:
+        q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+        with pytest.raises(ValueError, match="int32"):
+            mq.paged_attention("mxfp4", q, u8(3, 16, 2, 32), u8(3, 16, 2, 2), u8(3, 16, 2, 32),
+                               u8(3, 16, 2, 2), i32(2), i32(2, 4), 1, change["max_context_len"])
