@@ -443,11 +443,13 @@ def _block_size(block_size):
 
 
 def _fits(t, shape, dtype, device):
-    return (t.shape == shape and t.dtype is dtype and t.get_device() == device
+    return (t is not None and t.shape == shape and t.dtype is dtype and t.get_device() == device
             and t.is_contiguous())
 
 
 def _table_fits(t, batch, blocks, device):
+    if t is None:
+        return False
     shape = t.shape
     return (len(shape) == 2 and shape[0] == batch and shape[1] >= blocks
             and t.dtype is torch.int32 and t.get_device() == device
@@ -612,7 +614,7 @@ def paged_attention(fmt, q, k_pool, k_sf_pool, v_pool, v_sf_pool, context_lens, 
     byte, i32 = k_pool.dtype, torch.int32
     if not (dev >= 0 and byte.itemsize == 1 and _fits(k_pool, codes, byte, dev)
             and _fits(v_pool, codes, byte, dev)
-            and k_sf_pool.dtype.itemsize == 1 and _fits(k_sf_pool, scales, k_sf_pool.dtype, dev)
+            and k_sf_pool is not None and k_sf_pool.dtype.itemsize == 1 and _fits(k_sf_pool, scales, k_sf_pool.dtype, dev)
             and _fits(v_sf_pool, scales, k_sf_pool.dtype, dev)
             and _fits(context_lens, (batch,), i32, dev)
             and _table_fits(block_table, batch, -(-max_context_len // block_size), dev)

@@ -162,3 +162,14 @@ def test_binding_refuses_sizes_beyond_int32(change):
         with pytest.raises(ValueError, match="int32"):
             mq.paged_attention("mxfp4", q, u8(3, 16, 2, 32), u8(3, 16, 2, 2), u8(3, 16, 2, 32),
                                u8(3, 16, 2, 2), i32(2), i32(2, 4), 1, change["max_context_len"])
+
+
+@pytest.mark.parametrize("at,name", [(3, "k_sf_pool"), (4, "v_pool"), (5, "v_sf_pool"), (7, "block_table")])
+def test_binding_names_what_is_missing(at, name):
+    args = ["mxfp4", torch.zeros(2, 4, 64, dtype=torch.bfloat16), u8(3, 16, 2, 32), u8(3, 16, 2, 2),
+            u8(3, 16, 2, 32), u8(3, 16, 2, 2), i32(2), i32(2, 4), 1, 16]
+    args[at] = None
+    with pytest.raises(ValueError, match=name + " is required"):
+        mq.paged_attention(*args)
+    with pytest.raises(ValueError, match="slots is required"):
+        mq.paged_kv_write("mxfp4", torch.zeros(2, 2, 64), None, u8(3, 16, 2, 32), u8(3, 16, 2, 2))
