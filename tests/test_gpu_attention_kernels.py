@@ -19,6 +19,7 @@ pytestmark = pytest.mark.gpu
 # hq, hkv, next_n that make a kernel of a long bound
 HEADS = [(8, 4, 1), (64, 8, 1), (8, 8, 3), (32, 4, 2), (12, 12, 16)]
 WIDE = [(65, 1, 1), (128, 1, 1), (64, 1, 2), (64, 1, 4), (200, 2, 1), (40, 2, 16)]
+TWO_GROUPS = [(33, 1, 1), (64, 1, 1), (16, 1, 4), (80, 2, 1), (4, 1, 12)]    # of 32 rows
 LENGTHS = [0, 1, 15, 16, 17, 31, 33, 47, 48, 63, 64, 65, 95, 97, 127, 128, 129, 143, 160, 161, 255,
            256, 257, 300, 511, 513]
 
@@ -40,13 +41,13 @@ def test_a_head_per_wave(hq, hkv, next_n, d, dtype, bs):
 
 @pytest.mark.parametrize("d,dtype,bs", [(128, "bf16", 16), (64, "fp16", 32), (128, "fp16", 64),
                                         (64, "bf16", 16)])
-@pytest.mark.parametrize("hq,hkv,next_n", WIDE)
+@pytest.mark.parametrize("hq,hkv,next_n", WIDE + TWO_GROUPS)
 def test_many_rows(hq, hkv, next_n, d, dtype, bs):
     Case(LENGTHS[::2], next_n=next_n, hq=hq, hkv=hkv, d=d, bs=bs, dtype=dtype, max_ctx=262144,
          seed=hq + d).check("wide")
 
 
-@pytest.mark.parametrize("hq,hkv,next_n", [(8, 4, 2), (64, 1, 2), (20, 2, 3), (6, 2, 1)])
+@pytest.mark.parametrize("hq,hkv,next_n", [(8, 4, 2), (64, 1, 2), (20, 2, 3), (6, 2, 1), (64, 1, 1)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_contexts_longer_than_a_stage(hq, hkv, next_n, dtype):
     # more keys than a workgroup holds places for at a time
@@ -56,7 +57,7 @@ def test_contexts_longer_than_a_stage(hq, hkv, next_n, dtype):
 
 
 @pytest.mark.parametrize("batch", [63, 64, 65, 256, 257, 700])
-@pytest.mark.parametrize("hq,hkv,next_n", [(2, 1, 1), (4, 4, 1), (33, 1, 2)])
+@pytest.mark.parametrize("hq,hkv,next_n", [(2, 1, 1), (4, 4, 1), (33, 1, 2), (33, 1, 1)])
 def test_batches(batch, hq, hkv, next_n):
     # the search for a worker's first sequence: up to 64 at once, or 256 by 256
     lens = np.random.default_rng(batch).integers(0, 200, batch)
@@ -81,7 +82,7 @@ def wide_selection(c, topk, seed):
     return c
 
 
-@pytest.mark.parametrize("hq,hkv,topk", [(64, 64, 3000), (8, 4, 8000), (130, 1, 70000)])
+@pytest.mark.parametrize("hq,hkv,topk", [(64, 64, 3000), (8, 4, 8000), (130, 1, 70000), (50, 1, 70000)])
 @pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "fp16")])
 def test_selected_keys_of_each_kernel(hq, hkv, topk, d, dtype):
     rng = np.random.default_rng(hq)
@@ -96,7 +97,8 @@ def test_selected_keys_whole_units(rows):
     Case([500] * rows, next_n=1, hq=40, hkv=1, d=64, bs=64, topk=200, seed=rows).check("units")
 
 
-@pytest.mark.parametrize("hq,hkv,next_n,max_ctx", [(8, 4, 4, 65536), (64, 1, 4, 262144), (6, 2, 4, 600)])
+@pytest.mark.parametrize("hq,hkv,next_n,max_ctx", [(8, 4, 4, 65536), (64, 1, 4, 262144), (6, 2, 4, 600),
+                                                    (14, 1, 4, 262144)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_nan_in_each_kernel(hq, hkv, next_n, max_ctx, d):
     # NaN scales of K and of V in the middle of contexts, at tile and step
@@ -112,7 +114,7 @@ def test_nan_in_each_kernel(hq, hkv, next_n, max_ctx, d):
         assert bool(torch.isnan(out).any()) and bool(torch.isfinite(out).any())
 
 
-@pytest.mark.parametrize("hq,hkv,max_ctx", [(8, 4, 65536), (128, 1, 262144), (8, 2, 3000)])
+@pytest.mark.parametrize("hq,hkv,max_ctx", [(8, 4, 65536), (128, 1, 262144), (8, 2, 3000), (64, 1, 262144)])
 def test_late_maxima_in_each_kernel(hq, hkv, max_ctx):
     # keys that grow along the context: the running maximum is left behind again
     # and again, by far
@@ -126,14 +128,14 @@ def test_late_maxima_in_each_kernel(hq, hkv, max_ctx):
 
 def test_every_tile_count_of_each_kernel():
     # one sequence of n tiles and a bit, n = 0 .. 17, joined with a neighbour
-    for hq, hkv, max_ctx in ((4, 4, 65536), (70, 1, 262144), (3, 1, 700)):
+    for hq, hkv, max_ctx in ((4, 4, 65536), (70, 1, 262144), (3, 1, 700), (25, 1, 524288)):
         for n in range(18):
             Case([32 * n + 5, 70], next_n=2, hq=hq, hkv=hkv, d=64, bs=32, max_ctx=max_ctx,
                  seed=n).check("tiles")
 
 
 @pytest.mark.parametrize("hq,hkv,next_n,max_ctx,topk", [
-    (64, 8, 1, 65536, 0), (64, 1, 4, 262144, 0), (32, 4, 1, 4000, 0), (64, 1, 1, 4000, 600)])
+    (64, 8, 1, 65536, 0), (64, 1, 4, 262144, 0), (64, 1, 1, 524288, 0), (32, 4, 1, 4000, 0), (64, 1, 1, 4000, 600)])
 def test_graph_replays_over_growing_contexts(hq, hkv, next_n, max_ctx, topk):
     # lengths, queries and indices change between the replays of one graph
     import mqa_logits_amd as mq
@@ -199,7 +201,7 @@ def test_two_graphs_with_their_own_workspaces():
 def test_outputs_hold_nothing_but_their_rows():
     # guard rows behind the output, lse and indices; a q view inside wider rows
     import mqa_logits_amd as mq
-    for hq, hkv, max_ctx in ((8, 4, 65536), (128, 1, 262144), (10, 2, 300)):
+    for hq, hkv, max_ctx in ((8, 4, 65536), (128, 1, 262144), (10, 2, 300), (60, 1, 524288)):
         c = Case([300, 17], hq=hq, hkv=hkv, bs=16, max_ctx=max_ctx, seed=4)
         out = torch.full((4, hq, 128), 3.0, dtype=torch.bfloat16, device="cuda")
         lse = torch.full((4, hq), 3.0, device="cuda")
@@ -279,7 +281,7 @@ def test_units_of_one_step(batch, hq, hkv, topk):
     Case(lens, hq=hq, hkv=hkv, d=64, bs=16, max_ctx=128, topk=topk, seed=batch).check("one step")
 
 
-@pytest.mark.parametrize("hq,hkv,max_ctx", [(8, 4, 65536), (128, 1, 262144), (8, 2, 300)])
+@pytest.mark.parametrize("hq,hkv,max_ctx", [(8, 4, 65536), (128, 1, 262144), (8, 2, 300), (64, 1, 524288)])
 def test_largest_scales(hq, hkv, max_ctx):
     # a factor whose product with log2(e) is beyond fp32: scores of 0 weigh the same
     c = Case([300, 0, 40], hq=hq, hkv=hkv, bs=16, max_ctx=max_ctx, seed=6)
