@@ -37,20 +37,23 @@
 // (packed pair, scale applied) loses nothing; V's pairs (two elements of a key)
 // become operand pairs (two keys of an element) with one byte permute each.
 //
-// q is bf16, or fp16 split exactly into two bf16 parts.  p is rounded to bf16
-// for the second product (relative 2^-8 at most, the size of the bf16 result's
-// own rounding); with fp16 q it is split into two bf16 parts, because fp16
-// results keep eleven bits.  The sum of p, the maximum and all accumulators are fp32.
+// q is bf16, or fp16 split exactly into two bf16 parts.  p is split into two bf16
+// parts for the second product (2^-16 left), for either type of result: one part
+// would round every weight by up to 2^-8 while the sum they are divided by keeps
+// all bits, and with weights of one size that does not average out (values that
+// are all 1 gave 0.996).  The second part costs bf16 calls that the matrix cores
+// bound 15 to 23% (64 x 4 query tokens of 64 heads: 221 us, 180 with one) and
+// others up to 6%.  The sum of p, the maximum and all accumulators are fp32.
 //
 // What bounds it.  With few rows the cache's bytes: (D/2 + D/32) * 2 per key and
 // KV head.  With many the matrix cores and the vector ALU one after the other,
-// which hardly overlap on this chip: 32 keys x 32 rows are 32 products (512
+// which hardly overlap on this chip: 32 keys x 32 rows are 48 products (768
 // cycles) and, with the keys converted by every wave, about 240 vector
 // instructions (1000 cycles).  Measured: 64 x 4 query
-// tokens of 64 heads over 1024..32768 keys 176 us, 0.81 PFLOP/s (matrix cores
-// busy 35% of the time); 32 sequences of those lengths, 8 KV heads of 8 fp16 rows
-// each, 138 us, 4.2 TB/s (busy 23%); one context of 131072 keys, 4 KV heads,
-// 26 us; 2048 selected keys of 64 heads for 256 query tokens 42 us, for one 10.5.
+// tokens of 64 heads over 1024..32768 keys 221 us, 0.64 PFLOP/s; 32 sequences of
+// those lengths, 8 KV heads of 8 fp16 rows each, 138 us, 4.2 TB/s; one context of
+// 131072 keys, 4 KV heads, 28 us; 2048 selected keys of 64 heads for 256 query
+// tokens 48 us, for one 10.6.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -225,7 +228,8 @@ template <int D, int RT, bool F16, bool QUERIES_IN_LDS>
 struct Rows {
   static constexpr int kSteps = D / 32;      // products along D
   static constexpr int kCols = D / 16;       // 16-element column groups of V
-  static constexpr int kParts = F16 ? 2 : 1;
+  static constexpr int kParts = F16 ? 2 : 1;  // bf16 parts of a query
+  static constexpr int kWeightParts = 2;     // and of a weight
   // the pitch of V's rows keeps both the 16-byte writes and the 4-byte reads
   // free of bank conflicts
   static constexpr int kPitch = D == 128 ? 80 : 40;
@@ -403,7 +407,7 @@ struct Rows {
   // Weights of one row tile from its scores, packed for the second product.
   // Whether a maximum was left behind shows in the weights themselves; then
   // they are formed again.
-  __device__ __forceinline__ void weights(const f32x4 (&x)[2], int rt, float c2, u32x4 (&p)[kParts]) {
+  __device__ __forceinline__ void weights(const f32x4 (&x)[2], int rt, float c2, u32x4 (&p)[kWeightParts]) {
     float w[8];
     const auto form = [&] {
 #pragma unroll
@@ -432,8 +436,7 @@ struct Rows {
     for (int i = 0; i < 4; ++i) {
       const uint32_t hi = pack_bf16(w[2 * i], w[2 * i + 1]);
       p[0][i] = hi;
-      if constexpr (F16)
-        p[1][i] = pack_bf16(w[2 * i] - bf16_lo(hi), w[2 * i + 1] - bf16_hi(hi));
+      p[1][i] = pack_bf16(w[2 * i] - bf16_lo(hi), w[2 * i + 1] - bf16_hi(hi));
     }
   }
 
@@ -473,7 +476,7 @@ struct Rows {
     uint32_t v[8];
     float vs[8];
     read_values(v, vs);
-    u32x4 p[RT][kParts];
+    u32x4 p[RT][kWeightParts];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) weights(x.s[rt], rt, c2, p[rt]);
     // in turn: interleaved, their operands would not fit the registers
@@ -491,11 +494,11 @@ struct Rows {
 
   template <int SEL>
   __device__ __forceinline__ void add_values(const uint32_t (&v)[8], const float (&vs)[8],
-                                             const u32x4 (&p)[RT][kParts]) {
+                                             const u32x4 (&p)[RT][kWeightParts]) {
     u32x4 even, odd;
     value_operands<SEL>(v, vs, even, odd);
 #pragma unroll
-    for (int part = 0; part < kParts; ++part)
+    for (int part = 0; part < kWeightParts; ++part)
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         o[rt][2 * SEL] = mma(even, p[rt][part], o[rt][2 * SEL]);
@@ -578,13 +581,13 @@ struct Rows {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) a[j] = vops[j * 64];
     __builtin_amdgcn_sched_barrier(0);
-    u32x4 p[RT][kParts];
+    u32x4 p[RT][kWeightParts];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) weights(s.s[rt], rt, c2, p[rt]);
 #pragma unroll
     for (int j = 0; j < kCols; ++j) {
 #pragma unroll
-      for (int part = 0; part < kParts; ++part)
+      for (int part = 0; part < kWeightParts; ++part)
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) o[rt][j] = mma(a[j % kAhead], p[rt][part], o[rt][j]);
       if (j + kAhead < kCols) {

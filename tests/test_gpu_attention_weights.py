@@ -1,0 +1,76 @@
+"""GPU tests of attention's weights: how exactly they enter the result.
+
+One element of a key decides its score, the first step's keys (the first tile of
+every wave, whichever kernel runs) score 0 and the rest `gap` octaves more, with
+gaps up to 8: the running maximum stays behind, so the weights of most keys are
+not near 1 and none of them is a power of two.  With values that are all alike
+the result is that value, whatever the scores' rounding, for the same weights
+stand above and below the fraction: what remains is the weights' own rounding
+(two bf16 parts: 2^-16) and fp32 sums of at most 700 terms, 2^-15 together.
+The results are rounded to nearest, and the nearest border lies 2^-9 (bf16) or
+2^-12 (fp16) away: they have to be the value itself.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BATCH = 1100        # so many that a workgroup's piece holds whole sequences
+# hq, hkv, next_n, max_context_len, topk (0: whole contexts): each kernel
+KERNELS = [(8, 1, 1, 512, 0), (30, 1, 1, 512, 0), (7, 3, 2, 512, 0), (128, 1, 1, 65536, 0), (40, 1, 4, 65536, 0),
+           (16, 4, 1, 65536, 0), (16, 8, 3, 8192, 0), (8, 1, 1, 512, 512), (64, 1, 1, 512, 512),
+           (8, 4, 1, 512, 1024), (130, 1, 1, 512, 1024)]
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import mqa_logits_amd  # noqa: F401
+
+
+def alike(hq, hkv, next_n, max_ctx, topk, d, dtype, code, byte, batch=BATCH, keys=400, low=128):
+    """(arguments, gaps [rows, hq], keys that a row sees, of which `low` score 0)."""
+    bs = 64
+    q_heads = hq // hkv * hkv
+    per = -(-keys // bs)
+    rng = np.random.default_rng(hq * 7 + d)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    k = torch.zeros(batch * per, bs, hkv, d // 2, dtype=torch.uint8, device="cuda")
+    k.view(batch, per * bs, hkv, d // 2)[:, low:, :, 0] = 0x02           # element 0 is 1
+    sf = torch.full((batch * per, bs, hkv, d // 32), 127, dtype=torch.uint8, device="cuda")
+    v, vs = torch.full_like(k, code * 17), torch.full_like(sf, byte)
+    table = torch.zeros(batch, max(per, -(-max_ctx // bs)), **i32)
+    table[:, :per] = torch.arange(batch * per, **i32).view(batch, per)
+    gaps = torch.from_numpy(rng.uniform(0.05, 7.99, (batch * next_n, q_heads))).to(dtype)
+    q = torch.zeros(batch * next_n, q_heads, d, dtype=dtype)
+    q[:, :, 0] = gaps
+    seen = keys - next_n + 1 + torch.arange(next_n).repeat(batch)
+    indices = None
+    if topk:
+        indices = torch.full((batch * next_n, topk), -1, **i32)
+        indices[:, :keys] = torch.arange(keys, **i32)
+    args = ("mxfp4", q.cuda(), k, sf, v, vs, torch.full((batch,), keys, **i32), table, next_n, max_ctx)
+    return args, dict(scale=math.log(2.0), indices=indices, return_lse=True), gaps.double(), seen, low
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv,next_n,max_ctx,topk", KERNELS)
+def test_values_all_alike(hq, hkv, next_n, max_ctx, topk, d, dtype):
+    import mqa_logits_amd as mq
+    print(f"[weights] {hq}/{hkv} next_n={next_n} max_ctx={max_ctx} topk={topk} D={d} {dtype}", flush=True)
+    args, kw, gaps, seen, low = alike(hq, hkv, next_n, max_ctx, topk, d, dtype, code=2, byte=127)
+    out, lse = mq.paged_attention(*args, **kw)
+    torch.cuda.synchronize()
+    off = (out.float() - 1).abs().max()
+    print(f"   largest difference {float(off):.3g}", flush=True)
+    assert bool((out == 1).all())
+    # lse: scores of up to 8 octaves rounded to fp32 a few times (2^-20), a sum of up to 700 terms
+    ref = torch.log(low + (seen[:, None] - low) * torch.exp2(gaps))
+    assert float((lse.double().cpu() - ref).abs().max()) <= 2.0 ** -16
