@@ -342,7 +342,8 @@ mqa_status paged_kv_write(mqa_dtype dt, const void* x, mqa_float x_type, int64_t
  *            q_stride elements from row to row (a multiple of 8, >= Hq * D)
  *   k_pool, v_pool [num_blocks, block_size, Hkv, D/2] packed e2m1
  *   k_sf_pool, v_sf_pool [num_blocks, block_size, Hkv, D/32] e8m0; bytes over
- *            252 (products beyond fp32) count as NaN
+ *            252 (products beyond fp32) count as NaN.  The sum of a row's values
+ *            is held in fp32: n keys times the largest |v| must stay below 2^128
  *   context_lens, block_table, max_context_len: as paged_mqa_logits; row
  *            b*next_n + t sees keys
  *            [0, clamp(ctx_b - next_n + t + 1, 0, min(ctx_b, max_context_len)))

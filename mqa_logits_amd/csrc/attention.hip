@@ -74,9 +74,13 @@ constexpr int kAttnThreads = 64 * kWaves;   // two workgroups per compute unit, 
 constexpr int kTile = 32;                    // keys per wave and step
 // Scale bytes above this could overflow fp32 (6 * 2^126): they count as NaN.
 constexpr uint32_t kLastScale = 252;
-// The running maximum follows a new one only when that leaves a weight above
-// this; most tiles rescale nothing.
-constexpr float kMostWeight = 256.f;
+// The running maximum is set this many octaves above the largest score, and
+// follows a new one only when that leaves a weight above 1; most tiles rescale
+// nothing.  With weights of at most 1 the unnormalised sums of n keys stay within n
+// times the largest value (set to the largest score itself and left 8 octaves
+// behind, they overflowed fp32 for averages far inside it).
+constexpr float kRoom = 8.f;
+constexpr float kMostWeight = 1.f;
 constexpr float kLowest = -0x1.fffffep127f;  // a maximum before any key (finite: no inf - inf)
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -421,7 +425,7 @@ struct Rows {
       asm volatile("");                      // rare: nothing of it belongs before the branch
       const float best = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])),
                                fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3]))) * c2;
-      const float next = fmaxf(m[rt], row_max(best));
+      const float next = fmaxf(m[rt], row_max(best) + kRoom);
       const float f = __builtin_amdgcn_exp2f(m[rt] - next);
       m[rt] = next;
       l[rt] *= f;

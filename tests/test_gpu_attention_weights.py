@@ -17,6 +17,8 @@ import numpy as np
 import pytest
 import torch
 
+from tests.test_gpu_attention import Case
+
 pytestmark = pytest.mark.gpu
 
 BATCH = 1100        # so many that a workgroup's piece holds whole sequences
@@ -74,3 +76,36 @@ def test_values_all_alike(hq, hkv, next_n, max_ctx, topk, d, dtype):
     # lse: scores of up to 8 octaves rounded to fp32 a few times (2^-20), a sum of up to 700 terms
     ref = torch.log(low + (seen[:, None] - low) * torch.exp2(gaps))
     assert float((lse.double().cpu() - ref).abs().max()) <= 2.0 ** -16
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv,next_n,max_ctx,topk", KERNELS)
+def test_large_values_all_alike(hq, hkv, next_n, max_ctx, topk, d):
+    # 400 keys of 6 * 2^116: their sum is 0.59 * 2^128, inside fp32 as the
+    # fraction's own terms are, however far the maximum stays behind
+    import mqa_logits_amd as mq
+    print(f"[large] {hq}/{hkv} next_n={next_n} max_ctx={max_ctx} topk={topk} D={d}", flush=True)
+    args, kw, *_ = alike(hq, hkv, next_n, max_ctx, topk, d, torch.bfloat16, code=7, byte=243)
+    out, lse = mq.paged_attention(*args, **kw)
+    torch.cuda.synchronize()
+    assert bool((out == 6 * 2.0 ** 116).all()) and bool(torch.isfinite(lse).all())
+
+
+@pytest.mark.parametrize("hq,hkv,max_ctx", [(8, 1, 700), (30, 1, 700), (128, 1, 262144), (16, 4, 65536)])
+@pytest.mark.parametrize("q_size", [0.1, 3.0])
+def test_large_values_of_either_sign(hq, hkv, max_ctx, q_size):
+    # up to 700 keys of up to 6 * 2^115
+    c = Case([300, 0, 1, 700], next_n=1, hq=hq, hkv=hkv, bs=16, max_ctx=max_ctx, q_size=q_size, seed=hq)
+    c.vs = np.where(c.vs < 253, c.vs + 112, c.vs).astype(np.uint8)      # 237 .. 241
+    out, _ = c.check("large values")
+    assert bool(torch.isfinite(out).all()) and float(out.abs().max()) > 2.0 ** 110
+
+
+@pytest.mark.parametrize("hq,hkv,max_ctx", [(8, 1, 16), (30, 1, 16), (128, 1, 262144), (16, 4, 65536), (8, 2, 4096)])
+def test_one_key_of_the_largest_scale(hq, hkv, max_ctx):
+    # byte 252: up to 6 * 2^125, which the key alone has to give back exactly
+    c = Case([1, 1], next_n=1, hq=hq, hkv=hkv, bs=16, max_ctx=max_ctx, seed=hq)
+    c.vs = np.where(c.vs < 253, 252, c.vs).astype(np.uint8)
+    out, _ = c.run()
+    ref, *_ = c.reference()
+    assert np.array_equal(out.double().cpu().numpy(), ref) and np.abs(ref).max() == 1.5 * 2.0 ** 127
