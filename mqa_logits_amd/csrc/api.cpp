@@ -639,9 +639,11 @@ mqa_status paged_attention(mqa_dtype dt, const void* q, mqa_float q_type, int64_
   p.member_rows = a.member_rows;
   p.row_groups = a.row_groups;
   p.negate = scale < 0.f;
-  // positive and finite: a masked score (-inf) or one of 0 stays out of NaN
-  p.c2 = std::clamp((scale < 0.f ? -scale : scale) * 1.4426950408889634f, 0x1p-126f,
-                    std::numeric_limits<float>::max());
+  // positive and finite: a masked score (-inf) or one of 0 stays out of NaN.  (The
+  // least subnormal stands for 0: it leaves any finite <q, k> a score under 2^-20;
+  // the kernels keep subnormals.)
+  p.c2 = std::clamp((scale < 0.f ? -scale : scale) * 1.4426950408889634f,
+                    std::numeric_limits<float>::denorm_min(), std::numeric_limits<float>::max());
   if (debug_enabled())
     fprintf(stderr, "[mqa_logits] %s Hq=%d Hkv=%d D=%d batch=%d next_n=%d bs=%d topk=%d workers=%d rows=%d x %d\n",
             who, hq, hkv, d, batch, next_n, block_size, topk, a.workers, a.member_rows, a.row_groups);

@@ -109,3 +109,25 @@ def test_one_key_of_the_largest_scale(hq, hkv, max_ctx):
     out, _ = c.run()
     ref, *_ = c.reference()
     assert np.array_equal(out.double().cpu().numpy(), ref) and np.abs(ref).max() == 1.5 * 2.0 ** 127
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-44, 1e-40, -1e-40, 4e-39, -2e-38])
+@pytest.mark.parametrize("hq,hkv,next_n,max_ctx,topk", KERNELS)
+def test_factors_near_zero(hq, hkv, next_n, max_ctx, topk, scale):
+    # <q, k> is 2^126 for the later keys and 0 for the others: scores of at most
+    # 2.5 octaves, and none under a factor of 0
+    import mqa_logits_amd as mq
+    print(f"[factor] {scale} {hq}/{hkv} next_n={next_n} max_ctx={max_ctx} topk={topk}", flush=True)
+    args, kw, _, seen, low = alike(hq, hkv, next_n, max_ctx, topk, 64, torch.bfloat16, code=4, byte=127)
+    q, sf, v = args[1], args[3], args[4]
+    q[:, :, 0] = 2.0 ** 63
+    sf.fill_(127 + 63)
+    v.view(BATCH, -1, hkv, 32)[:, :low] = 0x22                       # 1 instead of 2
+    kw["scale"] = scale
+    out, lse = mq.paged_attention(*args, **kw)
+    torch.cuda.synchronize()
+    r, late = math.exp(float(np.float32(scale)) * 2.0 ** 126), (seen - low).double()[:, None]
+    ref = (low + 2 * late * r) / (low + late * r)
+    # the result's rounding; a factor below 2^-126 times log2(e) is rounded by 2^-150, 2^-24 of a score
+    assert float((out.double().cpu() - ref[..., None]).abs().max()) <= 2 * 2.0 ** -8 + 2.0 ** -14
+    assert float((lse.double().cpu() - torch.log(low + late * r)).abs().max()) <= 2.0 ** -16
