@@ -239,11 +239,16 @@ __device__ __forceinline__ void find_rows(const int32_t* start, int n, const int
   }
 }
 
+// Blocks of n tokens (n + block_size may pass int32).
+__device__ __forceinline__ int blocks_of(int n, int shift) {
+  return (n >> shift) + ((n & ((1 << shift) - 1)) != 0);
+}
+
 __global__ void __launch_bounds__(kSlotThreads) kv_slots_kernel(const SlotParams p) {
   __shared__ SlotSums sums;
   __shared__ int32_t wave_tok[kSlotThreads / 64], wave_blk[kSlotThreads / 64];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const int round_up = (1 << p.bs_shift) - 1;
+  const int in_block = (1 << p.bs_shift) - 1;
   int tok_base = 0, blk_base = 0;
   for (int b0 = 0; b0 < p.batch; b0 += kSlotThreads) {
     const int b = b0 + t;
@@ -252,7 +257,7 @@ __global__ void __launch_bounds__(kSlotThreads) kv_slots_kernel(const SlotParams
       const int len = min(max(p.ctx[b], 0), p.max_ctx);
       tok = min(max(p.new_lens[b], 0), len);
       old = len - tok;
-      blk = ((len + round_up) >> p.bs_shift) - ((old + round_up) >> p.bs_shift);
+      blk = blocks_of(len, p.bs_shift) - blocks_of(old, p.bs_shift);
     }
     int st = tok, sb = blk;                    // inclusive scans
 #pragma unroll
@@ -309,12 +314,12 @@ __global__ void __launch_bounds__(kSlotThreads) kv_slots_kernel(const SlotParams
       slot[u] = -1;
       if (k0 + u * n_threads < tok_base) {
         const int old = sums.old[b[u]], pos = old + (k[u] - sums.token[b[u]]);
-        const int first = (old + round_up) >> p.bs_shift, j = pos >> p.bs_shift;
+        const int first = blocks_of(old, p.bs_shift), j = pos >> p.bs_shift;
         const int at = sums.block[b[u]] + j - first;
         const int32_t* src = j < first ? p.bt + b[u] * p.bt_stride + j
                              : at < p.num_free ? p.free_ids + at : nullptr;
         const int id = src ? *src : -1;
-        if (id >= 0 && id < p.num_blocks) slot[u] = ((int64_t)id << p.bs_shift) + (pos & round_up);
+        if (id >= 0 && id < p.num_blocks) slot[u] = ((int64_t)id << p.bs_shift) + (pos & in_block);
       }
     }
 #pragma unroll
@@ -326,7 +331,7 @@ __global__ void __launch_bounds__(kSlotThreads) kv_slots_kernel(const SlotParams
     const int want[1] = {(int)k};
     int b[1];
     find_rows(sums.block, p.batch, want, b);
-    const int first = (sums.old[b[0]] + round_up) >> p.bs_shift;
+    const int first = blocks_of(sums.old[b[0]], p.bs_shift);
     p.bt[b[0] * p.bt_stride + first + ((int)k - sums.block[b[0]])] = k < p.num_free ? p.free_ids[k] : -1;
   }
 }
