@@ -324,7 +324,8 @@ mqa_status paged_kv_slots(const int32_t* context_lens, const int32_t* new_lens,
  * power-of-two scale under which none exceeds the largest code (448 or 6), at
  * least 2^-127 (FP8: 2^-126), and 1 for zeros; codes are the elements over the
  * scale rounded to nearest, ties to even.  A group that holds an infinity or
- * NaN gets code 0 and a NaN scale (e8m0: 255).
+ * NaN gets code 0 and a NaN scale (e8m0: 255).  An MXFP4 group with a magnitude
+ * over 1.5 * 2^127 gets e8m0 253, which paged_attention counts as NaN too.
  */
 mqa_status paged_kv_write(mqa_dtype dt, const void* x, mqa_float x_type, int64_t x_stride,
                           int64_t x_head_stride, const int64_t* slots, uint8_t* pool,

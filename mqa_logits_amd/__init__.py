@@ -510,7 +510,8 @@ def paged_kv_write(fmt, x, slots, kv_pool, kv_sf_pool=None, kv_scale_pool=None, 
     heads may be strided) and store them at `slots` (int64 [n]; outside the
     pool: not stored) of kv_pool [num_blocks, block_size(, heads), D or D/2]
     with kv_sf_pool [.., D/32] (MX formats) or kv_scale_pool (fp8).  Slots that
-    are stored must differ.  values (x's shape and type, contiguous) receives
+    are stored must differ.  (paged_attention counts mxfp4 groups with a magnitude
+    over 1.5 * 2 ** 127 as NaN.)  values (x's shape and type, contiguous) receives
     what the codes stand for."""
     code = _fmt(fmt)
     shape = x.shape
