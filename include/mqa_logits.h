@@ -355,9 +355,10 @@ mqa_status paged_kv_write(mqa_dtype dt, const void* x, mqa_float x_type, int64_t
  *   scale    finite factor of <q, k>; <q, k> and the scores times log2(e) are
  *            fp32 and must stay within +-2^127
  *   out      [batch*next_n, Hq, D] of q_type; head h reads KV head
- *            h / (Hq / Hkv).  0 for a row without keys.
+ *            h / (Hq / Hkv).  0 for a row without keys, or without a score
+ *            over -inf
  *   lse      NULL or [batch*next_n, Hq] fp32: log(sum exp(scale <q, k>)), -inf
- *            for a row without keys
+ *            for such a row
  *   workspace of at least paged_attention_workspace_size bytes for the same
  *            sizes (NULL if that is 0), 16-byte aligned.  Its contents matter
  *            only during the call: calls that may run at the same time need

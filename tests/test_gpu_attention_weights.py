@@ -131,3 +131,40 @@ def test_factors_near_zero(hq, hkv, next_n, max_ctx, topk, scale):
     # the result's rounding; a factor below 2^-126 times log2(e) is rounded by 2^-150, 2^-24 of a score
     assert float((out.double().cpu() - ref[..., None]).abs().max()) <= 2 * 2.0 ** -8 + 2.0 ** -14
     assert float((lse.double().cpu() - torch.log(low + late * r)).abs().max()) <= 2.0 ** -16
+
+
+INFINITE = [(8, 2, 1, 700, 0), (30, 1, 1, 700, 0), (128, 1, 1, 262144, 0), (16, 4, 1, 65536, 0), (30, 1, 1, 700, 90)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("hq,hkv,next_n,max_ctx,topk", INFINITE)
+def test_infinite_queries(hq, hkv, next_n, max_ctx, topk, dtype):
+    # Element 7 of every key is +1 (sequence 0), +1 or -1 (1), zero somewhere (2).
+    # A score of +inf, or 0 * inf, makes the row NaN; one of -inf is a weight of 0,
+    # and a row of nothing else has no weight at all: 0 and -inf.
+    inf = float("inf")
+    c = Case([300, 300, 300], next_n=next_n, hq=hq, hkv=hkv, bs=16, dtype=dtype, max_ctx=max_ctx,
+             topk=topk, seed=3)
+    print(f"[infinite] {hq}/{hkv} max_ctx={max_ctx} topk={topk} {dtype}", flush=True)
+    at = c.kept()
+
+    def set_key(b, j, code):
+        byte = c.k[at(b, j)]
+        byte[:, 3] = (byte[:, 3] & 0x0f) | code << 4
+    listed = [range(300)] * 3 if not topk else [c.indices[b] for b in range(3)]
+    for b in range(3):
+        for n, j in enumerate(listed[b]):
+            set_key(b, int(j), 2 if b != 1 or n % 3 else 10)
+    for n in (0, 40, 80):
+        set_key(2, int(listed[2][n]), 0)
+    finite, finite_lse = c.run()
+    for h, x in ((0, inf), (1, -inf), (hq - 1, -inf)):
+        c.q[:, h, 7] = x
+    out, lse = c.run()
+    torch.cuda.synchronize()
+    rest = [h for h in range(hq) if h not in (0, 1, hq - 1)]
+    assert torch.equal(out[:, rest], finite[:, rest]) and torch.equal(lse[:, rest], finite_lse[:, rest])
+    assert bool(torch.isnan(out[:, 0]).all()) and bool(torch.isnan(lse[:, 0]).all())
+    for h in (1, hq - 1):
+        assert bool((out[0, h] == 0).all()) and float(lse[0, h]) == -inf
+        assert bool(torch.isnan(out[1:, h]).all()) and bool(torch.isnan(lse[1:, h]).all())
