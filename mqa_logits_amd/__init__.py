@@ -442,6 +442,12 @@ def _block_size(block_size):
         raise ValueError(f"block_size must be one of {BLOCK_SIZES}, got {block_size}")
 
 
+def _required(**tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} is required")
+
+
 def _fits(t, shape, dtype, device):
     return (t is not None and t.shape == shape and t.dtype is dtype and t.get_device() == device
             and t.is_contiguous())
@@ -476,7 +482,9 @@ def paged_kv_slots(context_lens, new_lens, free_blocks, block_table, num_blocks,
     _block_size(block_size)
     if not (0 <= max_tokens < 2 ** 31 and 0 <= max_context_len < 2 ** 31 and 0 < num_blocks < 2 ** 31):
         raise ValueError("max_tokens, max_context_len and num_blocks must be int32 and not negative")
-    batch, dev = context_lens.shape[0], context_lens.get_device()
+    if context_lens is None or free_blocks is None:
+        _required(context_lens=context_lens, free_blocks=free_blocks)
+    batch, dev = context_lens.numel(), context_lens.get_device()
     i32, given = torch.int32, out is not None
     if not given:
         out = (context_lens.new_empty(max_tokens, dtype=torch.int64),
@@ -514,6 +522,8 @@ def paged_kv_write(fmt, x, slots, kv_pool, kv_sf_pool=None, kv_scale_pool=None, 
     over 1.5 * 2 ** 127 as NaN.)  values (x's shape and type, contiguous) receives
     what the codes stand for."""
     code = _fmt(fmt)
+    if x is None or kv_pool is None:
+        _required(x=x, kv_pool=kv_pool)
     shape = x.shape
     if len(shape) not in (2, 3) or x.dtype not in ROW_TYPES:
         raise ValueError(f"x must be [n, D] or [n, heads, D] of {sorted(map(str, ROW_TYPES))}, "
@@ -580,13 +590,15 @@ def paged_attention(fmt, q, k_pool, k_sf_pool, v_pool, v_sf_pool, context_lens, 
     if fmt != "mxfp4":
         _fmt(fmt)
         raise ValueError(f"paged_attention reads an mxfp4 cache, got {fmt!r}")
+    if q is None or k_pool is None or context_lens is None:
+        _required(q=q, k_pool=k_pool, context_lens=context_lens)
     if q.dim() != 3 or q.dtype not in QUERY_TYPES:
         raise ValueError(f"q must be [rows, Hq, D] of bfloat16 or float16, got {tuple(q.shape)} {q.dtype}")
     if k_pool.dim() != 4:
         raise ValueError(f"k_pool must be [num_blocks, block_size, Hkv, D/2], got {tuple(k_pool.shape)}")
     q_shape, q_stride, dev = q.shape, q.stride(), q.get_device()
     rows, hq, d = q_shape
-    batch = context_lens.shape[0]
+    batch = context_lens.numel()
     num_blocks, block_size, hkv, _ = k_pool.shape
     _block_size(block_size)
     if not 0 <= max_context_len < 2 ** 31:
