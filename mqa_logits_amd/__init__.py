@@ -413,17 +413,18 @@ def paged_mqa_logits(fmt, q, q_sf, kv_pool, kv_sf_pool, kv_scale_pool, weights,
 # first one expression over everything a call takes; only where that fails, the
 # checks one by one, which name what does not fit.
 
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
-
 
 def _call(fn, device, *args):
     """fn(*args, stream) on GPU `device` (kernels go to the current device)."""
-    if _current_device() == device:
-        status = fn(*args, _current_stream(device))
+    # the bindings under torch.cuda's current_device and current_stream, a
+    # microsecond sooner; a build of torch without GPU support lacks them
+    current = torch._C._cuda_getDevice
+    stream = torch._C._cuda_getCurrentRawStream
+    if current() == device:
+        status = fn(*args, stream(device))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, _current_stream(device))
+            status = fn(*args, stream(device))
     if status != 0:
         _check(status)
 

@@ -1,9 +1,16 @@
-"""The cache calls' binding: what is missing is named."""
+"""The cache calls' binding, without a GPU: what is missing is named, and the
+package imports on a PyTorch build without GPU support."""
+
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
 mq = pytest.importorskip("mqa_logits_amd")
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def u8(*shape):
@@ -49,3 +56,13 @@ def test_what_is_missing_is_named_on_the_gpu(fn, name):
         fn(**{**args, name: None})
     with pytest.raises(ValueError):
         fn(**{**args, name: args[name].new_zeros(())})
+
+
+def test_imports_without_gpu_support_in_torch():
+    code = ("import torch\n"
+            "for name in [n for n in dir(torch._C) if n.startswith('_cuda_get')]:\n"
+            "    delattr(torch._C, name)\n"
+            "import mqa_logits_amd\n"
+            "assert mqa_logits_amd.paged_attention_workspace_size(1, 1, 8, 1, 128, 100000) > 0\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
