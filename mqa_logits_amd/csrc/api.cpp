@@ -190,21 +190,24 @@ AttnPlan plan_attention(int32_t batch, int32_t next_n, int32_t hq, int32_t hkv, 
   // The kernels whose waves have rows of their own leave four times the parts,
   // so they need pieces long enough to outweigh that.
   // Over 64 rows, 128 at a time: 64 sequences of 1024..32768 keys, 256 rows, take
-  // 176 us, 221 with 32 rows at a time; 32 of 8192 keys, 128 rows (4 steps a
-  // piece), 45 against 39.
+  // 228 us, 262 with 32 rows at a time; 128 of 8192 keys, 128 rows (16 steps a
+  // piece), 123 against 137, 64 of them (8) 76 against 78, 32 (4) 50 against 45.
   if (rows > 64) split(128, 1);
   if (rows <= 64 || a.steps < 12 * (int64_t)a.workers) {
     // Up to 16 rows, a KV head per wave: 32 sequences of 1024..32768 keys, 8 KV
-    // heads, 138 us against 158; one of 131072 keys, 4 KV heads (2 steps a
-    // piece), 32 against 26.
+    // heads, 142 us against 163; 8 of 32768 keys, 4 KV heads (4 steps a piece), 39
+    // against 35, one of 131072 keys (2 steps) 42 against 28.
     if (rows <= 16 && hkv % 4 == 0) split(64, 4);
     if (rows > 16 || hkv % 4 || a.steps < 6 * (int64_t)a.workers) split(rows <= 16 ? 16 : 32, 1);
   }
-  // selected columns are units of one size: whole ones for every worker, where
-  // that divides evenly, leave nothing to join
+  // Selected columns are units of one size: whole ones for every worker, where
+  // that divides evenly, leave nothing to join.  Only where it keeps nine workers
+  // in ten: 2048 columns of 16 rows take 112 us against 123 for 1000 units (500 of
+  // 512 workers), 94 against 92 for 768 (384), but 73 against 54 for 514 (257).
   if (topk && a.workers < a.units) {
     const int32_t each = (a.units + a.workers - 1) / a.workers;
-    if (a.units % each == 0) a.workers = a.units / each;
+    if (a.units % each == 0 && 10 * (int64_t)(a.units / each) >= 9 * (int64_t)a.workers)
+      a.workers = a.units / each;
   }
   // (nor do units of a single step)
   a.join = a.workers > 1 && a.steps > a.units && !(topk && a.units % a.workers == 0);

@@ -1,5 +1,6 @@
-"""The cache calls' binding, without a GPU: what is missing is named, and the
-package imports on a PyTorch build without GPU support."""
+"""The cache calls' binding: what is missing is named, how attention's work is
+dealt out shows in its workspace, and the package imports on a PyTorch build
+without GPU support."""
 
 import os
 import subprocess
@@ -56,6 +57,17 @@ def test_what_is_missing_is_named_on_the_gpu(fn, name):
         fn(**{**args, name: None})
     with pytest.raises(ValueError):
         fn(**{**args, name: args[name].new_zeros(())})
+
+
+def test_selected_columns_keep_their_workers():
+    # Units of one size are dealt out whole, with nothing to join (no workspace),
+    # only where that leaves few of the 512 workers idle: not 257 of them for 514.
+    size = mq.paged_attention_workspace_size
+    for units, whole in ((512, True), (513, False), (514, False), (520, False), (640, False),
+                         (768, False), (1000, True), (1024, True), (1536, True)):
+        assert (size(units, 1, 16, 1, 128, 8192, 2048) == 0) == whole, units
+    for units, whole in ((256, True), (258, False), (320, False), (500, True), (512, True)):
+        assert (size(units, 1, 64, 1, 128, 8192, 2048) == 0) == whole, units
 
 
 def test_imports_without_gpu_support_in_torch():
