@@ -356,7 +356,8 @@ mqa_status paged_kv_write(mqa_dtype dt, const void* x, mqa_float x_type, int64_t
  *            fp32 and must stay within +-2^127
  *   out      [batch*next_n, Hq, D] of q_type; head h reads KV head
  *            h / (Hq / Hkv).  0 for a row without keys, or without a score
- *            over -inf
+ *            over -inf.  Scores, maxima and sums are fp32; the weights are
+ *            rounded to 2^-16 where they multiply V
  *   lse      NULL or [batch*next_n, Hq] fp32: log(sum exp(scale <q, k>)), -inf
  *            for such a row
  *   workspace of at least paged_attention_workspace_size bytes for the same

@@ -42,7 +42,7 @@
 // would round every weight by up to 2^-8 while the sum they are divided by keeps
 // all bits, and with weights of one size that does not average out (values that
 // are all 1 gave 0.996).  The second part costs bf16 calls that the matrix cores
-// bound 15 to 23% (64 x 4 query tokens of 64 heads: 221 us, 180 with one) and
+// bound 15 to 23% (64 x 4 query tokens of 64 heads: 222 us, 180 with one) and
 // others up to 6%.  The sum of p, the maximum and all accumulators are fp32.
 //
 // What bounds it.  With few rows the cache's bytes: (D/2 + D/32) * 2 per key and
@@ -50,10 +50,12 @@
 // which hardly overlap on this chip: 32 keys x 32 rows are 48 products (768
 // cycles) and, with the keys converted by every wave, about 240 vector
 // instructions (1000 cycles).  Measured: 64 x 4 query
-// tokens of 64 heads over 1024..32768 keys 221 us, 0.64 PFLOP/s; 32 sequences of
-// those lengths, 8 KV heads of 8 fp16 rows each, 138 us, 4.2 TB/s; one context of
-// 131072 keys, 4 KV heads, 28 us; 2048 selected keys of 64 heads for 256 query
-// tokens 48 us, for one 10.6.
+// tokens of 64 heads over 1024..32768 keys 222 us, 0.64 PFLOP/s (matrix cores
+// busy 42% of the time; every wave also reads a tile's 16 KB of operands from LDS
+// for its 32 rows, about 40% of the time at 128 bytes a clock); 32 sequences of
+// those lengths, 8 KV heads of 8 fp16 rows each, 138 us, 4.2 TB/s (busy 23%); one
+// context of 131072 keys, 4 KV heads, 28 us; 2048 selected keys of 64 heads for
+// 256 query tokens 49 us (busy 22%), for one 10.7.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
