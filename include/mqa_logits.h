@@ -352,8 +352,10 @@ mqa_status paged_kv_write(mqa_dtype dt, const void* x, mqa_float x_type, int64_t
  *            [batch*next_n, indices_stride] int32: row r attends to the keys
  *            among its first topk entries that it sees, any other entry (-1)
  *            is passed over; a key listed twice counts twice
- *   scale    finite factor of <q, k>; <q, k> and the scores times log2(e) are
- *            fp32 and must stay within +-2^127
+ *   scale    finite factor of <q, k>, which is fp32 (within +-2^127); scores
+ *            times log2(e) must stay within +-2^24 (beyond it neighbouring fp32
+ *            scores are octaves apart, and results may be 0 or NaN), or be
+ *            infinite
  *   out      [batch*next_n, Hq, D] of q_type; head h reads KV head
  *            h / (Hq / Hkv).  0 for a row without keys, or without a score
  *            over -inf.  Scores, maxima and sums are fp32; the weights are

@@ -583,7 +583,8 @@ def paged_attention(fmt, q, k_pool, k_sf_pool, v_pool, v_sf_pool, context_lens, 
     pools [num_blocks, block_size, Hkv, D/2] with e8m0 [.., D/32].  Row
     b * next_n + t sees the first context_lens[b] - next_n + 1 + t keys; with
     indices (int32 [rows, topk], as mqa_logits_topk gives them) it attends to
-    the listed ones among them.  scale defaults to D ** -0.5.  Returns out
+    the listed ones among them.  scale defaults to D ** -0.5; scores must stay
+    within +-2 ** 24 octaves.  Returns out
     (q's shape and type; zeros for a row without keys), or (out, lse fp32
     [rows, Hq]) with return_lse or an lse to fill.  workspace: a uint8 tensor
     of paged_attention_workspace_size bytes to keep between calls on one

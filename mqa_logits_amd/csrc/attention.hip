@@ -412,7 +412,10 @@ struct Rows {
 
   // Weights of one row tile from its scores, packed for the second product.
   // Whether a maximum was left behind shows in the weights themselves; then
-  // they are formed again.
+  // they are formed again.  One fused instruction scales and shifts a score; it
+  // leaves the maximum's own rounding in the exponent, half an octave at 2^24
+  // octaves, which is why scores may not be larger.  (Scaled and shifted apart,
+  // 64 x 4 query tokens of 64 heads took 228 us instead of 222.)
   __device__ __forceinline__ void weights(const f32x4 (&x)[2], int rt, float c2, u32x4 (&p)[kWeightParts]) {
     float w[8];
     const auto form = [&] {

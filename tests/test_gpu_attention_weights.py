@@ -168,3 +168,32 @@ def test_infinite_queries(hq, hkv, next_n, max_ctx, topk, dtype):
     for h in (1, hq - 1):
         assert bool((out[0, h] == 0).all()) and float(lse[0, h]) == -inf
         assert bool(torch.isnan(out[1:, h]).all()) and bool(torch.isnan(lse[1:, h]).all())
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("hq,hkv,next_n,max_ctx,topk", KERNELS)
+def test_scores_of_the_largest_size(hq, hkv, next_n, max_ctx, topk, dtype, sign):
+    # The later keys score +-2^23 .. 2^24 octaves, under a factor that is no power of
+    # two, the first 128 score 0: one side has all the weight.  Values are 1 and 2.
+    import mqa_logits_amd as mq
+    print(f"[scores] {sign} {hq}/{hkv} next_n={next_n} max_ctx={max_ctx} topk={topk} {dtype}", flush=True)
+    args, kw, _, seen, low = alike(hq, hkv, next_n, max_ctx, topk, 64, dtype, code=4, byte=127)
+    q, sf, v = args[1], args[3], args[4]
+    size = torch.linspace(1.05, 1.95, q.shape[0] * q.shape[1]).view(q.shape[:2]) * 2.0 ** 11
+    q[:, :, 0] = (sign * size).to(q)
+    sf.fill_(127 + 15)                                               # <q, k> = q 2^15
+    v.view(BATCH, -1, hkv, 32)[:, :low] = 0x22                       # 1 instead of 2
+    kw["scale"] = scale = float(np.float32(0.0884))
+    out, lse = mq.paged_attention(*args, **kw)
+    torch.cuda.synchronize()
+    score = scale * q[:, :, 0].double().cpu() * 2.0 ** 15
+    octaves = score.abs() / math.log(2.0)
+    assert 2.0 ** 22.9 < float(octaves.min()) and float(octaves.max()) < 2.0 ** 24
+    assert bool((out == (2 if sign > 0 else 1)).all())
+    if sign > 0:
+        ref = score + torch.log((seen - low).double())[:, None]
+    else:
+        ref = torch.full_like(score, math.log(low))
+    # the factor, its product, the maximum with the sum's logarithm, and ln 2: a rounding of 2^-24 each
+    assert bool(((lse.double().cpu() - ref).abs() <= 2.0 ** -22 * ref.abs()).all())
