@@ -17,7 +17,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_attention import Case
+from oracle import cache
+from tests.test_gpu_attention import Case, assert_within
 
 pytestmark = pytest.mark.gpu
 
@@ -197,3 +198,20 @@ def test_scores_of_the_largest_size(hq, hkv, next_n, max_ctx, topk, dtype, sign)
         ref = torch.full_like(score, math.log(low))
     # the factor, its product, the maximum with the sum's logarithm, and ln 2: a rounding of 2^-24 each
     assert bool(((lse.double().cpu() - ref).abs() <= 2.0 ** -22 * ref.abs()).all())
+
+
+@pytest.mark.parametrize("topk", [0, 200])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv,next_n,max_ctx", [(8, 1, 2, 700), (30, 1, 1, 700), (128, 1, 1, 262144), (24, 2, 4, 262144),
+                                                   (16, 4, 1, 65536), (24, 8, 3, 65536)])
+def test_bf16_against_64_bits(hq, hkv, next_n, max_ctx, d, topk):
+    # the oracle's bound, with 2^-16 for the weights
+    c = Case([0, 1, 33, 300, 700], next_n=next_n, hq=hq, hkv=hkv, d=d, bs=16, max_ctx=max_ctx, topk=topk, seed=hq + d)
+    print(f"[64 bits] {hq}/{hkv} next_n={next_n} D={d} max_ctx={max_ctx} topk={topk}", flush=True)
+    out, lse = c.run()
+    torch.cuda.synchronize()
+    ref, ref_lse, tol, tol_lse = cache.attention(
+        c.q.double().numpy(), c.k, c.ks, c.v, c.vs, c.ctx, c.table, next_n, max_ctx, c.scale,
+        HALF[torch.bfloat16], 2.0 ** -16, indices=c.indices)
+    assert_within(out.double().cpu().numpy(), ref, tol, "out")
+    assert_within(lse.double().cpu().numpy(), ref_lse, tol_lse, "lse")
