@@ -388,6 +388,44 @@ mqa_status paged_attention(mqa_dtype dt, const void* q, mqa_float q_type, int64_
                            int32_t block_size, int32_t num_blocks, int32_t max_context_len,
                            hipStream_t stream);
 
+/*
+ * Softmax attention of chunks of new tokens over a paged MXFP4 cache that holds
+ * them already (prompts, their continuation, drafts): paged_attention for a
+ * different, and any, number of query tokens a sequence.
+ *   q        [tokens, Hq, D] bf16 or fp16 (q_type), q_stride elements from token
+ *            to token (a multiple of 8, >= Hq * D)
+ *   token_offsets [batch + 1] int32: the rows of sequence b are token_offsets[b]
+ *            .. token_offsets[b + 1] - 1, its last tokens (paged_kv_slots writes
+ *            them; rows from `tokens` on are passed over, and others that no
+ *            sequence has are left as they were).  No row may be two
+ *            sequences'.  NULL: tokens / batch rows each
+ *   With n rows, row t of sequence b sees keys
+ *            [0, clamp(ctx_b - n + t + 1, 0, min(ctx_b, max_context_len)))
+ *   dt, pools, context_lens, block_table, scale, out [tokens, Hq, D], lse
+ *            [tokens, Hq]: as paged_attention, but n keys times the largest |v|
+ *            must stay below 2^112.  Where they multiply V, weights are rounded
+ *            to fp16 (2^-12 of themselves, or 2^-37 of the row's largest); in
+ *            steps of 64 keys among which a scale of V is outside 2^-15 .. 2^9
+ *            (or one of K, for fp16 queries), which take longer, to 2^-16.  out
+ *            is divided by the sum of the rounded ones, lse is from the others
+ *   workspace of at least paged_chunk_attention_workspace_size bytes for the same
+ *            sizes (NULL if that is 0), 16-byte aligned, as paged_attention's.
+ * Outputs and workspace must not overlap anything else.  Requires D in {64, 128},
+ * Hkv <= 256, Hq a multiple of Hkv and at most 1024, 1 <= batch <= 8192,
+ * block_size in {16, 32, 64}, max_context_len <= 2^30, pools as paged_attention's.
+ */
+int64_t paged_chunk_attention_workspace_size(int32_t batch, int32_t tokens, int32_t hq, int32_t hkv,
+                                             int32_t d, int32_t max_context_len);  /* bytes; negative on error */
+mqa_status paged_chunk_attention(mqa_dtype dt, const void* q, mqa_float q_type, int64_t q_stride,
+                                 const uint8_t* k_pool, const uint8_t* k_sf_pool,
+                                 const uint8_t* v_pool, const uint8_t* v_sf_pool,
+                                 const int32_t* context_lens, const int32_t* token_offsets,
+                                 const int32_t* block_table, int64_t block_table_stride, float scale,
+                                 void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                                 int32_t batch, int32_t tokens, int32_t hq, int32_t hkv, int32_t d,
+                                 int32_t block_size, int32_t num_blocks, int32_t max_context_len,
+                                 hipStream_t stream);
+
 /* Compute units of a device (the get_num_sms analogue of the DeepGEMM
  * article's paged example); negative on error. */
 int32_t mqa_num_cus(int32_t device);

@@ -17,6 +17,7 @@ Entry points (same names as the C ABI):
   paged_kv_slots                  block-table entries and slot map of a step's new tokens
   paged_kv_write                  quantise rows and store them at their slots
   paged_attention                 attention over a paged MXFP4 cache, whole or selected keys
+  paged_chunk_attention           the same for chunks of new tokens, a different number a sequence
   mqa_num_cus, paged_mqa_logits_default_splits
 """
 
@@ -70,6 +71,8 @@ def _load():
         "paged_kv_write": [I32, P, I32, I64, I64, P, P, P, P, P, I64, I32, I32, I32, P],
         "paged_attention": [I32, P, I32, I64, P, P, P, P, P, P, I64, P, I64, I32, ctypes.c_float,
                             P, P, P, I64, I32, I32, I32, I32, I32, I32, I32, I32, P],
+        "paged_chunk_attention": [I32, P, I32, I64, P, P, P, P, P, P, P, I64, ctypes.c_float, P, P, P,
+                                  I64, I32, I32, I32, I32, I32, I32, I32, I32, P],
     }
     for name, argtypes in sigs.items():
         fn = getattr(lib, name)
@@ -80,6 +83,8 @@ def _load():
         getattr(lib, name).restype = I64
     lib.paged_attention_workspace_size.argtypes = [I32] * 7
     lib.paged_attention_workspace_size.restype = I64
+    lib.paged_chunk_attention_workspace_size.argtypes = [I32] * 6
+    lib.paged_chunk_attention_workspace_size.restype = I64
     lib.mqa_num_cus.argtypes = [I32]
     lib.mqa_num_cus.restype = I32
     lib.paged_mqa_logits_default_splits.argtypes = [I32]
@@ -95,7 +100,9 @@ EXPORTED = ("mqa_logits", "mqa_logits_metadata_size", "mqa_logits_metadata", "mq
             "mqa_logits_compressed_offsets", "mqa_logits_compressed",
             "paged_mqa_logits_metadata_size", "paged_mqa_logits_metadata",
             "paged_mqa_logits", "paged_kv_slots", "paged_kv_write",
-            "paged_attention_workspace_size", "paged_attention", "mqa_num_cus", "paged_mqa_logits_default_splits",
+            "paged_attention_workspace_size", "paged_attention",
+            "paged_chunk_attention_workspace_size", "paged_chunk_attention",
+            "mqa_num_cus", "paged_mqa_logits_default_splits",
             "mqa_last_error")
 
 
@@ -659,4 +666,100 @@ def paged_attention(fmt, q, k_pool, k_sf_pool, v_pool, v_sf_pool, context_lens, 
           _row_stride(indices, topk) if topk else 0, topk,
           d ** -0.5 if scale is None else float(scale), out.data_ptr(), _data(lse),
           _data(workspace), size, batch, next_n, hq, hkv, d, block_size, num_blocks, max_context_len)
+    return out if lse is None else (out, lse)
+
+
+@functools.lru_cache(maxsize=1024)
+def paged_chunk_attention_workspace_size(batch, tokens, q_heads, kv_heads, d, max_context_len):
+    """Bytes of workspace of a paged_chunk_attention call of these sizes."""
+    n = lib.paged_chunk_attention_workspace_size(batch, tokens, q_heads, kv_heads, d, max_context_len)
+    if n < 0:
+        raise MqaError(2, lib.mqa_last_error().decode())
+    return n
+
+
+def _chunk_sizes(what, fmt, q, k_pool, context_lens, token_offsets, max_context_len):
+    """Sizes of a call for ragged tokens, from its first arguments: (tokens, Hq, D, batch, pool
+    shape, q's stride), once they make sense together."""
+    if fmt != "mxfp4":
+        _fmt(fmt)
+        raise ValueError(f"{what} reads an mxfp4 cache, got {fmt!r}")
+    if q is None or k_pool is None or context_lens is None:
+        _required(q=q, k_pool=k_pool, context_lens=context_lens)
+    if q.dim() != 3 or q.dtype not in QUERY_TYPES:
+        raise ValueError(f"q must be [tokens, Hq, D] of bfloat16 or float16, got {tuple(q.shape)} {q.dtype}")
+    if k_pool.dim() != 4:
+        raise ValueError(f"k_pool must be [num_blocks, block_size, Hkv, D/2], got {tuple(k_pool.shape)}")
+    tokens, hq, d = q.shape
+    stride, batch = q.stride(), context_lens.numel()
+    _block_size(k_pool.shape[1])
+    if not (0 <= max_context_len < 2 ** 31 and tokens < 2 ** 31):
+        raise ValueError("max_context_len and the number of tokens must be int32 and not negative")
+    if stride[2] != 1 or (hq > 1 and stride[1] != d):
+        raise ValueError("q rows must be contiguous")
+    if token_offsets is None and (batch == 0 or tokens % batch):
+        raise ValueError(f"{tokens} tokens of {batch} sequences need token_offsets")
+    return tokens, hq, d, batch, k_pool.shape, stride[0] if tokens > 1 else hq * d
+
+
+def paged_chunk_attention(fmt, q, k_pool, k_sf_pool, v_pool, v_sf_pool, context_lens, token_offsets,
+                          block_table, max_context_len, scale=None, out=None, lse=None,
+                          return_lse=False, workspace=None):
+    """Attention of chunks of new tokens over a paged 4-bit cache that holds them already.
+
+    fmt "mxfp4"; q [tokens, Hq, D] bf16 or fp16 (rows may be strided), pools [num_blocks,
+    block_size, Hkv, D/2] with e8m0 [.., D/32].  The rows of sequence b are token_offsets[b] ..
+    token_offsets[b + 1] - 1 (int32 [batch + 1], as paged_kv_slots gives them; None: as many for
+    every sequence), its last tokens: row t of n sees the first context_lens[b] - n + 1 + t keys.
+    scale defaults to D ** -0.5; scores must stay within +-2 ** 24 octaves.  Returns out (q's
+    shape and type; zeros for a row without keys), or (out, lse fp32 [tokens, Hq]) with return_lse
+    or an lse to fill; rows that no sequence has are left as they were.  workspace: a uint8 tensor of
+    paged_chunk_attention_workspace_size bytes to keep between calls on one stream, or None."""
+    tokens, hq, d, batch, (num_blocks, block_size, hkv, _), q_stride = _chunk_sizes(
+        "paged_chunk_attention", fmt, q, k_pool, context_lens, token_offsets, max_context_len)
+    dev = q.get_device()
+    # (what is made here needs no check)
+    given_out, given_lse, given_workspace = out is not None, lse is not None, workspace is not None
+    if not given_out:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if not given_lse and return_lse:
+        lse = q.new_empty((tokens, hq), dtype=torch.float32)
+    need = paged_chunk_attention_workspace_size(batch, tokens, hq, hkv, d, max_context_len)
+    if not given_workspace:
+        workspace, size = (q.new_empty(need, dtype=torch.uint8), need) if need else (None, 0)
+    else:
+        size = workspace.numel()
+    codes, scales = (num_blocks, block_size, hkv, d // 2), (num_blocks, block_size, hkv, d // 32)
+    byte, i32 = k_pool.dtype, torch.int32
+    if not (dev >= 0 and byte.itemsize == 1 and _fits(k_pool, codes, byte, dev)
+            and _fits(v_pool, codes, byte, dev)
+            and k_sf_pool is not None and k_sf_pool.dtype.itemsize == 1 and _fits(k_sf_pool, scales, k_sf_pool.dtype, dev)
+            and _fits(v_sf_pool, scales, k_sf_pool.dtype, dev)
+            and _fits(context_lens, (batch,), i32, dev)
+            and (token_offsets is None or _fits(token_offsets, (batch + 1,), i32, dev))
+            and _table_fits(block_table, batch, -(-max_context_len // block_size), dev)
+            and (not given_out or _fits(out, q.shape, q.dtype, dev))
+            and (not given_lse or _fits(lse, (tokens, hq), torch.float32, dev))
+            and (not given_workspace or _fits(workspace, (size,), torch.uint8, dev))):
+        a = _Args()
+        a.want(q[:0], "q", (0, hq, d))
+        for name, pool, sf in (("k", k_pool, k_sf_pool), ("v", v_pool, v_sf_pool)):
+            a.want(pool, name + "_pool", codes, itemsize=1)
+            a.want(sf, name + "_sf_pool", scales, itemsize=1)
+        a.want(context_lens, "context_lens", (batch,), I32_T)
+        if token_offsets is not None:
+            a.want(token_offsets, "token_offsets", (batch + 1,), I32_T)
+        _want_table(a, block_table, batch, block_size, max_context_len)
+        a.want(out, "out", (tokens, hq, d), (q.dtype,))
+        if lse is not None:
+            a.want(lse, "lse", (tokens, hq), (torch.float32,))
+        if workspace is not None:
+            a.want(workspace, "workspace", (None,), itemsize=1)
+        a.on_gpu()
+    _call(lib.paged_chunk_attention, dev, 2, q.data_ptr(), QUERY_TYPES[q.dtype], q_stride,
+          k_pool.data_ptr(), k_sf_pool.data_ptr(), v_pool.data_ptr(), v_sf_pool.data_ptr(),
+          context_lens.data_ptr(), _data(token_offsets), block_table.data_ptr(),
+          _row_stride(block_table, block_table.shape[1]), d ** -0.5 if scale is None else float(scale),
+          out.data_ptr(), _data(lse), _data(workspace), size, batch, tokens, hq, hkv, d, block_size,
+          num_blocks, max_context_len)
     return out if lse is None else (out, lse)

@@ -216,6 +216,46 @@ AttnPlan plan_attention(int32_t batch, int32_t next_n, int32_t hq, int32_t hkv, 
   return a;
 }
 
+// A chunk call's split: tiles of up to 128 rows, each whole heads of a few tokens.
+struct ChunkPlan {
+  int32_t tile_heads, head_groups, members, tile_tokens;
+  int32_t workers, whole;
+  int64_t parts, bytes;
+};
+constexpr int32_t kChunkRows = 128, kChunkLeast = 4;
+
+ChunkPlan plan_chunk(int32_t batch, int32_t tokens, int32_t hq, int32_t hkv, int32_t d,
+                     int32_t max_context_len) {
+  ChunkPlan a{};
+  const int32_t group = hq / hkv;
+  a.head_groups = (group + kChunkRows - 1) / kChunkRows;
+  a.tile_heads = (group + a.head_groups - 1) / a.head_groups;
+  a.members = hkv * a.head_groups;
+  a.tile_tokens = kChunkRows / a.tile_heads;
+  const int64_t tiles = std::min<int64_t>(tokens, ((int64_t)tokens + a.tile_tokens - 1) / a.tile_tokens + batch) * a.members;
+  const int64_t most = std::max<int64_t>(((int64_t)max_context_len + 63) / 64, 1);
+  a.whole = most <= 2 * kChunkLeast;
+  const int64_t limit = a.whole ? 65536 : mqa::kAttnResident;
+  a.workers = (int32_t)std::min(limit, a.whole || tiles >= limit ? tiles : std::max<int64_t>(tiles * most / kChunkLeast, 1));
+  a.parts = a.whole ? 0 : (int64_t)a.workers * 2 * kChunkRows;
+  a.bytes = a.whole ? 0 : a.parts * (d + 4) * 4 + (int64_t)a.workers * (int64_t)sizeof(mqa::ChunkNote);
+  return a;
+}
+
+mqa_status check_chunk_shape(int32_t batch, int32_t tokens, int32_t hq, int32_t hkv, int32_t d,
+                             int32_t max_context_len, const char* who) {
+  if (batch < 1 || batch > 8192) return fail(MQA_ERR_UNSUPPORTED, "%s: batch=%d not in [1, 8192]", who, batch);
+  if (tokens < 0) return fail(MQA_ERR_INVALID_ARG, "%s: negative number of tokens", who);
+  if (d != 64 && d != 128) return fail(MQA_ERR_UNSUPPORTED, "%s: D=%d not supported (64, 128)", who, d);
+  if (hkv < 1 || hkv > 256 || hq < 1 || hq > 1024 || hq % hkv)
+    return fail(MQA_ERR_UNSUPPORTED, "%s: Hq=%d Hkv=%d: Hkv in [1, 256], Hq a multiple of it and at most 1024",
+                who, hq, hkv);
+  if (max_context_len < 0) return fail(MQA_ERR_INVALID_ARG, "%s: negative max_context_len", who);
+  if (max_context_len > (1 << 30))
+    return fail(MQA_ERR_UNSUPPORTED, "%s: max_context_len=%d over 2^30", who, max_context_len);
+  return MQA_OK;
+}
+
 int32_t block_shift(int32_t block_size) { return block_size == 16 ? 4 : block_size == 32 ? 5 : 6; }
 
 mqa_status check_attention_shape(int32_t batch, int32_t next_n, int32_t hq, int32_t hkv, int32_t d,
@@ -237,6 +277,52 @@ mqa_status check_precision(mqa_precision precision, const char* who) {
   if (precision != MQA_PRECISION_DEFAULT && precision != MQA_PRECISION_EXACT_PRODUCTS)
     return fail(MQA_ERR_INVALID_ARG, "%s: unknown precision %d", who, (int)precision);
   return MQA_OK;
+}
+
+// What the calls for ragged tokens take alike.
+mqa_status check_chunk_cache(mqa_dtype dt, const void* q, mqa_float q_type, int64_t q_stride,
+                             const uint8_t* k_pool, const uint8_t* k_sf_pool,
+                             const int32_t* context_lens, const int32_t* token_offsets,
+                             const int32_t* block_table, int64_t block_table_stride, float scale,
+                             int32_t batch, int32_t tokens, int32_t hq, int32_t hkv, int32_t d,
+                             int32_t block_size, int32_t num_blocks, int32_t max_context_len,
+                             const char* who) {
+  if (dt != MQA_MXFP4_E2M1)
+    return fail(dt == MQA_FP8_E4M3 || dt == MQA_MXFP8_E4M3 ? MQA_ERR_UNSUPPORTED : MQA_ERR_INVALID_ARG,
+                "%s: the cache must be MXFP4 (dtype %d)", who, (int)dt);
+  if (q_type != MQA_BF16 && q_type != MQA_F16)
+    return fail(q_type == MQA_F32 ? MQA_ERR_UNSUPPORTED : MQA_ERR_INVALID_ARG,
+                "%s: q must be bf16 or fp16 (type %d)", who, (int)q_type);
+  if (block_size != 16 && block_size != 32 && block_size != 64)
+    return fail(MQA_ERR_UNSUPPORTED, "%s: block_size=%d not in {16, 32, 64}", who, block_size);
+  if (num_blocks < 1) return fail(MQA_ERR_INVALID_ARG, "%s: num_blocks < 1", who);
+  if ((int64_t)num_blocks * block_size > 0x7fffffff ||
+      (int64_t)num_blocks * block_size * hkv > 0xffffffffll / (d / 32) - 1)
+    return fail(MQA_ERR_UNSUPPORTED, "%s: pool of %d blocks too large", who, num_blocks);
+  if ((tokens > 0 && !q) || !k_pool || !k_sf_pool || !context_lens || (max_context_len > 0 && !block_table))
+    return fail(MQA_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(k_sf_pool, 16) || !aligned(context_lens, 4) ||
+      !aligned(token_offsets, 4) || !aligned(block_table, 4))
+    return fail(MQA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+  if (!token_offsets && tokens % batch)
+    return fail(MQA_ERR_INVALID_ARG, "%s: %d tokens of %d sequences need token_offsets", who, tokens, batch);
+  if (q_stride < (int64_t)hq * d || q_stride % 8)
+    return fail(MQA_ERR_INVALID_ARG, "%s: q_stride must be a multiple of 8 and at least Hq * D", who);
+  if (block_table_stride < ((int64_t)max_context_len + block_size - 1) / block_size)
+    return fail(MQA_ERR_INVALID_ARG, "%s: block_table_stride < ceil(max_context_len / block_size)", who);
+  uint32_t scale_bits;   // by its bits: this file is built without NaN semantics
+  std::memcpy(&scale_bits, &scale, 4);
+  if ((scale_bits & 0x7f800000u) == 0x7f800000u)
+    return fail(MQA_ERR_INVALID_ARG, "%s: scale is not finite", who);
+  return MQA_OK;
+}
+
+// |scale| * log2(e), positive and finite: a masked score (-inf) or one of 0 stays
+// out of NaN.  (The least subnormal stands for 0: it leaves any finite <q, k> a
+// score under 2^-20; the kernels keep subnormals.)
+float positive_c2(float scale) {
+  return std::clamp((scale < 0.f ? -scale : scale) * 1.4426950408889634f,
+                    std::numeric_limits<float>::denorm_min(), std::numeric_limits<float>::max());
 }
 
 }  // namespace
@@ -651,6 +737,80 @@ mqa_status paged_attention(mqa_dtype dt, const void* q, mqa_float q_type, int64_
     fprintf(stderr, "[mqa_logits] %s Hq=%d Hkv=%d D=%d batch=%d next_n=%d bs=%d topk=%d workers=%d rows=%d x %d\n",
             who, hq, hkv, d, batch, next_n, block_size, topk, a.workers, a.member_rows, a.row_groups);
   return hip_status(mqa::launch_attention(d, q_type == MQA_F16, p, stream), who);
+}
+
+int64_t paged_chunk_attention_workspace_size(int32_t batch, int32_t tokens, int32_t hq, int32_t hkv,
+                                             int32_t d, int32_t max_context_len) {
+  mqa_status st = check_chunk_shape(batch, tokens, hq, hkv, d, max_context_len,
+                                    "paged_chunk_attention_workspace_size");
+  if (st != MQA_OK) return -1;
+  return tokens == 0 ? 0 : plan_chunk(batch, tokens, hq, hkv, d, max_context_len).bytes;
+}
+
+mqa_status paged_chunk_attention(mqa_dtype dt, const void* q, mqa_float q_type, int64_t q_stride,
+                                 const uint8_t* k_pool, const uint8_t* k_sf_pool,
+                                 const uint8_t* v_pool, const uint8_t* v_sf_pool,
+                                 const int32_t* context_lens, const int32_t* token_offsets,
+                                 const int32_t* block_table, int64_t block_table_stride, float scale,
+                                 void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                                 int32_t batch, int32_t tokens, int32_t hq, int32_t hkv, int32_t d,
+                                 int32_t block_size, int32_t num_blocks, int32_t max_context_len,
+                                 hipStream_t stream) {
+  const char* who = "paged_chunk_attention";
+  mqa_status st = check_chunk_shape(batch, tokens, hq, hkv, d, max_context_len, who);
+  if (st != MQA_OK) return st;
+  st = check_chunk_cache(dt, q, q_type, q_stride, k_pool, k_sf_pool, context_lens, token_offsets, block_table,
+                         block_table_stride, scale, batch, tokens, hq, hkv, d, block_size, num_blocks,
+                         max_context_len, who);
+  if (st != MQA_OK) return st;
+  if (tokens == 0) return ok();
+  if (!v_pool || !v_sf_pool || !out) return fail(MQA_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!aligned(v_pool, 16) || !aligned(v_sf_pool, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
+      !aligned(workspace, 16))
+    return fail(MQA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+  const ChunkPlan a = plan_chunk(batch, tokens, hq, hkv, d, max_context_len);
+  if (workspace_bytes < a.bytes || (a.bytes > 0 && !workspace))
+    return fail(MQA_ERR_INVALID_ARG, "%s: workspace of %lld bytes, %lld needed", who,
+                (long long)workspace_bytes, (long long)a.bytes);
+  mqa::ChunkParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_stride = q_stride;
+  p.k = k_pool;
+  p.k_sf = k_sf_pool;
+  p.v = v_pool;
+  p.v_sf = v_sf_pool;
+  p.ctx = context_lens;
+  p.offsets = token_offsets;
+  p.bt = block_table;
+  p.bt_stride = block_table_stride;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float4*>(p.part_o + a.parts * d);
+  p.notes = a.whole ? nullptr : reinterpret_cast<mqa::ChunkNote*>(p.part_ml + a.parts);
+  p.batch = batch;
+  p.tokens = tokens;
+  p.next_n = token_offsets ? 0 : tokens / batch;
+  p.kv_heads = hkv;
+  p.group = hq / hkv;
+  p.q_heads = hq;
+  p.num_blocks = num_blocks;
+  p.bs_shift = block_shift(block_size);
+  p.max_ctx = max_context_len;
+  p.tile_tokens = a.tile_tokens;
+  p.tile_heads = a.tile_heads;
+  p.tile_rows = kChunkRows;
+  p.head_groups = a.head_groups;
+  p.members = a.members;
+  p.workers = a.workers;
+  p.whole = a.whole;
+  p.least = a.whole ? 1 : kChunkLeast;
+  p.negate = scale < 0.f;
+  p.c2 = positive_c2(scale);
+  if (debug_enabled())
+    fprintf(stderr, "[mqa_logits] %s Hq=%d Hkv=%d D=%d batch=%d tokens=%d bs=%d workers=%d tile=%d x %d whole=%d\n",
+            who, hq, hkv, d, batch, tokens, block_size, a.workers, a.tile_tokens, a.tile_heads, a.whole);
+  return hip_status(mqa::launch_chunk(d, q_type == MQA_F16, p, stream), who);
 }
 
 }  // extern "C"

@@ -121,6 +121,41 @@ struct AttnParams {
   float c2;                  // |scale| * log2(e)
 };
 
+// The tile that a worker of the chunk kernel ends and others began.
+struct ChunkNote {
+  int32_t worker, parts;     // first of its workers, and how many (0: no such tile)
+  int32_t token, head;       // its first row: (token, query head)
+  int32_t heads, rows;       // query heads of a token, and rows in all
+};
+
+struct ChunkParams {
+  const uint16_t* q;         // [tokens, Hq, D] bf16 or fp16 bits
+  int64_t q_stride;          // elements from one token to the next
+  const uint8_t* k;          // [num_blocks, bs, Hkv, D/2] packed e2m1
+  const uint8_t* k_sf;       // [num_blocks, bs, Hkv, D/32] e8m0
+  const uint8_t* v;
+  const uint8_t* v_sf;
+  const int32_t* ctx;        // [batch]
+  const int32_t* offsets;    // [batch + 1], or null (next_n tokens a sequence)
+  const int32_t* bt;         // [batch, bt_stride]
+  int64_t bt_stride;
+  uint16_t* out;             // [tokens, Hq, D], q's type
+  float* lse;                // [tokens, Hq] or null
+  float* part_o;             // [workers, 2, tile_rows, D]
+  float4* part_ml;           // [workers, 2, tile_rows] maximum (log2), sum, sum of the rounded
+  ChunkNote* notes;          // [workers], or null if no tile can be cut
+  int32_t batch, tokens, next_n;
+  int32_t kv_heads, group, q_heads;  // Hkv, Hq / Hkv, Hq
+  int32_t num_blocks, bs_shift, max_ctx;
+  int32_t tile_tokens, tile_heads, tile_rows;   // of a workgroup's tile of rows
+  int32_t head_groups, members;      // tiles beside each other on a KV head; on all of them
+  int32_t workers;           // workgroups
+  int32_t whole;             // tiles are never cut
+  int32_t least;             // steps that a worker takes at least, if there are that many
+  int32_t negate;            // scale < 0: the queries' signs are flipped
+  float c2;                  // |scale| * log2(e)
+};
+
 struct WriteParams {
   const void* x;             // rows of heads of D elements
   int64_t x_stride, x_head_stride;   // elements
@@ -146,6 +181,7 @@ struct SlotParams {
 };
 
 hipError_t launch_attention(int d, int f16, const AttnParams& p, hipStream_t s);
+hipError_t launch_chunk(int d, int f16, const ChunkParams& p, hipStream_t s);
 hipError_t launch_kv_write(int fmt, int d, int in_type, const WriteParams& p, hipStream_t s);
 hipError_t launch_kv_slots(const SlotParams& p, hipStream_t s);
 hipError_t launch_topk(int in_type, const TopkParams& p, hipStream_t s);

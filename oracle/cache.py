@@ -115,11 +115,31 @@ def attention(q, k_pool, k_sf_pool, v_pool, v_sf_pool, context_lens, block_table
     sum_j w_j |v_j| (e_j + max e + weight_step + (n / 64 + 100) 2^-22) and its
     rounding, and lse by max e + (n / 64 + 100) 2^-23 and its own rounding.
     """
+    _, seen = paged_row_ranges(context_lens, next_n, max_context_len)
+    return attend_rows(q, k_pool, k_sf_pool, v_pool, v_sf_pool, block_table,
+                       np.arange(len(seen)) // next_n, seen, scale, half_step, weight_step, indices)
+
+
+def chunk_rows(context_lens, token_offsets, tokens, max_context_len):
+    """(sequence, keys seen) of every row of q, -1 and 0 for rows that no sequence has: row t of
+    the n of a sequence sees min(ctx - n + 1 + t, max_context_len) keys."""
+    sequence, seen = np.full(tokens, -1), np.zeros(tokens, np.int64)
+    for b, ctx in enumerate(np.asarray(context_lens, np.int64)):
+        lo, hi = int(token_offsets[b]), int(token_offsets[b + 1])
+        for r in range(max(lo, 0), min(hi, tokens)):
+            sequence[r] = b
+            seen[r] = min(max(ctx - (hi - lo) + 1 + r - lo, 0), max(ctx, 0), max_context_len)
+    return sequence, seen
+
+
+def attend_rows(q, k_pool, k_sf_pool, v_pool, v_sf_pool, block_table, sequence, seen, scale,
+                half_step, weight_step, indices=None, weight_floor=0.0):
+    """attention() for rows of given sequences that see their first `seen` keys.  weight_floor:
+    the least rounding of a weight, relative to the row's largest one."""
     q = np.asarray(q, dtype=np.float64)
     rows, hq, d = q.shape
     bs, hkv = k_pool.shape[1], k_pool.shape[2]
     group = hq // hkv
-    _, seen = paged_row_ranges(context_lens, next_n, max_context_len)
     out, lse = np.zeros((rows, hq, d)), np.full((rows, hq), -np.inf)
     out_bound, lse_bound = np.zeros((rows, hq, d)), np.zeros((rows, hq))
     for r in range(rows):
@@ -130,7 +150,7 @@ def attention(q, k_pool, k_sf_pool, v_pool, v_sf_pool, context_lens, block_table
         n = keys.size
         if n == 0:
             continue
-        block = np.clip(np.asarray(block_table)[r // next_n, keys // bs], 0, len(k_pool) - 1)
+        block = np.clip(np.asarray(block_table)[sequence[r], keys // bs], 0, len(k_pool) - 1)
         at = block, keys % bs
         k = decode_cache(k_pool[at], k_sf_pool[at])
         v = decode_cache(v_pool[at], v_sf_pool[at])
@@ -148,7 +168,8 @@ def attention(q, k_pool, k_sf_pool, v_pool, v_sf_pool, context_lens, block_table
                 np.abs(s) + np.abs(s).max(-1, keepdims=True)) + 2.0 ** -20
             chain = (n / 64 + 100)
             worst = e.max(-1, keepdims=True)
-            out_bound[r, hs] = ((w * (e + worst + weight_step + chain * 2.0 ** -22)) @ np.abs(v[:, h])
+            out_bound[r, hs] = ((w * (e + worst + weight_step + chain * 2.0 ** -22)
+                                  + weight_floor * w.max(-1, keepdims=True)) @ np.abs(v[:, h])
                                 * (1 + 2 * half_step) + half_step * np.abs(out[r, hs]) + 2.0 ** -24)
             lse_bound[r, hs] = worst[:, 0] + chain * 2.0 ** -23 + 2.0 ** -22 * np.abs(lse[r, hs])
     return out, lse, out_bound, lse_bound
