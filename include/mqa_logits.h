@@ -404,10 +404,10 @@ mqa_status paged_attention(mqa_dtype dt, const void* q, mqa_float q_type, int64_
  *   dt, pools, context_lens, block_table, scale, out [tokens, Hq, D], lse
  *            [tokens, Hq]: as paged_attention, but n keys times the largest |v|
  *            must stay below 2^112.  Where they multiply V, weights are rounded
- *            to fp16 (2^-12 of themselves, or 2^-37 of the row's largest); in
- *            steps of 64 keys among which a scale of V is outside 2^-15 .. 2^9
- *            (or one of K, for fp16 queries), which take longer, to 2^-16.  out
- *            is divided by the sum of the rounded ones, lse is from the others
+ *            to fp16 (2^-12 of themselves, or 2^-37 of the row's largest); from a
+ *            scale of V outside 2^-22 .. 2^9 on (or one of K, for fp16 queries),
+ *            which takes longer, to 2^-16.  out is divided by the sum of the
+ *            rounded ones, lse is from the others
  *   workspace of at least paged_chunk_attention_workspace_size bytes for the same
  *            sizes (NULL if that is 0), 16-byte aligned, as paged_attention's.
  * Outputs and workspace must not overlap anything else.  Requires D in {64, 128},

@@ -216,13 +216,13 @@ AttnPlan plan_attention(int32_t batch, int32_t next_n, int32_t hq, int32_t hkv, 
   return a;
 }
 
-// A chunk call's split: tiles of up to 128 rows, each whole heads of a few tokens.
+// A chunk call's split: tiles of up to 256 rows, each whole heads of a few tokens.
 struct ChunkPlan {
   int32_t tile_heads, head_groups, members, tile_tokens;
   int32_t workers, whole;
   int64_t parts, bytes;
 };
-constexpr int32_t kChunkRows = 128, kChunkLeast = 4;
+constexpr int32_t kChunkRows = 256, kChunkLeast = 4;
 
 ChunkPlan plan_chunk(int32_t batch, int32_t tokens, int32_t hq, int32_t hkv, int32_t d,
                      int32_t max_context_len) {
@@ -235,7 +235,7 @@ ChunkPlan plan_chunk(int32_t batch, int32_t tokens, int32_t hq, int32_t hkv, int
   const int64_t tiles = std::min<int64_t>(tokens, ((int64_t)tokens + a.tile_tokens - 1) / a.tile_tokens + batch) * a.members;
   const int64_t most = std::max<int64_t>(((int64_t)max_context_len + 63) / 64, 1);
   a.whole = most <= 2 * kChunkLeast;
-  const int64_t limit = a.whole ? 65536 : mqa::kAttnResident;
+  const int64_t limit = a.whole ? 65536 : mqa::kChunkResident;
   a.workers = (int32_t)std::min(limit, a.whole || tiles >= limit ? tiles : std::max<int64_t>(tiles * most / kChunkLeast, 1));
   a.parts = a.whole ? 0 : (int64_t)a.workers * 2 * kChunkRows;
   a.bytes = a.whole ? 0 : a.parts * (d + 4) * 4 + (int64_t)a.workers * (int64_t)sizeof(mqa::ChunkNote);

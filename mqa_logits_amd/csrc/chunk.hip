@@ -22,21 +22,21 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kKeys = 64;                    // of a step
 constexpr int kStage = 16384;                // keys whose places LDS holds at a time
 constexpr uint32_t kLastScale = 252;         // bytes above could overflow fp32: they count as NaN
-// Scale bytes (2^-15 .. 2^9) whose steps are worked on in fp16.  Every e2m1 value
-// under 2^-23 .. 2^13 is exact there; the narrower range bounds what the weights'
+// Scale bytes (2^-22 .. 2^9) whose steps are worked on in fp16.  Every e2m1 value
+// under 2^-23 .. 2^13 is exact there; large ones are left out for what the weights'
 // own end costs, see kRoom.
-constexpr uint32_t kHalfLow = 112, kHalfHigh = 136;
+constexpr uint32_t kHalfLow = 105, kHalfHigh = 136;
 // The running maximum is set kRoom octaves below the largest score, and follows a
-// new one only when that leaves a weight above kMost (fp16 ends at 65504); most
-// steps rescale nothing.  The largest weight is then between 2^kRoom and kMost,
+// new one only when that leaves a weight above 2^kMost (fp16 ends at 65504); most
+// steps rescale nothing.  The largest weight is then between 2^kRoom and 2^kMost,
 // and half a step of fp16's least subnormal is 2^-37 of it at most.  The
 // unnormalised sums of n keys stay within n * 2^15 times the largest value.
-constexpr float kRoom = 12.f, kMost = 32768.f;
+constexpr float kRoom = 12.f, kMost = 15.f;
 constexpr float kLowest = -0x1.fffffep127f;  // a maximum before any key (finite: no inf - inf)
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -255,98 +255,116 @@ struct Stage {
   static constexpr int kBytes = kKeys * kKeyPitch + D * kValPitch;
 };
 
-// What a thread loads of a step: D/4 bytes of codes of one key and their scale,
-// and D/32 bytes of codes of V of four keys and theirs.
-template <int D>
+// What a thread loads of a step.  The first half of the workgroup takes D/8 bytes
+// of codes of a key each and their scale; the second D/32 bytes of V's codes of four
+// keys and their scales.
 struct Raw {
-  u32x4 k;                 // (D = 64: x, y)
-  uint32_t v[4];
-  uint32_t ks, vs[4];
+  u32x4 codes;
+  uint32_t scales[4];
 };
 
 template <int D>
 struct Loader {
   const ChunkParams& p;
-  const uint32_t* places;  // pool slot of every 16th key
-  int kv_head;
+  const uint32_t* places;  // first block (of 32 elements) of every 16th key
+  uint32_t key_blocks;     // blocks from one key of the pool to the next
 
-  __device__ __forceinline__ uint64_t row(int key) const {
-    const uint32_t slot = places[key >> 4] + (key & 15);
-    return (uint64_t)slot * p.kv_heads + kv_head;
-  }
   // key0: the step's first key, from the stage's; n: keys of the context from there on
-  __device__ __forceinline__ void load(Raw<D>& r, int tid, int key0, int n) const {
-    {
+  template <bool KEYS>
+  __device__ __forceinline__ void load(Raw& r, int tid, int key0, int n) const {
+    if constexpr (KEYS) {
       const int j = tid >> 2, c = tid & 3;
-      const uint64_t at = row(key0 + j);
-      const uint8_t* src = p.k + at * (D / 2) + c * (D / 8);
+      const uint32_t block = places[(key0 + j) >> 4] + (j & 15) * key_blocks;
+      const uint8_t* src = p.k + ((uint64_t)block << 4) + c * (D / 8);
       if constexpr (D == 128) {
-        r.k = *reinterpret_cast<const u32x4*>(src);
+        r.codes = *reinterpret_cast<const u32x4*>(src);
       } else {
         const u32x2 x = *reinterpret_cast<const u32x2*>(src);
-        r.k = u32x4{x[0], x[1], 0u, 0u};
+        r.codes = u32x4{x[0], x[1], 0u, 0u};
       }
-      const uint32_t s = p.k_sf[at * (D / 32) + c * (D / 4) / 32];
-      r.ks = j < n ? s : 127u;               // (any finite one where nothing is stored)
-    }
-    const int j = (tid >> 4) * 4, c = tid & 15;
+      const uint32_t s = p.k_sf[(uint64_t)block + c * (D / 4) / 32];
+      r.scales[0] = j < n ? s : 127u;        // (any finite one where nothing is stored)
+    } else {
+      const int j = Values::key(tid), c = Values::column(tid);
+      const uint32_t first = places[(key0 + j) >> 4] + (j & 15) * key_blocks;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint64_t at = row(key0 + j + i);
-      const uint8_t* src = p.v + at * (D / 2) + c * (D / 32);
-      r.v[i] = D == 128 ? *reinterpret_cast<const uint32_t*>(src) : *reinterpret_cast<const uint16_t*>(src);
-      const uint32_t s = p.v_sf[at * (D / 32) + c * (D / 16) / 32];
-      r.vs[i] = j + i < n ? s : 127u;
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t block = first + i * key_blocks;
+        const uint8_t* src = p.v + ((uint64_t)block << 4) + c * (D / 32);
+        r.codes[i] = D == 128 ? *reinterpret_cast<const uint32_t*>(src) : *reinterpret_cast<const uint16_t*>(src);
+        const uint32_t s = p.v_sf[(uint64_t)block + c * (D / 16) / 32];
+        r.scales[i] = j + i < n ? s : 127u;
+      }
     }
   }
+
+  // The second half's keys and columns: 16 lanes in a row write all banks.
+  struct Values {
+    __device__ __forceinline__ static int quad(int tid) { return (tid & 3) | (tid >> 6 & 3) << 2; }
+    __device__ __forceinline__ static int key(int tid) { return quad(tid) * 4; }
+    __device__ __forceinline__ static int column(int tid) { return tid >> 2 & 15; }
+  };
 };
 
-// K as rows of D, V transposed: row D/32 * ... of the products' order, see Rows.
-template <int D, bool KHALF, bool VHALF>
-__device__ __forceinline__ void put(const Raw<D>& r, int tid, char* lds) {
-  {
-    char* dst = lds + (tid >> 2) * Stage<D>::kKeyPitch + (tid & 3) * (D / 2);
-    const float s = scale_of(r.ks);
+// K as rows of D (KEYS), or V transposed, into a step's LDS.
+template <int D, bool KEYS, bool HALF>
+__device__ __forceinline__ void put(const Raw& r, int tid, char* lds) {
+  if constexpr (KEYS) {
+    const int c = tid & 3;
+    char* dst = lds + (tid >> 2) * Stage<D>::kKeyPitch + c * (D / 2);
+    const float s = scale_of(r.scales[0]);
+    if constexpr (D == 128) {
+      // half of the lanes the other way round: 8 in a row write all banks
+      const int turn = c & 2;
+      const u32x4 x = turn ? u32x4{r.codes[2], r.codes[3], r.codes[0], r.codes[1]} : r.codes;
+      char* one = dst + turn * 16;
+      char* two = dst + (turn ^ 2) * 16;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) *reinterpret_cast<u32x4*>(dst + i * 16) = cvt_eight<KHALF>(r.k[i], s);
-  }
-  // element e of the thread's D/16 is row e % (D/32) * 32 + 2 c + e / (D/32); four
-  // keys are one half of what a lane multiplies of 16
-  const int quad = tid >> 4, c = tid & 15;
-  char* dst = lds + kKeys * Stage<D>::kKeyPitch + 2 * c * Stage<D>::kValPitch + (quad >> 2) * 32 +
-              (quad & 1) * 16 + (quad >> 1 & 1) * 8;
-  float s[4];
+      for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(one + i * 16) = cvt_eight<HALF>(x[i], s);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) s[i] = scale_of(r.vs[i]);
-  const auto two = [&](auto sel) {
-    constexpr int SEL = decltype(sel)::value;
-    uint32_t x[4];
+      for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(two + i * 16) = cvt_eight<HALF>(x[i + 2], s);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = cvt_pair<VHALF, SEL>(r.v[i], s[i]);
-#pragma unroll
-    for (int odd = 0; odd < 2; ++odd) {
-      constexpr int kCols = D / 32;
-      const int e = 2 * SEL + odd, at = e % kCols * 32 + e / kCols;
-      const uint32_t pick = odd ? 0x07060302u : 0x05040100u;
-      *reinterpret_cast<u32x2*>(dst + at * Stage<D>::kValPitch) =
-          u32x2{__builtin_amdgcn_perm(x[1], x[0], pick), __builtin_amdgcn_perm(x[3], x[2], pick)};
+      for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(dst + i * 16) = cvt_eight<HALF>(r.codes[i], s);
     }
-  };
-  two(std::integral_constant<int, 0>{});
-  two(std::integral_constant<int, 1>{});
-  if constexpr (D == 128) {
-    two(std::integral_constant<int, 2>{});
-    two(std::integral_constant<int, 3>{});
+  } else {
+    // element e of the thread's D/16 is row e % (D/32) * 32 + 2 c + e / (D/32); four
+    // keys are one half of what a lane multiplies of 16
+    const int quad = Loader<D>::Values::quad(tid), c = Loader<D>::Values::column(tid);
+    char* dst = lds + kKeys * Stage<D>::kKeyPitch + 2 * c * Stage<D>::kValPitch + (quad >> 2) * 32 +
+                (quad & 1) * 16 + (quad >> 1 & 1) * 8;
+    float s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = scale_of(r.scales[i]);
+    const auto two = [&](auto sel) {
+      constexpr int SEL = decltype(sel)::value;
+      uint32_t x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = cvt_pair<HALF, SEL>(r.codes[i], s[i]);
+#pragma unroll
+      for (int odd = 0; odd < 2; ++odd) {
+        constexpr int kCols = D / 32;
+        const int e = 2 * SEL + odd, at = e % kCols * 32 + e / kCols;
+        const uint32_t pick = odd ? 0x07060302u : 0x05040100u;
+        *reinterpret_cast<u32x2*>(dst + at * Stage<D>::kValPitch) =
+            u32x2{__builtin_amdgcn_perm(x[1], x[0], pick), __builtin_amdgcn_perm(x[3], x[2], pick)};
+      }
+    };
+    two(std::integral_constant<int, 0>{});
+    two(std::integral_constant<int, 1>{});
+    if constexpr (D == 128) {
+      two(std::integral_constant<int, 2>{});
+      two(std::integral_constant<int, 3>{});
+    }
   }
 }
 
-template <int D, bool F16>
-__device__ __forceinline__ bool wide_scales(const Raw<D>& r) {
+// Some scale is outside what the fp16 (or, for bf16 queries, K's bf16) products take.
+template <bool KEYS, bool F16>
+__device__ __forceinline__ bool wide_scales(const Raw& r) {
   const auto wide = [](uint32_t s) { return s - kHalfLow > kHalfHigh - kHalfLow; };
-  bool w = F16 ? wide(r.ks) : r.ks > kLastScale;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w |= wide(r.vs[i]);
-  return w;
+  if constexpr (KEYS) return F16 ? wide(r.scales[0]) : r.scales[0] > kLastScale;
+  return wide(r.scales[0]) || wide(r.scales[1]) || wide(r.scales[2]) || wide(r.scales[3]);
 }
 
 // ---------------------------------------------------------------------------
@@ -377,18 +395,19 @@ struct Rows {
   }
 
   // One step.  WIDE: some scale is outside fp16's range; LDS holds bf16.
-  __device__ __forceinline__ void step(const char* lds, int key0, bool masked, float c2) {
-    part<false, 2>(lds, 0, key0, masked, c2);
+  template <bool MASKED>
+  __device__ __forceinline__ void step(const char* lds, int key0, float c2) {
+    part<false, MASKED, 2>(lds, 0, key0, c2);
   }
   __device__ __forceinline__ void wide_step(const char* lds, int key0, float c2) {
 #pragma nounroll
-    for (int h = 0; h < 2; ++h) part<true, 1>(lds, h, key0, true, c2);
+    for (int h = 0; h < 2; ++h) part<true, true, 1>(lds, h, key0, c2);
   }
 
   // H halves of 32 keys of it.
-  template <bool WIDE, int H>
-  __device__ __forceinline__ void part(const char* lds, int first, int key0, bool masked, float c2) {
-    const int lane = here_only(threadIdx.x & 63), half = lane >> 5;
+  template <bool WIDE, bool MASKED, int H>
+  __device__ __forceinline__ void part(const char* lds, int first, int key0, float c2) {
+    const int lane = WIDE || MASKED ? here_only(threadIdx.x & 63) : threadIdx.x & 63, half = lane >> 5;
     const char* keys = lds + (first * 32 + (lane & 31)) * Stage<D>::kKeyPitch + half * 16;
     const char* vals = lds + kKeys * Stage<D>::kKeyPitch + (lane & 31) * Stage<D>::kValPitch + half * 16 + first * 64;
     f32x16 s[QT][H];
@@ -399,42 +418,51 @@ struct Rows {
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[t][h][i] = 0.f;
     // A product must not overlap its operands.  The compiler was seen to let one
-    // with a constant 0 to add to overlap them; here the zeros are registers, and
-    // its other products are checked in the generated code.
+    // with a constant 0 to add to overlap them: the operands are used once more
+    // behind it, or (here) the zeros are registers.
     if (WIDE) asm volatile("" : "+v"(s[0][0]));
+    // operands are read kAhead products before their use
+    constexpr int kAhead = 4;
+    const auto key_operand = [&](int n) {
+      return *reinterpret_cast<const u32x4*>(keys + n % H * 32 * Stage<D>::kKeyPitch + n / H * 32);
+    };
+    u32x4 a[kAhead];
 #pragma unroll
-    for (int st = 0; st < kSteps; ++st)
+    for (int n = 0; n < kAhead; ++n) a[n] = key_operand(n);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
-        const u32x4 a = *reinterpret_cast<const u32x4*>(keys + h * 32 * Stage<D>::kKeyPitch + st * 32);
+    for (int n = 0; n < H * kSteps; ++n) {
+      const int st = n / H, h = n % H;
 #pragma unroll
-        for (int t = 0; t < QT; ++t) {
-          if constexpr (WIDE && F16) {
-            // the query's two exact bf16 parts; an infinity stays in the first alone
-            u32x4 hi, lo;
+      for (int t = 0; t < QT; ++t) {
+        if constexpr (WIDE && F16) {
+          // the query's two exact bf16 parts; an infinity stays in the first alone
+          u32x4 hi, lo;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const f16x2 x = __builtin_bit_cast(f16x2, here_only(q[t][st][i]));
-              const float y = (float)x[0], z = (float)x[1];
-              hi[i] = pack_bf16(y, z);
-              const float ry = y - bf16_lo(hi[i]), rz = z - bf16_hi(hi[i]);
-              lo[i] = pack_bf16(__builtin_isfinite(y) ? ry : 0.f, __builtin_isfinite(z) ? rz : 0.f);
-            }
-            s[t][h] = mma<false>(a, hi, s[t][h]);
-            s[t][h] = mma<false>(a, lo, s[t][h]);
-            __builtin_amdgcn_sched_barrier(0);
-          } else {
-            s[t][h] = mma<F16>(a, q[t][st], s[t][h]);
+          for (int i = 0; i < 4; ++i) {
+            const f16x2 x = __builtin_bit_cast(f16x2, here_only(q[t][st][i]));
+            const float y = (float)x[0], z = (float)x[1];
+            hi[i] = pack_bf16(y, z);
+            const float ry = y - bf16_lo(hi[i]), rz = z - bf16_hi(hi[i]);
+            lo[i] = pack_bf16(__builtin_isfinite(y) ? ry : 0.f, __builtin_isfinite(z) ? rz : 0.f);
           }
+          s[t][h] = mma<false>(a[n % kAhead], hi, s[t][h]);
+          s[t][h] = mma<false>(a[n % kAhead], lo, s[t][h]);
+        } else {
+          s[t][h] = mma<F16>(a[n % kAhead], q[t][st], s[t][h]);
         }
       }
-    // The compiler was seen to read a product's result right behind a branch,
-    // before it is there; ahead of a branch, the products end here.
+      __builtin_amdgcn_sched_barrier(0);
+      if (n < H) asm volatile("" ::"v"(a[n % kAhead]));   // still its own behind the product
+      if (n + kAhead < H * kSteps) a[n % kAhead] = key_operand(n + kAhead);
+    }
+    const auto value_operand = [&](int n) {
+      return *reinterpret_cast<const u32x4*>(vals + n % kCols * 32 * Stage<D>::kValPitch + n / kCols * 32);
+    };
 #pragma unroll
-    for (int t = 0; t < QT; ++t)
-#pragma unroll
-      for (int h = 0; h < H; ++h) asm volatile("s_nop 7\n\ts_nop 7" : "+v"(s[t][h]));
-    if (masked) {
+    for (int n = 0; n < kAhead; ++n) a[n] = value_operand(n);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (MASKED) {
 #pragma unroll
       for (int t = 0; t < QT; ++t)
 #pragma unroll
@@ -448,35 +476,27 @@ struct Rows {
     u32x4 w[QT][WIDE ? 2 : 1][2 * H];        // [high and low part][16 keys]
 #pragma unroll
     for (int t = 0; t < QT; ++t) weights<WIDE, H>(s[t], t, c2, w[t]);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int k = 0; k < 2 * H; ++k)
+    for (int n = 0; n < 2 * H * kCols; ++n) {
+      const int k = n / kCols, c = n % kCols;
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) {
-        const u32x4 a = *reinterpret_cast<const u32x4*>(vals + c * 32 * Stage<D>::kValPitch + k * 32);
+      for (int t = 0; t < QT; ++t)
 #pragma unroll
-        for (int t = 0; t < QT; ++t)
-#pragma unroll
-          for (int x = 0; x < (WIDE ? 2 : 1); ++x) o[t][c] = mma<!WIDE>(a, w[t][x][k], o[t][c]);
-      }
+        for (int x = 0; x < (WIDE ? 2 : 1); ++x) o[t][c] = mma<!WIDE>(a[n % kAhead], w[t][x][k], o[t][c]);
+      if (n + kAhead < 2 * H * kCols) a[n % kAhead] = value_operand(n + kAhead);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
 
   // Weights relative to the running maximum m.
   template <bool WIDE, int H>
   __device__ __forceinline__ void weights(const f32x16 (&s)[H], int t, float c2, u32x4 (&w)[WIDE ? 2 : 1][2 * H]) {
-    float x[16 * H];
-    const auto form = [&] {
+    float best = s[0][0];
 #pragma unroll
-      for (int i = 0; i < 16 * H; ++i) x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 4][i & 15], c2, -m[t]));
-    };
-    form();
-    float most = x[0];
-#pragma unroll
-    for (int i = 1; i < 16 * H; ++i) most = fmaxf(most, x[i]);
-    if (__builtin_expect(__any(most > kMost), 0)) {
+    for (int i = 1; i < 16 * H; ++i) best = fmaxf(best, s[i >> 4][i & 15]);
+    if (__builtin_expect(__any(__builtin_fmaf(best, c2, -m[t]) > kMost), 0)) {
       asm volatile("");                      // rare: nothing of it belongs before the branch
-      float best = s[0][0];
-#pragma unroll
-      for (int i = 1; i < 16 * H; ++i) best = fmaxf(best, s[i >> 4][i & 15]);
       best = fmaxf(best, __shfl_xor(best, 32)) * c2;
       const float next = fmaxf(m[t], best - kRoom);
       const float f = __builtin_amdgcn_exp2f(m[t] - next);
@@ -487,8 +507,10 @@ struct Rows {
       for (int c = 0; c < kCols; ++c)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[t][c][i] *= f;
-      form();
     }
+    float x[16 * H];
+#pragma unroll
+    for (int i = 0; i < 16 * H; ++i) x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 4][i & 15], c2, -m[t]));
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 16 * H; i += 4) sum += (x[i] + x[i + 1]) + (x[i + 2] + x[i + 3]);
@@ -509,12 +531,89 @@ struct Rows {
   }
 };
 
-template <int D, int QT, bool F16>
-__global__ void __launch_bounds__(kThreads, QT == 1 ? 2 : 1)
+// The steps of a stage, for a wave of the half that loads K (KEYS) or V.
+template <bool KEYS, int D, int QT, bool F16, class InContext>
+__device__ __forceinline__ void walk(const Loader<D>& loader, Rows<D, QT, F16>& rows,
+                                     char (&stage)[2][Stage<D>::kBytes], int* flags, uint8_t (&nan_marks)[2][kKeys][4],
+                                     int stage0, int steps, int least, const InContext& in_context, float c2) {
+  const int tid = threadIdx.x & (kThreads / 2 - 1);
+  constexpr bool kHalf = KEYS ? F16 : true;
+  Raw raw;
+  const auto store = [&](int i) {
+    const int me = here_only(tid);
+    if (wide_scales<KEYS, F16>(raw)) flags[i & 1] = i;
+    put<D, KEYS, kHalf>(raw, me, stage[i & 1]);
+  };
+  const auto fetch = [&](int i) { loader.template load<KEYS>(raw, here_only(tid), i * kKeys, in_context(i)); };
+  fetch(0);
+  store(0);
+  fetch(min(1, steps - 1));
+  __syncthreads();
+  // Steps whose keys all rows see, then those at the rows' own ends.  (Past the
+  // last step, the last again is stored and never used.)
+  const int clear = min(max(least - stage0, 0) / kKeys, steps);
+  int i = 0;
+  const auto narrow = [&] { return __builtin_amdgcn_readfirstlane(flags[i & 1]) != i; };
+  const auto turn = [&] {
+    store(i + 1);
+    fetch(min(i + 2, steps - 1));
+    ++i;
+    __syncthreads();
+  };
+#pragma nounroll
+  while (i < clear && narrow()) {
+    rows.template step<false>(stage[i & 1], 0, c2);
+    turn();
+  }
+#pragma nounroll
+  while (i < steps && narrow()) {
+    rows.template step<true>(stage[i & 1], stage0 + i * kKeys, c2);
+    turn();
+  }
+  if (__builtin_expect(i == steps, 1)) return;
+  // from a step with unusual scales on, in bf16, NaN scales apart
+  loader.template load<KEYS>(raw, here_only(tid), i * kKeys, in_context(i));
+#pragma nounroll
+  for (; i < steps; ++i) {
+    const int me = here_only(tid);
+    if constexpr (KEYS) {
+      if (raw.scales[0] > kLastScale) raw.scales[0] = 255;
+    } else {
+      const int c = Loader<D>::Values::column(me), b = c * (D / 16) / 32;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool bad = raw.scales[j] > kLastScale;
+        if (c % (512 / D) == 0) nan_marks[i & 1][Loader<D>::Values::key(me) + j][b] = bad;
+        raw.scales[j] = bad ? 0u : raw.scales[j];
+      }
+    }
+    __syncthreads();                         // the stage's last use is over
+    put<D, KEYS, false>(raw, me, stage[i & 1]);
+    __syncthreads();
+    loader.template load<KEYS>(raw, here_only(tid), min(i + 1, steps - 1) * kKeys, in_context(min(i + 1, steps - 1)));
+    const int key0 = stage0 + i * kKeys;
+    uint32_t marks = 0;
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b) marks |= (uint32_t)nan_marks[i & 1][me & 63][b] << b;
+    if (__builtin_expect(__any(marks != 0), 0))
+#pragma nounroll
+      for (int j = 0; j < kKeys; ++j) {
+        const uint32_t word = __shfl(marks, j);
+#pragma unroll
+        for (int t = 0; t < QT; ++t)
+          if (key0 + j < rows.seen[t]) rows.nan_blocks[t] |= word;
+      }
+    rows.wide_step(stage[i & 1], key0, c2);
+  }
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 2)
 chunk_kernel(const ChunkParams p) {
+  constexpr int QT = 1;
   __shared__ __attribute__((aligned(16))) char stage[2][Stage<D>::kBytes];
   __shared__ uint32_t places[kStage / 16];
-  __shared__ uint32_t nan_words[kKeys];
+  __shared__ uint8_t nan_marks[2][kKeys][4];
   __shared__ int flags[2];
   __shared__ int64_t sums[kWaves], found[2];
 
@@ -545,28 +644,24 @@ chunk_kernel(const ChunkParams p) {
     const int end = p.whole ? tile_seen
                             : (int)min((int64_t)tile_seen, (min(tile_end, piece.end) - piece.tile_begin) * kKeys);
     const int wave_row = wave * 32 * QT;
-    const bool works = wave_row < n_rows;
-    int least = 0, most = 0;                 // keys that all, and that some, of the wave's rows see
+    const int least = s.seen(token0);        // keys that all rows see
     rows.clear();
-    if (works) {
-      least = s.seen(token0 + wave_row / heads);
-      most = s.seen(token0 + min(wave_row + 32 * QT, n_rows) / heads);
 #pragma unroll
-      for (int t = 0; t < QT; ++t) {
-        // lanes past the last row repeat it; their results are dropped
-        const int r = min(wave_row + t * 32 + (lane & 31), n_rows - 1);
-        const int at = r / heads;
-        rows.seen[t] = s.seen(token0 + at);
-        const uint16_t* src = p.q + (int64_t)(s.first + token0 + at) * p.q_stride + (head0 + r - at * heads) * D + half * 8;
+    for (int t = 0; t < QT; ++t) {
+      // lanes past the last row repeat it; their results are dropped
+      const int r = min(wave_row + t * 32 + (lane & 31), n_rows - 1);
+      const int at = r / heads;
+      rows.seen[t] = s.seen(token0 + at);
+      const uint16_t* src = p.q + (int64_t)(s.first + token0 + at) * p.q_stride + (head0 + r - at * heads) * D + half * 8;
 #pragma unroll
-        for (int st = 0; st < D / 16; ++st) {
-          rows.q[t][st] = *reinterpret_cast<const u32x4*>(src + st * 16);
-          if (p.negate) rows.q[t][st] ^= 0x80008000u;
-        }
+      for (int st = 0; st < D / 16; ++st) {
+        rows.q[t][st] = *reinterpret_cast<const u32x4*>(src + st * 16);
+        if (p.negate) rows.q[t][st] ^= 0x80008000u;
       }
     }
     const int32_t* table = p.bt + (int64_t)piece.b * p.bt_stride;
-    const Loader<D> loader{p, places, kv_head};
+    const uint32_t key_blocks = p.kv_heads * (D / 32);
+    const Loader<D> loader{p, places, key_blocks};
     for (int stage0 = begin; stage0 < end; stage0 += kStage) {
       const int stage_end = min(end, stage0 + kStage), n = stage_end - stage0;
       const int steps = (n + kKeys - 1) / kKeys;
@@ -574,66 +669,24 @@ chunk_kernel(const ChunkParams p) {
       for (int i = tid; i < steps * (kKeys / 16); i += kThreads) {
         const int j = min(stage0 + i * 16, s.cap - 1);
         const int id = min(max(table[j >> p.bs_shift], 0), p.num_blocks - 1);
-        places[i] = ((uint32_t)id << p.bs_shift) + (stage0 + i * 16 & (1 << p.bs_shift) - 1);
+        const uint32_t slot = ((uint32_t)id << p.bs_shift) + (stage0 + i * 16 & (1 << p.bs_shift) - 1);
+        places[i] = slot * key_blocks + kv_head * (D / 32);
       }
       if (tid < 2) flags[tid] = -1;
       __syncthreads();
       const auto in_context = [&](int i) { return s.cap - stage0 - i * kKeys; };
-      Raw<D> raw;
-      loader.load(raw, here_only(tid), 0, in_context(0));
-      if (wide_scales<D, F16>(raw)) flags[0] = 0;
-      put<D, F16, true>(raw, here_only(tid), stage[0]);
-      if (steps > 1) loader.load(raw, here_only(tid), kKeys, in_context(1));
-      __syncthreads();
-#pragma nounroll
-      for (int i = 0; i < steps; ++i) {
-        char* here = stage[i & 1];
-        const int key0 = stage0 + i * kKeys;
-        const bool wide = __builtin_amdgcn_readfirstlane(flags[i & 1]) == i;
-        const bool use = works && key0 < most;
-        if (__builtin_expect(wide, 0)) {
-          // rare: the step anew, in bf16, with its NaN scales apart
-          const int me = here_only(tid);
-          Raw<D> again;
-          loader.load(again, me, i * kKeys, in_context(i));
-          __syncthreads();                   // the flag is read
-          if (me < kKeys) nan_words[me] = 0;
-          __syncthreads();
-          if (again.ks > kLastScale) again.ks = 255;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (again.vs[j] > kLastScale) {
-              atomicOr(&nan_words[(me >> 4) * 4 + j], 1u << ((me & 15) * (D / 16) / 32));
-              again.vs[j] = 0;
-            }
-          put<D, false, false>(again, me, here);
-          __syncthreads();
-          for (int j = 0; j < kKeys; ++j) {
-            const uint32_t word = nan_words[j];
-#pragma unroll
-            for (int t = 0; t < QT; ++t)
-              if (key0 + j < rows.seen[t]) rows.nan_blocks[t] |= word;
-          }
-          if (use) rows.wide_step(here, key0, p.c2);
-        } else if (use) {
-          rows.step(here, key0, key0 + kKeys > least, p.c2);
-        }
-        if (i + 1 < steps) {
-          if (wide_scales<D, F16>(raw)) flags[i + 1 & 1] = i + 1;
-          put<D, F16, true>(raw, here_only(tid), stage[i + 1 & 1]);
-          if (i + 2 < steps) loader.load(raw, here_only(tid), (i + 2) * kKeys, in_context(i + 2));
-        }
-        __syncthreads();
-      }
+      if (wave < kWaves / 2)
+        walk<true>(loader, rows, stage, flags, nan_marks, stage0, steps, least, in_context, p.c2);
+      else
+        walk<false>(loader, rows, stage, flags, nan_marks, stage0, steps, least, in_context, p.c2);
     }
 
     const bool first_part = piece.at == piece.tile_begin, last_part = tile_end <= piece.end;
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-      if (!works) break;
       const float m = rows.m[t], l = rows.l[t] + __shfl_xor(rows.l[t], 32);
       const float rounded = rows.r[t] + __shfl_xor(rows.r[t], 32);
-      const int r = wave_row + t * 32 + (lane & 31);
+      const int r = here_only(wave_row + t * 32 + (lane & 31));
 #pragma unroll
       for (int c = 0; c < D / 32; ++c)
 #pragma unroll
@@ -741,7 +794,7 @@ chunk_join_kernel(const ChunkParams p) {
 
 template <int D, bool F16>
 hipError_t launch(const ChunkParams& p, hipStream_t s) {
-  chunk_kernel<D, 1, F16><<<(uint32_t)((p.workers + 7) / 8 * 8), kThreads, 0, s>>>(p);
+  chunk_kernel<D, F16><<<(uint32_t)((p.workers + 7) / 8 * 8), kThreads, 0, s>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.notes) return e;
   constexpr int kRows = 256 / (D / 4);

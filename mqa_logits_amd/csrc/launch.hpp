@@ -128,6 +128,9 @@ struct ChunkNote {
   int32_t heads, rows;       // query heads of a token, and rows in all
 };
 
+// Chunk workgroups the chip holds at a time: one per compute unit.
+constexpr int kChunkResident = 256;
+
 struct ChunkParams {
   const uint16_t* q;         // [tokens, Hq, D] bf16 or fp16 bits
   int64_t q_stride;          // elements from one token to the next
