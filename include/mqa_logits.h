@@ -426,6 +426,90 @@ mqa_status paged_chunk_attention(mqa_dtype dt, const void* q, mqa_float q_type, 
                                  int32_t block_size, int32_t num_blocks, int32_t max_context_len,
                                  hipStream_t stream);
 
+/*
+ * The attention weight that every cached token has gathered: what the rows of q,
+ * of a chunk or of a decoding step, give to each key, added to what it had.
+ *   out[b, j] = weights[b, j] + sum over rows r of sequence b that see key j, and
+ *               over query heads h, of exp(scale <q[r, h], k[j, h / (Hq / Hkv)]> - lse[r, h])
+ *   for j < min(ctx_b, max_context_len), and 0 behind.
+ *   q, dt, k_pool, k_sf_pool, context_lens, token_offsets, block_table, scale:
+ *            as paged_chunk_attention (the same rows see the same keys)
+ *   lse      [tokens, Hq] fp32, as paged_attention and paged_chunk_attention
+ *            write it; rows of -inf (no keys) give nothing, and rows may be left
+ *            out that way
+ *   weights  [batch, weights_stride] fp32, or NULL (0)
+ *   out      [batch, out_stride] fp32; it may be `weights` itself.  Columns from
+ *            max_context_len on are not written
+ *   workspace of at least paged_attention_weights_workspace_size bytes for the
+ *            same sizes (NULL if that is 0), 16-byte aligned.
+ * Scores and sums are fp32, added in an order that only the sizes decide.
+ * Requires what paged_chunk_attention does.
+ */
+int64_t paged_attention_weights_workspace_size(int32_t batch, int32_t tokens, int32_t hq, int32_t hkv,
+                                               int32_t d, int32_t max_context_len);  /* bytes; negative on error */
+mqa_status paged_attention_weights(mqa_dtype dt, const void* q, mqa_float q_type, int64_t q_stride,
+                                   const float* lse, const uint8_t* k_pool, const uint8_t* k_sf_pool,
+                                   const int32_t* context_lens, const int32_t* token_offsets,
+                                   const int32_t* block_table, int64_t block_table_stride, float scale,
+                                   const float* weights, int64_t weights_stride, float* out,
+                                   int64_t out_stride, void* workspace, int64_t workspace_bytes,
+                                   int32_t batch, int32_t tokens, int32_t hq, int32_t hkv, int32_t d,
+                                   int32_t block_size, int32_t num_blocks, int32_t max_context_len,
+                                   hipStream_t stream);
+
+/* A pool of the paged cache, [num_blocks, block_size] tokens of token_bytes each. */
+typedef struct {
+  void* data;
+  int64_t token_bytes;   /* at most 2^24 */
+} mqa_pool;
+
+/*
+ * Eviction: sequences longer than `keep` tokens are cut to them.  Of the n =
+ * clamp(ctx_b, 0, max_context_len) tokens of such a sequence stay the last
+ * `recent`, and of those before them the keep - recent with the largest weight
+ * (in the order of mqa_logits_topk, so equal ones by position; a weight of -inf
+ * is never chosen, and then fewer may stay).  They are copied, in order, to
+ * blocks taken from free_blocks, in every pool; the old blocks are not written,
+ * so other sequences may share them.
+ *   weights  [batch, weights_stride] fp32, as paged_attention_weights gathers them
+ *   context_lens [batch], block_table [batch, block_table_stride] int32: read
+ *   free_blocks [num_free] int32: ids of free blocks, in the order to take them.
+ *            A sequence that the list does not suffice for, after the longer ones
+ *            before it, stays as it is, and so do the others behind the end
+ *   pools    [num_pools] (host memory, read before the call returns), at most 16
+ *   new_context_lens [batch] int32: tokens afterwards
+ *   new_block_table [batch, new_block_table_stride] int32: entries for them, and
+ *            -1 up to ceil(max_context_len / block_size); the old entries of
+ *            sequences that stay as they are
+ *   new_weights [batch, new_weights_stride] fp32: the weights of the tokens that
+ *            stay, in order, and 0 up to max_context_len
+ *   kept     [batch, kept_stride] int32: the old positions of the tokens that
+ *            stay, in order, -1 up to `keep` (throughout for a longer sequence
+ *            that had to stay as it is)
+ *   freed_blocks [batch * ceil(max_context_len / block_size)] int32: the old
+ *            blocks of the sequences that were cut, sequence after sequence, and
+ *            -1 behind them (a block that two of them share is listed twice)
+ *   counts   [2] int32: blocks asked of the free list (more than num_free: it did
+ *            not suffice), blocks in freed_blocks
+ *   workspace of at least paged_kv_evict_workspace_size bytes, 16-byte aligned.
+ * Tokens whose old or new block id lies outside [0, num_blocks) are not copied.
+ * Nothing that is written may overlap anything else, free blocks no block of a
+ * sequence.  Requires 1 <= batch <= 8192, block_size in {16, 32, 64}, 1 <= keep,
+ * 0 <= recent <= keep, batch * max_context_len and batch * keep below 2^31,
+ * num_blocks * block_size < 2^31.
+ */
+int64_t paged_kv_evict_workspace_size(int32_t batch);  /* bytes; negative on error */
+mqa_status paged_kv_evict(const float* weights, int64_t weights_stride, const int32_t* context_lens,
+                          const int32_t* block_table, int64_t block_table_stride,
+                          const int32_t* free_blocks, int32_t num_free, const mqa_pool* pools,
+                          int32_t num_pools, int32_t* new_context_lens, int32_t* new_block_table,
+                          int64_t new_block_table_stride, float* new_weights,
+                          int64_t new_weights_stride, int32_t* kept, int64_t kept_stride,
+                          int32_t* freed_blocks, int32_t* counts, void* workspace,
+                          int64_t workspace_bytes, int32_t batch, int32_t block_size,
+                          int32_t num_blocks, int32_t max_context_len, int32_t keep, int32_t recent,
+                          hipStream_t stream);
+
 /* Compute units of a device (the get_num_sms analogue of the DeepGEMM
  * article's paged example); negative on error. */
 int32_t mqa_num_cus(int32_t device);

@@ -18,9 +18,12 @@ Entry points (same names as the C ABI):
   paged_kv_write                  quantise rows and store them at their slots
   paged_attention                 attention over a paged MXFP4 cache, whole or selected keys
   paged_chunk_attention           the same for chunks of new tokens, a different number a sequence
+  paged_attention_weights         the attention weight that every cached token has gathered
+  paged_kv_evict                  cut long sequences to their heaviest and their last tokens
   mqa_num_cus, paged_mqa_logits_default_splits
 """
 
+import collections
 import ctypes
 import functools
 import os
@@ -73,6 +76,10 @@ def _load():
                             P, P, P, I64, I32, I32, I32, I32, I32, I32, I32, I32, P],
         "paged_chunk_attention": [I32, P, I32, I64, P, P, P, P, P, P, P, I64, ctypes.c_float, P, P, P,
                                   I64, I32, I32, I32, I32, I32, I32, I32, I32, P],
+        "paged_attention_weights": [I32, P, I32, I64, P, P, P, P, P, P, I64, ctypes.c_float, P, I64, P, I64,
+                                    P, I64, I32, I32, I32, I32, I32, I32, I32, I32, P],
+        "paged_kv_evict": [P, I64, P, P, I64, P, I32, P, I32, P, P, I64, P, I64, P, I64, P, P, P, I64,
+                           I32, I32, I32, I32, I32, I32, P],
     }
     for name, argtypes in sigs.items():
         fn = getattr(lib, name)
@@ -85,6 +92,10 @@ def _load():
     lib.paged_attention_workspace_size.restype = I64
     lib.paged_chunk_attention_workspace_size.argtypes = [I32] * 6
     lib.paged_chunk_attention_workspace_size.restype = I64
+    lib.paged_attention_weights_workspace_size.argtypes = [I32] * 6
+    lib.paged_attention_weights_workspace_size.restype = I64
+    lib.paged_kv_evict_workspace_size.argtypes = [I32]
+    lib.paged_kv_evict_workspace_size.restype = I64
     lib.mqa_num_cus.argtypes = [I32]
     lib.mqa_num_cus.restype = I32
     lib.paged_mqa_logits_default_splits.argtypes = [I32]
@@ -102,6 +113,8 @@ EXPORTED = ("mqa_logits", "mqa_logits_metadata_size", "mqa_logits_metadata", "mq
             "paged_mqa_logits", "paged_kv_slots", "paged_kv_write",
             "paged_attention_workspace_size", "paged_attention",
             "paged_chunk_attention_workspace_size", "paged_chunk_attention",
+            "paged_attention_weights_workspace_size", "paged_attention_weights",
+            "paged_kv_evict_workspace_size", "paged_kv_evict",
             "mqa_num_cus", "paged_mqa_logits_default_splits",
             "mqa_last_error")
 
@@ -763,3 +776,185 @@ def paged_chunk_attention(fmt, q, k_pool, k_sf_pool, v_pool, v_sf_pool, context_
           out.data_ptr(), _data(lse), _data(workspace), size, batch, tokens, hq, hkv, d, block_size,
           num_blocks, max_context_len)
     return out if lse is None else (out, lse)
+
+
+@functools.lru_cache(maxsize=1024)
+def paged_attention_weights_workspace_size(batch, tokens, q_heads, kv_heads, d, max_context_len):
+    """Bytes of workspace of a paged_attention_weights call of these sizes."""
+    n = lib.paged_attention_weights_workspace_size(batch, tokens, q_heads, kv_heads, d, max_context_len)
+    if n < 0:
+        raise MqaError(2, lib.mqa_last_error().decode())
+    return n
+
+
+def paged_attention_weights(fmt, q, lse, k_pool, k_sf_pool, context_lens, token_offsets, block_table,
+                            max_context_len, scale=None, weights=None, out=None, workspace=None):
+    """The attention weight that every cached token has gathered, after one more step.
+
+    out[b, j] = weights[b, j] (0 without weights) + the sum of exp(scale <q, k_j> - lse) over
+    the rows of sequence b that see key j and over query heads, 0 behind the context: fp32
+    [batch, max_context_len].  q, the pools, token_offsets and what a row sees are as in
+    paged_chunk_attention, lse [tokens, Hq] is what that (or paged_attention) gave for q; rows of
+    -inf give nothing.  weights and out may have wider rows, and be the same tensor.
+    workspace: a uint8 tensor of paged_attention_weights_workspace_size bytes to keep between
+    calls on one stream, or None."""
+    tokens, hq, d, batch, (num_blocks, block_size, hkv, _), q_stride = _chunk_sizes(
+        "paged_attention_weights", fmt, q, k_pool, context_lens, token_offsets, max_context_len)
+    dev = q.get_device()
+    given_out, given_workspace = out is not None, workspace is not None
+    if not given_out:
+        out = q.new_empty((batch, max_context_len), dtype=torch.float32)
+    need = paged_attention_weights_workspace_size(batch, tokens, hq, hkv, d, max_context_len)
+    if not given_workspace:
+        workspace, size = (q.new_empty(need, dtype=torch.uint8), need) if need else (None, 0)
+    else:
+        size = workspace.numel()
+    codes, scales = (num_blocks, block_size, hkv, d // 2), (num_blocks, block_size, hkv, d // 32)
+    byte, i32 = k_pool.dtype, torch.int32
+    if not (dev >= 0 and byte.itemsize == 1 and _fits(k_pool, codes, byte, dev)
+            and k_sf_pool is not None and k_sf_pool.dtype.itemsize == 1 and _fits(k_sf_pool, scales, k_sf_pool.dtype, dev)
+            and _fits(lse, (tokens, hq), torch.float32, dev)
+            and _fits(context_lens, (batch,), i32, dev)
+            and (token_offsets is None or _fits(token_offsets, (batch + 1,), i32, dev))
+            and _table_fits(block_table, batch, -(-max_context_len // block_size), dev)
+            and (weights is None or _rows_fit(weights, batch, max_context_len, dev))
+            and (not given_out or _rows_fit(out, batch, max_context_len, dev))
+            and (not given_workspace or _fits(workspace, (size,), torch.uint8, dev))):
+        a = _Args()
+        a.want(q[:0], "q", (0, hq, d))
+        a.want(lse, "lse", (tokens, hq), (torch.float32,))
+        a.want(k_pool, "k_pool", codes, itemsize=1)
+        a.want(k_sf_pool, "k_sf_pool", scales, itemsize=1)
+        a.want(context_lens, "context_lens", (batch,), I32_T)
+        if token_offsets is not None:
+            a.want(token_offsets, "token_offsets", (batch + 1,), I32_T)
+        _want_table(a, block_table, batch, block_size, max_context_len)
+        for name, t in (("weights", weights), ("out", out)):
+            if t is not None:
+                _want_rows(a, t, name, batch, max_context_len)
+        if workspace is not None:
+            a.want(workspace, "workspace", (None,), itemsize=1)
+        a.on_gpu()
+    _call(lib.paged_attention_weights, dev, 2, q.data_ptr(), QUERY_TYPES[q.dtype], q_stride, lse.data_ptr(),
+          k_pool.data_ptr(), k_sf_pool.data_ptr(), context_lens.data_ptr(), _data(token_offsets),
+          block_table.data_ptr(), _row_stride(block_table, block_table.shape[1]),
+          d ** -0.5 if scale is None else float(scale), _data(weights),
+          0 if weights is None else _row_stride(weights, weights.shape[1]), out.data_ptr(),
+          _row_stride(out, out.shape[1]), _data(workspace), size, batch, tokens, hq, hkv, d, block_size,
+          num_blocks, max_context_len)
+    return out
+
+
+def _rows_fit(t, batch, width, device):
+    """fp32 rows of at least `width`, a row for each sequence, elements of a row adjacent."""
+    shape = t.shape
+    return (len(shape) == 2 and shape[0] == batch and shape[1] >= width and t.dtype is torch.float32
+            and t.get_device() == device and (t.stride(1) == 1 or shape[1] <= 1))
+
+
+def _want_rows(a, t, name, batch, width):
+    a.want(t, name, (batch, None), (torch.float32,), rows=True)
+    if t.shape[1] < width:
+        raise ValueError(f"{name} rows must hold max_context_len = {width} values, got {t.shape[1]}")
+
+
+class _Pool(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_bytes", ctypes.c_int64)]
+
+
+Eviction = collections.namedtuple("Eviction", "context_lens block_table weights kept freed counts")
+
+
+def paged_kv_evict(weights, context_lens, block_table, free_blocks, pools, keep, recent, max_context_len,
+                   out=None, workspace=None):
+    """Cut sequences longer than `keep` tokens to their last `recent` and the heaviest of the others.
+
+    weights fp32 [batch, >= max_context_len] (paged_attention_weights); context_lens, block_table
+    and free_blocks (int32, in the order to take them) are only read.  The tokens that stay
+    are copied, in order, to free blocks of every pool in `pools` (contiguous
+    [num_blocks, block_size, ...] tensors of any type: K, V, their scales, the indexer's keys),
+    whose old blocks are not written.  Returns Eviction(context_lens int32 [batch], block_table
+    int32 [batch, blocks] (-1 behind), weights fp32 [batch, max_context_len] (0 behind), kept
+    int32 [batch, keep] (the old positions, -1 behind), freed int32 [batch * blocks] (the old
+    blocks of cut sequences, -1 behind), counts int32 [2]: blocks asked of the free list
+    and blocks in freed); `out` may hold these.  Where the first count exceeds
+    len(free_blocks), the sequences that the list did not reach stay as they are.  Sequences of
+    up to `keep` tokens stay as they are.  workspace: a uint8 tensor of
+    paged_kv_evict_workspace_size(batch) bytes to keep between calls on one stream, or None."""
+    if weights is None or context_lens is None or free_blocks is None or pools is None:
+        _required(weights=weights, context_lens=context_lens, free_blocks=free_blocks, pools=pools)
+    if not pools:
+        raise ValueError("pools must hold at least one tensor")
+    if len(pools[0].shape) < 2:
+        raise ValueError(f"pools must be [num_blocks, block_size, ...], got {tuple(pools[0].shape)}")
+    num_blocks, block_size = pools[0].shape[:2]
+    _block_size(block_size)
+    if not (1 <= keep < 2 ** 31 and 0 <= recent <= keep and 0 <= max_context_len < 2 ** 31
+            and num_blocks < 2 ** 31):
+        raise ValueError("keep must be at least 1, recent within [0, keep], sizes int32 and not negative")
+    batch, dev = context_lens.numel(), context_lens.get_device()
+    width = -(-max_context_len // block_size)
+    i32, given = torch.int32, out is not None
+    if not given:
+        new = context_lens.new_empty
+        out = Eviction(new(batch, dtype=i32), new((batch, width), dtype=i32),
+                       new((batch, max_context_len), dtype=torch.float32), new((batch, keep), dtype=i32),
+                       new(batch * width, dtype=i32), new(2, dtype=i32))
+    else:
+        out = Eviction(*out)
+    size = paged_kv_evict_workspace_size(batch)
+    if workspace is None:
+        workspace, given_workspace = context_lens.new_empty(size, dtype=torch.uint8), False
+    else:
+        size, given_workspace = workspace.numel(), True
+    if not (dev >= 0 and _rows_fit(weights, batch, max_context_len, dev)
+            and _fits(context_lens, (batch,), i32, dev) and _table_fits(block_table, batch, width, dev)
+            and _fits(free_blocks, (free_blocks.numel(),), i32, dev)
+            and all(p.get_device() == dev and p.shape[:2] == pools[0].shape[:2] and p.is_contiguous()
+                    for p in pools)
+            and (not given or (_fits(out.context_lens, (batch,), i32, dev)
+                               and _table_fits(out.block_table, batch, width, dev)
+                               and _rows_fit(out.weights, batch, max_context_len, dev)
+                               and _table_fits(out.kept, batch, keep, dev)
+                               and _fits(out.freed, (batch * width,), i32, dev)
+                               and _fits(out.counts, (2,), i32, dev)))
+            and (not given_workspace or _fits(workspace, (size,), torch.uint8, dev))):
+        a = _Args()
+        _want_rows(a, weights, "weights", batch, max_context_len)
+        a.want(context_lens, "context_lens", (batch,), I32_T)
+        _want_table(a, block_table, batch, block_size, max_context_len)
+        a.want(free_blocks, "free_blocks", (None,), I32_T)
+        for i, p in enumerate(pools):
+            a.want(p, f"pools[{i}]", (num_blocks, block_size, *p.shape[2:]))
+        a.want(out.context_lens, "out.context_lens", (batch,), I32_T)
+        a.want(out.block_table, "out.block_table", (batch, None), I32_T, rows=True)
+        if out.block_table.shape[1] < width:
+            raise ValueError(f"out.block_table rows must hold {width} blocks, got {out.block_table.shape[1]}")
+        _want_rows(a, out.weights, "out.weights", batch, max_context_len)
+        a.want(out.kept, "out.kept", (batch, None), I32_T, rows=True)
+        if out.kept.shape[1] < keep:
+            raise ValueError(f"out.kept rows must hold keep = {keep} positions, got {out.kept.shape[1]}")
+        a.want(out.freed, "out.freed", (batch * width,), I32_T)
+        a.want(out.counts, "out.counts", (2,), I32_T)
+        a.want(workspace, "workspace", (None,), itemsize=1)
+        a.on_gpu()
+    described = (_Pool * len(pools))()
+    for p, d in zip(pools, described):
+        d.data, d.token_bytes = p.data_ptr(), p[0, 0].numel() * p.element_size() if num_blocks else 0
+    _call(lib.paged_kv_evict, dev, weights.data_ptr(), _row_stride(weights, weights.shape[1]),
+          context_lens.data_ptr(), block_table.data_ptr(), _row_stride(block_table, block_table.shape[1]),
+          free_blocks.data_ptr(), free_blocks.shape[0], described, len(pools), out.context_lens.data_ptr(),
+          out.block_table.data_ptr(), _row_stride(out.block_table, out.block_table.shape[1]),
+          out.weights.data_ptr(), _row_stride(out.weights, out.weights.shape[1]), out.kept.data_ptr(),
+          _row_stride(out.kept, out.kept.shape[1]), out.freed.data_ptr(), out.counts.data_ptr(),
+          workspace.data_ptr(), size, batch, block_size, num_blocks, max_context_len, keep, recent)
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def paged_kv_evict_workspace_size(batch):
+    """Bytes of workspace of a paged_kv_evict call for this many sequences."""
+    n = lib.paged_kv_evict_workspace_size(batch)
+    if n < 0:
+        raise MqaError(2, lib.mqa_last_error().decode())
+    return n

@@ -21,8 +21,8 @@ LIB = os.path.join(PKG, "libmqa_logits.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["dense.hip", "dense_bf16.hip", "dense_sched.hip", "dense_sched_bf16.hip",
-           "topk.hip", "paged.hip", "attention.hip", "chunk.hip", "cache.hip",
-           "api.cpp"]
+           "topk.hip", "paged.hip", "attention.hip", "chunk.hip", "weights.hip",
+           "evict.hip", "cache.hip", "api.cpp"]
 # measurement aid for bench.py, linked into a library of its own
 PROBE_SOURCES = ["peak.hip"]
 PROBE_LIB = os.path.join(PKG, "libmqa_peak.so")
@@ -40,7 +40,7 @@ COMMON_FLAGS = [
 # No NaN canonicalisation in front of each ReLU max; the cache and attention
 # kernels pass NaNs on and are built without it.
 NO_NANS = ["-fno-honor-nans"]
-HONOR_NANS = ("attention.hip", "chunk.hip", "cache.hip")
+HONOR_NANS = ("attention.hip", "chunk.hip", "weights.hip", "cache.hip")
 
 
 def _compile(src):

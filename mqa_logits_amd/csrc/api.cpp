@@ -317,6 +317,16 @@ mqa_status check_chunk_cache(mqa_dtype dt, const void* q, mqa_float q_type, int6
   return MQA_OK;
 }
 
+// Parts that the rows of a sequence are cut into, for sums of weights: as many as
+// the workgroups along the keys leave compute units idle (four for each), and as
+// there are tiles of 32 rows to share.
+int32_t weight_splits(int32_t batch, int32_t tokens, int32_t hq, int32_t hkv, int32_t max_context_len) {
+  const int64_t groups = (int64_t)batch * ((max_context_len + 127) / 128);
+  const int64_t tiles = ((int64_t)tokens * (hq / hkv) / batch + 31) / 32 * hkv;   // of a usual sequence
+  const int64_t splits = std::min<int64_t>(1024 / std::max<int64_t>(groups, 1), tiles / 4);
+  return (int32_t)std::clamp<int64_t>(splits, 1, 64);
+}
+
 // |scale| * log2(e), positive and finite: a masked score (-inf) or one of 0 stays
 // out of NaN.  (The least subnormal stands for 0: it leaves any finite <q, k> a
 // score under 2^-20; the kernels keep subnormals.)
@@ -811,6 +821,164 @@ mqa_status paged_chunk_attention(mqa_dtype dt, const void* q, mqa_float q_type, 
     fprintf(stderr, "[mqa_logits] %s Hq=%d Hkv=%d D=%d batch=%d tokens=%d bs=%d workers=%d tile=%d x %d whole=%d\n",
             who, hq, hkv, d, batch, tokens, block_size, a.workers, a.tile_tokens, a.tile_heads, a.whole);
   return hip_status(mqa::launch_chunk(d, q_type == MQA_F16, p, stream), who);
+}
+
+int64_t paged_attention_weights_workspace_size(int32_t batch, int32_t tokens, int32_t hq, int32_t hkv,
+                                               int32_t d, int32_t max_context_len) {
+  mqa_status st = check_chunk_shape(batch, tokens, hq, hkv, d, max_context_len,
+                                    "paged_attention_weights_workspace_size");
+  if (st != MQA_OK) return -1;
+  const int32_t splits = weight_splits(batch, tokens, hq, hkv, max_context_len);
+  return splits > 1 ? (int64_t)splits * batch * max_context_len * 4 : 0;
+}
+
+mqa_status paged_attention_weights(mqa_dtype dt, const void* q, mqa_float q_type, int64_t q_stride,
+                                   const float* lse, const uint8_t* k_pool, const uint8_t* k_sf_pool,
+                                   const int32_t* context_lens, const int32_t* token_offsets,
+                                   const int32_t* block_table, int64_t block_table_stride, float scale,
+                                   const float* weights, int64_t weights_stride, float* out,
+                                   int64_t out_stride, void* workspace, int64_t workspace_bytes,
+                                   int32_t batch, int32_t tokens, int32_t hq, int32_t hkv, int32_t d,
+                                   int32_t block_size, int32_t num_blocks, int32_t max_context_len,
+                                   hipStream_t stream) {
+  const char* who = "paged_attention_weights";
+  mqa_status st = check_chunk_shape(batch, tokens, hq, hkv, d, max_context_len, who);
+  if (st != MQA_OK) return st;
+  st = check_chunk_cache(dt, q, q_type, q_stride, k_pool, k_sf_pool, context_lens, token_offsets, block_table,
+                         block_table_stride, scale, batch, tokens, hq, hkv, d, block_size, num_blocks,
+                         max_context_len, who);
+  if (st != MQA_OK) return st;
+  if (max_context_len == 0) return ok();
+  if ((tokens > 0 && !lse) || !out) return fail(MQA_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!aligned(lse, 4) || !aligned(weights, 4) || !aligned(out, 4) || !aligned(workspace, 16))
+    return fail(MQA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+  if (out_stride < max_context_len || (weights && weights_stride < max_context_len))
+    return fail(MQA_ERR_INVALID_ARG, "%s: rows of weights or out shorter than max_context_len", who);
+  const int32_t splits = weight_splits(batch, tokens, hq, hkv, max_context_len);
+  const int64_t need = splits > 1 ? (int64_t)splits * batch * max_context_len * 4 : 0;
+  if (workspace_bytes < need || (need > 0 && !workspace))
+    return fail(MQA_ERR_INVALID_ARG, "%s: workspace of %lld bytes, %lld needed", who,
+                (long long)workspace_bytes, (long long)need);
+  mqa::WeightParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_stride = q_stride;
+  p.lse = lse;
+  p.k = k_pool;
+  p.k_sf = k_sf_pool;
+  p.ctx = context_lens;
+  p.offsets = token_offsets;
+  p.bt = block_table;
+  p.bt_stride = block_table_stride;
+  p.before = weights;
+  p.before_stride = weights_stride;
+  p.out = out;
+  p.out_stride = out_stride;
+  p.part = splits > 1 ? static_cast<float*>(workspace) : nullptr;
+  p.batch = batch;
+  p.tokens = tokens;
+  p.next_n = token_offsets ? 0 : tokens / batch;
+  p.kv_heads = hkv;
+  p.group = hq / hkv;
+  p.num_blocks = num_blocks;
+  p.bs_shift = block_shift(block_size);
+  p.max_ctx = max_context_len;
+  p.splits = splits;
+  p.negate = scale < 0.f;
+  p.c2 = positive_c2(scale);
+  if (debug_enabled())
+    fprintf(stderr, "[mqa_logits] %s Hq=%d Hkv=%d D=%d batch=%d tokens=%d bs=%d splits=%d\n", who, hq, hkv, d,
+            batch, tokens, block_size, splits);
+  return hip_status(mqa::launch_weights(d, q_type == MQA_F16, p, stream), who);
+}
+
+int64_t paged_kv_evict_workspace_size(int32_t batch) {
+  if (batch < 1 || batch > 8192) {
+    fail(MQA_ERR_UNSUPPORTED, "paged_kv_evict_workspace_size: batch=%d not in [1, 8192]", batch);
+    return -1;
+  }
+  return (int64_t)batch * (int64_t)(sizeof(mqa::EvictPlan) + 8);
+}
+
+mqa_status paged_kv_evict(const float* weights, int64_t weights_stride, const int32_t* context_lens,
+                          const int32_t* block_table, int64_t block_table_stride,
+                          const int32_t* free_blocks, int32_t num_free, const mqa_pool* pools,
+                          int32_t num_pools, int32_t* new_context_lens, int32_t* new_block_table,
+                          int64_t new_block_table_stride, float* new_weights,
+                          int64_t new_weights_stride, int32_t* kept, int64_t kept_stride,
+                          int32_t* freed_blocks, int32_t* counts, void* workspace,
+                          int64_t workspace_bytes, int32_t batch, int32_t block_size,
+                          int32_t num_blocks, int32_t max_context_len, int32_t keep, int32_t recent,
+                          hipStream_t stream) {
+  const char* who = "paged_kv_evict";
+  if (batch < 1 || batch > 8192) return fail(MQA_ERR_UNSUPPORTED, "%s: batch=%d not in [1, 8192]", who, batch);
+  if (block_size != 16 && block_size != 32 && block_size != 64)
+    return fail(MQA_ERR_UNSUPPORTED, "%s: block_size=%d not in {16, 32, 64}", who, block_size);
+  if (num_blocks < 1 || num_free < 0 || max_context_len < 0)
+    return fail(MQA_ERR_INVALID_ARG, "%s: negative size or num_blocks < 1", who);
+  if ((int64_t)num_blocks * block_size > 0x7fffffff)
+    return fail(MQA_ERR_UNSUPPORTED, "%s: pool of %d blocks too large", who, num_blocks);
+  if (keep < 1 || recent < 0 || recent > keep)
+    return fail(MQA_ERR_INVALID_ARG, "%s: keep=%d recent=%d: keep >= 1, recent in [0, keep]", who, keep, recent);
+  if ((int64_t)batch * max_context_len >= 0x7fffffff || (int64_t)batch * keep >= 0x7fffffff ||
+      (int64_t)max_context_len * 4 >= kMaxRangeBytes)
+    return fail(MQA_ERR_UNSUPPORTED, "%s: batch * max_context_len or batch * keep too large", who);
+  if (num_pools < 0 || num_pools > mqa::kEvictPools)
+    return fail(MQA_ERR_UNSUPPORTED, "%s: num_pools=%d not in [0, %d]", who, num_pools, mqa::kEvictPools);
+  const int64_t width = ((int64_t)max_context_len + block_size - 1) / block_size;
+  const bool some = max_context_len > 0;
+  if (!context_lens || !new_context_lens || !kept || !counts || !workspace ||
+      (some && (!weights || !block_table || !new_block_table || !new_weights || !freed_blocks)) ||
+      (num_free > 0 && !free_blocks) || (num_pools > 0 && !pools))
+    return fail(MQA_ERR_INVALID_ARG, "%s: null pointer", who);
+  for (const void* a : {(const void*)weights, (const void*)context_lens, (const void*)block_table,
+                        (const void*)free_blocks, (const void*)new_context_lens, (const void*)new_block_table,
+                        (const void*)new_weights, (const void*)kept, (const void*)freed_blocks,
+                        (const void*)counts})
+    if (!aligned(a, 4)) return fail(MQA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+  if (!aligned(workspace, 16)) return fail(MQA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+  if (weights_stride < max_context_len || new_weights_stride < max_context_len || kept_stride < keep ||
+      block_table_stride < width || new_block_table_stride < width)
+    return fail(MQA_ERR_INVALID_ARG, "%s: rows shorter than what they hold", who);
+  if (workspace_bytes < paged_kv_evict_workspace_size(batch))
+    return fail(MQA_ERR_INVALID_ARG, "%s: workspace of %lld bytes, %lld needed", who,
+                (long long)workspace_bytes, (long long)paged_kv_evict_workspace_size(batch));
+  mqa::EvictParams p{};
+  for (int i = 0; i < num_pools; ++i) {
+    if (!pools[i].data || pools[i].token_bytes < 1)
+      return fail(MQA_ERR_INVALID_ARG, "%s: pool %d is null or has no bytes", who, i);
+    if (pools[i].token_bytes > (1 << 24))
+      return fail(MQA_ERR_UNSUPPORTED, "%s: pool %d has %lld bytes a token", who, i, (long long)pools[i].token_bytes);
+    int32_t piece = 16;
+    while (piece > 1 && (pools[i].token_bytes % piece || !aligned(pools[i].data, piece))) piece /= 2;
+    p.pools[i] = mqa::EvictPool{pools[i].data, pools[i].token_bytes, piece};
+  }
+  p.weights = weights;
+  p.weights_stride = weights_stride;
+  p.ctx = context_lens;
+  p.bt = block_table;
+  p.bt_stride = block_table_stride;
+  p.free_ids = free_blocks;
+  p.new_ctx = new_context_lens;
+  p.new_bt = new_block_table;
+  p.new_bt_stride = new_block_table_stride;
+  p.new_weights = new_weights;
+  p.new_weights_stride = new_weights_stride;
+  p.kept = kept;
+  p.kept_stride = kept_stride;
+  p.freed = freed_blocks;
+  p.counts = counts;
+  p.plan = static_cast<mqa::EvictPlan*>(workspace);
+  p.k_start = reinterpret_cast<int32_t*>(p.plan + batch);
+  p.k_end = p.k_start + batch;
+  p.batch = batch;
+  p.num_free = num_free;
+  p.num_blocks = num_blocks;
+  p.bs_shift = block_shift(block_size);
+  p.max_ctx = max_context_len;
+  p.keep = keep;
+  p.recent = recent;
+  p.num_pools = num_pools;
+  return hip_status(mqa::launch_evict(p, stream), who);
 }
 
 }  // extern "C"

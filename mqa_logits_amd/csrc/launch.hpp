@@ -159,6 +159,67 @@ struct ChunkParams {
   float c2;                  // |scale| * log2(e)
 };
 
+struct WeightParams {
+  const uint16_t* q;         // [tokens, Hq, D] bf16 or fp16 bits
+  int64_t q_stride;
+  const float* lse;          // [tokens, Hq]
+  const uint8_t* k;          // [num_blocks, bs, Hkv, D/2] packed e2m1
+  const uint8_t* k_sf;       // [num_blocks, bs, Hkv, D/32] e8m0
+  const int32_t* ctx;        // [batch]
+  const int32_t* offsets;    // [batch + 1], or null (next_n tokens a sequence)
+  const int32_t* bt;         // [batch, bt_stride]
+  int64_t bt_stride;
+  const float* before;       // [batch, before_stride], or null (0)
+  int64_t before_stride;
+  float* out;                // [batch, out_stride]
+  int64_t out_stride;
+  float* part;               // [splits, batch, max_ctx], or null with one split
+  int32_t batch, tokens, next_n;
+  int32_t kv_heads, group;
+  int32_t num_blocks, bs_shift, max_ctx;
+  int32_t splits;            // of the rows of a sequence
+  int32_t negate;
+  float c2;
+};
+
+// Pools that one eviction repacks, at most.
+constexpr int kEvictPools = 16;
+
+struct EvictPool {
+  void* data;                // [num_blocks, bs, bytes]
+  int64_t bytes;             // of a token
+  int32_t width;             // of a copied piece: 16, 8, 4, 2 or 1 bytes
+};
+
+struct EvictPlan {
+  int32_t chosen;            // tokens kept before the recent ones; -1: the sequence stays as it is
+  int32_t cut;               // it is longer than `keep`
+  int32_t first, freed;      // its first entry of the free list, and of the freed blocks'
+};
+
+struct EvictParams {
+  const float* weights;      // [batch, weights_stride]
+  int64_t weights_stride;
+  const int32_t* ctx;        // [batch]
+  const int32_t* bt;         // [batch, bt_stride]
+  int64_t bt_stride;
+  const int32_t* free_ids;   // [num_free]
+  int32_t* new_ctx;          // [batch]
+  int32_t* new_bt;           // [batch, new_bt_stride]
+  int64_t new_bt_stride;
+  float* new_weights;        // [batch, new_weights_stride]
+  int64_t new_weights_stride;
+  int32_t* kept;             // [batch, kept_stride]
+  int64_t kept_stride;
+  int32_t* freed;            // [batch * blocks of max_ctx]
+  int32_t* counts;           // [2] blocks taken, blocks freed
+  int32_t* k_start;          // [batch]
+  int32_t* k_end;            // [batch]
+  EvictPlan* plan;           // [batch]
+  int32_t batch, num_free, num_blocks, bs_shift, max_ctx, keep, recent, num_pools;
+  EvictPool pools[kEvictPools];
+};
+
 struct WriteParams {
   const void* x;             // rows of heads of D elements
   int64_t x_stride, x_head_stride;   // elements
@@ -185,6 +246,8 @@ struct SlotParams {
 
 hipError_t launch_attention(int d, int f16, const AttnParams& p, hipStream_t s);
 hipError_t launch_chunk(int d, int f16, const ChunkParams& p, hipStream_t s);
+hipError_t launch_weights(int d, int f16, const WeightParams& p, hipStream_t s);
+hipError_t launch_evict(const EvictParams& p, hipStream_t s);
 hipError_t launch_kv_write(int fmt, int d, int in_type, const WriteParams& p, hipStream_t s);
 hipError_t launch_kv_slots(const SlotParams& p, hipStream_t s);
 hipError_t launch_topk(int in_type, const TopkParams& p, hipStream_t s);

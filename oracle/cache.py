@@ -6,6 +6,8 @@ Straight from the definitions, in float64 and Python integers:
   quantise    the smallest power-of-two scale of a group under which no element
               exceeds the largest code, then the nearest code (ties to the even
               code) by comparison with every code of the format;
+  gathered    the attention weight that every key has gathered;
+  evict       the recent tokens and the heaviest of the others, in free blocks;
   attention   out = sum_j softmax_j(scale <q, k_j>) v_j over the keys a row
               sees (or the listed ones among them), lse = log sum_j exp(..),
               with an error bound per entry.
@@ -173,3 +175,83 @@ def attend_rows(q, k_pool, k_sf_pool, v_pool, v_sf_pool, block_table, sequence, 
                                 * (1 + 2 * half_step) + half_step * np.abs(out[r, hs]) + 2.0 ** -24)
             lse_bound[r, hs] = worst[:, 0] + chain * 2.0 ** -23 + 2.0 ** -22 * np.abs(lse[r, hs])
     return out, lse, out_bound, lse_bound
+
+
+def gathered(q, lse, k_pool, k_sf_pool, block_table, sequence, seen, scale, lengths, before=None):
+    """(sums, bound) float64 [batch, most]: before + sum exp(scale <q, k> - lse) of the rows that see a
+    key, for keys below `lengths`, 0 behind.
+
+    The bound: a score is off by e (see attention), the shift by lse by 2^-22 (|score| + |lse|), which
+    with the exponential's own 2^-22 is the relative error of a term; sums of n terms, in parts that are
+    added in turn, by at most n 2^-24 + 2^-20 of their sum."""
+    q = np.asarray(q, dtype=np.float64)
+    hq, d = q.shape[1:]
+    bs, hkv = k_pool.shape[1], k_pool.shape[2]
+    group = hq // hkv
+    lengths = np.asarray(lengths)
+    sums = np.zeros((len(lengths), max(int(lengths.max()), 1)))
+    error, count = np.zeros_like(sums), np.zeros_like(sums)
+    for b, n in enumerate(lengths):
+        if before is not None:
+            sums[b, :n] = np.asarray(before, np.float64)[b, :n]
+        keys = np.arange(n)
+        block = np.clip(np.asarray(block_table)[b, keys // bs], 0, len(k_pool) - 1)
+        k = decode_cache(k_pool[block, keys % bs], k_sf_pool[block, keys % bs])
+        for r in np.flatnonzero(np.asarray(sequence) == b):
+            m = int(seen[r])
+            for h in range(hq):
+                if m == 0 or np.isneginf(lse[r, h]):
+                    continue
+                kh = k[:m, h // group]
+                s = (kh @ q[r, h]) * scale
+                p = np.exp(s - float(lse[r, h]))
+                e = (abs(scale) * d * 2.0 ** -23 * (np.abs(kh) @ np.abs(q[r, h]))
+                     + 2.0 ** -22 * (np.abs(s) + abs(float(lse[r, h]))) + 2.0 ** -22)
+                sums[b, :m] += p
+                error[b, :m] += p * e
+                count[b, :m] += 1
+    return sums, error * 1.01 + np.abs(sums) * (count * 2.0 ** -24 + 2.0 ** -20)
+
+
+def evict(weights, context_lens, block_table, free_blocks, pools, keep, recent, max_context_len):
+    """(context_lens, block_table, weights, kept, freed, counts, pools) afterwards."""
+    size = pools[0].shape[1]
+    table, weights = np.asarray(block_table), np.asarray(weights)
+    batch, width = len(table), -(-max_context_len // size)
+    num_blocks = len(pools[0])
+    new_table = np.full((batch, width), -1, np.int32)
+    new_weights = np.zeros((batch, max_context_len), np.float32)
+    kept, lens, freed, taken = np.full((batch, keep), -1, np.int32), [], [], 0
+    before, pools = pools, [np.array(p) for p in pools]
+    for b, ctx in enumerate(context_lens):
+        n = min(max(int(ctx), 0), max_context_len)
+        old, at, moved = table[b, :-(-n // size)], np.arange(n), False
+        if n > keep:
+            w = weights[b, :n - recent]
+            bits = w.view(np.int32).astype(np.int64)
+            order = np.where(bits < 0, -(bits & 0x7fffffff) - 1, bits)     # IEEE total order
+            chosen = [j for j in sorted(range(n - recent), key=lambda j: (-order[j], j)) if w[j] != -np.inf]
+            at = np.array(sorted(chosen[:keep - recent]) + list(range(n - recent, n)), int)
+            want = -(-len(at) // size)
+            moved = taken + want <= len(free_blocks)
+            if moved:
+                mine = np.asarray(free_blocks[taken:taken + want], np.int32)
+                for i, j in enumerate(at):
+                    src, dst = old[j // size], mine[i // size]
+                    if 0 <= src < num_blocks and 0 <= dst < num_blocks:
+                        for p, q in zip(before, pools):
+                            q[dst, i % size] = p[src, j % size]
+                freed += old.tolist()
+                old = mine
+            else:
+                at = np.arange(n)
+            taken += want
+        new_table[b, :len(old)] = old
+        if n <= keep or moved:
+            kept[b, :len(at)] = at
+        new_weights[b, :len(at)] = weights[b, at]
+        lens.append(len(at))
+    back = np.full(batch * width, -1, np.int32)
+    back[:len(freed)] = freed
+    return (np.array(lens, np.int32), new_table, new_weights, kept, back,
+            np.array([taken, len(freed)], np.int32), pools)
