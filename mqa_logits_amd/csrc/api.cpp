@@ -317,14 +317,24 @@ mqa_status check_chunk_cache(mqa_dtype dt, const void* q, mqa_float q_type, int6
   return MQA_OK;
 }
 
-// Parts that the rows of a sequence are cut into, for sums of weights: as many as
-// the workgroups along the keys leave compute units idle (four for each), and as
-// there are tiles of 32 rows to share.
-int32_t weight_splits(int32_t batch, int32_t tokens, int32_t hq, int32_t hkv, int32_t max_context_len) {
-  const int64_t groups = (int64_t)batch * ((max_context_len + 127) / 128);
-  const int64_t tiles = ((int64_t)tokens * (hq / hkv) / batch + 31) / 32 * hkv;   // of a usual sequence
-  const int64_t splits = std::min<int64_t>(1024 / std::max<int64_t>(groups, 1), tiles / 4);
-  return (int32_t)std::clamp<int64_t>(splits, 1, 64);
+// KV heads that the four waves of a workgroup take beside each other.
+int32_t weight_heads(int32_t hkv) { return hkv >= 4 ? 4 : hkv == 2 ? 2 : 1; }
+
+// A weights call's split: blocks of 64 keys that a wave takes one after the other
+// (what it reads of the rows then serves them all), as many as leave four
+// workgroups for each compute unit; where there are fewer, parts that the rows of a sequence are
+// cut into, as far as there are tiles of 32 rows to share.
+struct WeightPlan {
+  int32_t heads, blocks, splits;
+};
+WeightPlan plan_weights(int32_t batch, int32_t tokens, int32_t hq, int32_t hkv, int32_t max_context_len) {
+  WeightPlan a{};
+  a.heads = weight_heads(hkv);
+  const int64_t keys = 256 / a.heads, groups = (int64_t)batch * ((max_context_len + keys - 1) / keys);
+  a.blocks = (int32_t)std::clamp<int64_t>(groups / 2048, 1, mqa::kWeightBlocks);
+  const int64_t tiles = ((int64_t)tokens * (hq / hkv) / batch + 31) / 32;   // of a usual sequence and KV head
+  a.splits = (int32_t)std::clamp<int64_t>(std::min<int64_t>(512 / std::max<int64_t>(groups, 1), tiles / 2), 1, 64);
+  return a;
 }
 
 // |scale| * log2(e), positive and finite: a masked score (-inf) or one of 0 stays
@@ -828,7 +838,7 @@ int64_t paged_attention_weights_workspace_size(int32_t batch, int32_t tokens, in
   mqa_status st = check_chunk_shape(batch, tokens, hq, hkv, d, max_context_len,
                                     "paged_attention_weights_workspace_size");
   if (st != MQA_OK) return -1;
-  const int32_t splits = weight_splits(batch, tokens, hq, hkv, max_context_len);
+  const int32_t splits = plan_weights(batch, tokens, hq, hkv, max_context_len).splits;
   return splits > 1 ? (int64_t)splits * batch * max_context_len * 4 : 0;
 }
 
@@ -854,7 +864,8 @@ mqa_status paged_attention_weights(mqa_dtype dt, const void* q, mqa_float q_type
     return fail(MQA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
   if (out_stride < max_context_len || (weights && weights_stride < max_context_len))
     return fail(MQA_ERR_INVALID_ARG, "%s: rows of weights or out shorter than max_context_len", who);
-  const int32_t splits = weight_splits(batch, tokens, hq, hkv, max_context_len);
+  const WeightPlan a = plan_weights(batch, tokens, hq, hkv, max_context_len);
+  const int32_t splits = a.splits;
   const int64_t need = splits > 1 ? (int64_t)splits * batch * max_context_len * 4 : 0;
   if (workspace_bytes < need || (need > 0 && !workspace))
     return fail(MQA_ERR_INVALID_ARG, "%s: workspace of %lld bytes, %lld needed", who,
@@ -883,11 +894,13 @@ mqa_status paged_attention_weights(mqa_dtype dt, const void* q, mqa_float q_type
   p.bs_shift = block_shift(block_size);
   p.max_ctx = max_context_len;
   p.splits = splits;
+  p.heads_beside = a.heads;
+  p.blocks = a.blocks;
   p.negate = scale < 0.f;
   p.c2 = positive_c2(scale);
   if (debug_enabled())
-    fprintf(stderr, "[mqa_logits] %s Hq=%d Hkv=%d D=%d batch=%d tokens=%d bs=%d splits=%d\n", who, hq, hkv, d,
-            batch, tokens, block_size, splits);
+    fprintf(stderr, "[mqa_logits] %s Hq=%d Hkv=%d D=%d batch=%d tokens=%d bs=%d blocks=%d splits=%d\n", who, hq, hkv, d,
+            batch, tokens, block_size, a.blocks, splits);
   return hip_status(mqa::launch_weights(d, q_type == MQA_F16, p, stream), who);
 }
 

@@ -159,6 +159,9 @@ struct ChunkParams {
   float c2;                  // |scale| * log2(e)
 };
 
+// Blocks of 64 keys that a wave of the weights kernel takes at most.
+constexpr int kWeightBlocks = 8;
+
 struct WeightParams {
   const uint16_t* q;         // [tokens, Hq, D] bf16 or fp16 bits
   int64_t q_stride;
@@ -178,6 +181,8 @@ struct WeightParams {
   int32_t kv_heads, group;
   int32_t num_blocks, bs_shift, max_ctx;
   int32_t splits;            // of the rows of a sequence
+  int32_t heads_beside;      // KV heads that waves of a workgroup take beside each other
+  int32_t blocks;            // of 64 keys that a wave takes, one after the other
   int32_t negate;
   float c2;
 };

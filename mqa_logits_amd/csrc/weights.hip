@@ -16,6 +16,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -77,71 +78,101 @@ struct Seq {
   }
 };
 
-// A wave has 32 * KT keys of a sequence, and goes through the rows of every KV
-// head, 32 at a time: S[key, row] = K Q^T, A = 32 keys x 16 of D, B = 16 of D x
-// 32 rows.  A lane's results are 16 keys of one row, and what it adds up over
-// the rows stays in its registers; the 32 lanes of a key are added at the end.
+// A wave has 64 keys of a sequence and KV head in registers, and goes through the
+// head's rows, 32 at a time:
+//
+//   S[row, key] = Q K^T   A = 32 rows x 16 of D, B = 16 of D x 32 keys
+//
+// A lane's results are 16 rows of one key, so what the rows give to a key is
+// added up in one register, and rows that a tile lacks cost no exponentials.
+// The order of the contracted index is free: half l / 32 of the lanes carries the
+// D/2 elements from l / 32 * D/2 on.
+constexpr int kChunk = 256;                  // rows whose places LDS holds at a time, for a wave
+constexpr int kKeys = 64;                    // of a wave
+
+struct __attribute__((aligned(16))) Places {
+  int64_t at[kChunk];      // first element of a row's query
+  float shift[kChunk];     // -lse, in octaves; -inf for a row that gives nothing
+  int seen[kChunk];        // keys that it sees
+};
+
 template <int D, bool F16>
 struct Wave {
-  static constexpr int kSteps = D / 16;
-  u32x4 k[kSteps];         // key l % 32, elements 16 st + 8 (l / 32) ..
-  f32x16 sum;              // keys i % 4 + 8 (i / 4) + 4 (l / 32) of row l % 32
+  static constexpr int kSteps = D / 16, kHalves = kKeys / 32;
 
-  // K of one KV head.  Whether some scale needs the wide products (fp16 queries).
-  __device__ __forceinline__ bool load_keys(const WeightParams& p, uint32_t block, bool held) {
+  struct RawKeys {
+    u32x4 x[kHalves][D / 64];
+    uint32_t s[kHalves];
+  };
+  u32x4 k[kHalves][kSteps];
+  float sum[kHalves];
+
+  // block: of the lane's key of each half
+  __device__ __forceinline__ static void fetch_keys(RawKeys& r, const WeightParams& p, const uint32_t (&block)[kHalves]) {
     const int half = (threadIdx.x & 63) >> 5;
-    // element order of the contraction: a lane's 16-byte piece of a 32-element
-    // block holds what it multiplies in two steps' halves
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+      const uint8_t* src = p.k + ((uint64_t)block[h] << 4) + half * (D / 4);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) r.x[h][i] = *reinterpret_cast<const u32x4*>(src + i * 16);
+      const uint8_t* sf = p.k_sf + (uint64_t)block[h] + half * (D / 64);
+      r.s[h] = D == 128 ? *reinterpret_cast<const uint16_t*>(sf) : *sf;
+    }
+  }
+
+  // Whether some scale needs the wide products (fp16 queries).
+  __device__ __forceinline__ bool put_keys(const RawKeys& r) {
     bool wide = false;
-    uint32_t s[D / 32];
+    float s[kHalves][D / 64];
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      s[c] = held ? p.k_sf[(uint64_t)block + c] : 127u;
-      wide |= s[c] - kHalfLow > kHalfHigh - kHalfLow;
-      if (s[c] > kLastScale) s[c] = 255;
-    }
+    for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const uint32_t byte = r.s[h] >> (8 * i) & 0xffu;
+        wide |= byte - kHalfLow > kHalfHigh - kHalfLow;
+        s[h][i] = scale_of(byte > kLastScale ? 255u : byte);
+      }
     wide = F16 && __any(wide);
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      const u32x2 x = *reinterpret_cast<const u32x2*>(p.k + ((uint64_t)block << 4) + c * 16 + half * 8);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        k[2 * c + i] = wide || !F16 ? cvt_eight<false>(x[i], scale_of(s[c])) : cvt_eight<true>(x[i], scale_of(s[c]));
-    }
+    if (F16 && !wide)
+      convert<true>(r, s);
+    else
+      convert<false>(r, s);
     return wide;
   }
-
-  struct Row {
-    u32x4 q[kSteps];
-    float shift;           // -lse, in octaves; -inf for a row that counts for nothing
-    int seen;
-  };
-
-  __device__ __forceinline__ static void load_row(Row& x, const WeightParams& p, const Seq& s, int kv_head, int r, int rows) {
-    const int half = (threadIdx.x & 63) >> 5;
-    const int at = min(r, rows - 1), t = at / p.group;
-    const int64_t token = s.first + t;
-    const int head = kv_head * p.group + at - t * p.group;
-    const uint16_t* src = p.q + token * p.q_stride + head * D + half * 16;
+  template <bool HALF>
+  __device__ __forceinline__ void convert(const RawKeys& r, const float (&s)[kHalves][D / 64]) {
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c)
+    for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        x.q[2 * c + i] = *reinterpret_cast<const u32x4*>(src + c * 32 + i * 8);
-        if (p.negate) x.q[2 * c + i] ^= 0x80008000u;
+      for (int st = 0; st < kSteps; ++st) {
+        const uint32_t word = r.x[h][st / 4][st % 4];
+        k[h][st] = cvt_eight<HALF>(word, s[h][st / 4]);
       }
-    const float lse = p.lse[token * (p.kv_heads * p.group) + head];
-    x.shift = r < rows && lse != -__builtin_inff() ? -lse * kLog2e : -__builtin_inff();
-    x.seen = r < rows ? s.seen(t) : 0;
   }
 
-  template <bool WIDE>
-  __device__ __forceinline__ void add(const Row& x, int key0, bool masked, float c2) {
-    const int half = (threadIdx.x & 63) >> 5;
-    f32x16 s;
+  struct Tile { u32x4 q[kSteps]; };
+  __device__ __forceinline__ static void fetch_tile(Tile& x, const WeightParams& p, const Places& places, int tile) {
+    const int lane = threadIdx.x & 63;
+    const uint16_t* src = p.q + places.at[tile * 32 + (lane & 31)] + (lane >> 5) * (D / 2);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = 0.f;
-    asm volatile("" : "+v"(s));              // (a product must not overlap its operands)
+    for (int st = 0; st < kSteps; ++st) x.q[st] = *reinterpret_cast<const u32x4*>(src + st * 8);
+  }
+
+  // rows: that the tile has (FULL: 32).  key0: the first of the keys (MASKED: some
+  // row may not see all of them).
+  template <bool WIDE, bool MASKED, bool FULL>
+  __device__ __forceinline__ void add(const Tile& x, const Places& places, int tile, int rows, int key0, float c2) {
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    f32x4 shift[4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) shift[a] = *reinterpret_cast<const f32x4*>(&places.shift[tile * 32 + 8 * a + 4 * half]);
+    f32x16 s[kHalves];
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[h][i] = 0.f;
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) asm volatile("" : "+v"(s[h]));   // (a product must not overlap its operands)
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) {
       if constexpr (WIDE) {
@@ -156,85 +187,152 @@ struct Wave {
           const float ra = a - bf16_lo(hi[i]), rb = b - bf16_hi(hi[i]);
           lo[i] = pack_bf16(__builtin_isfinite(a) ? ra : 0.f, __builtin_isfinite(b) ? rb : 0.f);
         }
-        s = mma<false>(k[st], hi, s);
-        s = mma<false>(k[st], lo, s);
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
+          s[h] = mma<false>(hi, k[h][st], s[h]);
+          s[h] = mma<false>(lo, k[h][st], s[h]);
+        }
       } else {
-        s = mma<F16>(k[st], x.q[st], s);
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) s[h] = mma<F16>(x.q[st], k[h][st], s[h]);
       }
     }
     // (the compiler was seen to read a product's result too early behind a branch)
-    asm volatile("s_nop 7\n\ts_nop 7" : "+v"(s));
-    if (masked) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c2, x.shift));
-        sum[i] += key0 + (i & 3) + 8 * (i >> 2) + 4 * half < x.seen ? w : 0.f;
+    for (int h = 0; h < kHalves; ++h) asm volatile("s_nop 7\n\ts_nop 7" : "+v"(s[h]));
+    // registers 4 a .. 4 a + 3: rows 8 a + 4 half ..
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      if (!FULL && 8 * a >= rows) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
+          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][4 * a + i], c2, shift[a][i]));
+          if constexpr (MASKED)
+            sum[h] += key0 + h * 32 + (lane & 31) < places.seen[tile * 32 + 8 * a + 4 * half + i] ? w : 0.f;
+          else
+            sum[h] += w;
+        }
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) sum[i] += __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c2, x.shift));
     }
   }
 };
 
+// Waves of a workgroup beside each other: on different KV heads (heads of them,
+// so that whole rows of the cache are read at about the same time), then on the
+// keys that follow.
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 2)
 weights_kernel(const WeightParams p) {
-  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  using W = Wave<D, F16>;
+  constexpr int kHalves = kKeys / 32;
+  __shared__ Places all_places[kWaves];
+  __shared__ float all_sums[kWaves][kWeightBlocks * kKeys];
+  const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int b = blockIdx.y, split = blockIdx.z;
-  const int key0 = (blockIdx.x * kWaves + wave) * 32;
-  if (key0 >= p.max_ctx) return;
+  const int beside = p.heads_beside, first_head = wave % beside;
+  const int wave_keys = p.blocks * kKeys, group_keys = kWaves / beside * wave_keys;   // of the workgroup
+  const int wave_key0 = blockIdx.x * group_keys + wave / beside * wave_keys;
   const Seq s(p, b);
-  float* out = p.part ? p.part + ((int64_t)split * p.batch + b) * p.max_ctx : p.out + b * p.out_stride;
-  Wave<D, F16> w;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) w.sum[i] = 0.f;
-  if (key0 < s.cap && s.n > 0) {
-    const int j = min(key0 + (lane & 31), s.cap - 1);
+  Places& places = all_places[wave];
+  float* const sums = all_sums[wave];
+  for (int i = lane; i < wave_keys; i += 64) sums[i] = 0.f;
+  // this split's rows of each head
+  const int64_t rows_all = (int64_t)s.n * p.group, tiles_all = (rows_all + 31) / 32;
+  const int64_t from = tiles_all * split / p.splits * 32;
+  const int64_t to = min(rows_all, tiles_all * (split + 1) / p.splits * 32);
+  const int blocks = min((s.cap - wave_key0 + kKeys - 1) / kKeys, p.blocks);
+  if (blocks > 0 && from < to) {
     const int32_t* table = p.bt + (int64_t)b * p.bt_stride;
-    const int id = min(max(table[j >> p.bs_shift], 0), p.num_blocks - 1);
-    const uint32_t slot = ((uint32_t)id << p.bs_shift) + (j & (1 << p.bs_shift) - 1);
-    const int rows = s.n * p.group, tiles = (rows + 31) / 32;
-    // this split's tiles of all KV heads', end to end
-    const int64_t all = (int64_t)tiles * p.kv_heads;
-    int64_t at = all * split / p.splits;
-    const int64_t end = all * (split + 1) / p.splits;
-    while (at < end) {
-      const int kv_head = (int)(at / tiles);
-      int tile = (int)(at - (int64_t)kv_head * tiles);
-      const int last = (int)min((int64_t)tiles, tile + end - at);
-      at += last - tile;
-      const bool wide = w.load_keys(p, (slot * p.kv_heads + kv_head) * (D / 32), true);
-      typename Wave<D, F16>::Row x;
-      for (; tile < last; ++tile) {
-        // rows whose last sees none of the keys
-        const int r = tile * 32;
-        if (s.seen(min(r + 31, rows - 1) / p.group) <= key0) continue;
-        w.load_row(x, p, s, kv_head, r + (lane & 31), rows);
-        const bool masked = r + 32 > rows || s.seen(r / p.group) < key0 + 32;
-        if (F16 && wide)
-          w.template add<F16>(x, key0, masked, p.c2);
-        else
-          w.template add<false>(x, key0, masked, p.c2);
+    const auto fetch = [&](typename W::RawKeys& raw, int block, int head) {
+      uint32_t first[kHalves];
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        const int j = min(wave_key0 + block * kKeys + h * 32 + (lane & 31), s.cap - 1);
+        const int id = min(max(table[j >> p.bs_shift], 0), p.num_blocks - 1);
+        const uint32_t slot = ((uint32_t)id << p.bs_shift) + (j & (1 << p.bs_shift) - 1);
+        first[h] = (slot * p.kv_heads + head) * (D / 32);
+      }
+      W::fetch_keys(raw, p, first);
+    };
+    W w;
+    typename W::RawKeys raw;
+    typename W::Tile x[2];
+    fetch(raw, 0, first_head);
+    for (int head = first_head; head < p.kv_heads; head += beside) {
+      for (int64_t r0 = from; r0 < to; r0 += kChunk) {
+        const int rows = (int)min(to - r0, (int64_t)kChunk), tiles = (rows + 31) / 32;
+        __builtin_amdgcn_wave_barrier();
+        bool left_out = false;               // a row that gives nothing, whatever its scores
+        for (int i = 0; i < tiles * 32; i += 64) {
+          const int r = min(i + lane, rows - 1);
+          const int t = (int)((r0 + r) / p.group);
+          const int q_head = head * p.group + (int)(r0 + r - (int64_t)t * p.group);
+          const int64_t token = s.first + t;
+          const float lse = p.lse[token * (p.kv_heads * p.group) + q_head];
+          const bool gives = i + lane < rows && lse != -__builtin_inff();
+          left_out |= i + lane < rows && !gives;
+          places.at[i + lane] = token * p.q_stride + q_head * D;
+          places.shift[i + lane] = gives ? -lse * kLog2e : -__builtin_inff();
+          places.seen[i + lane] = gives ? s.seen(t) : 0;
+        }
+        __builtin_amdgcn_wave_barrier();
+        const bool some_left_out = __any(left_out);
+        const int most = s.seen((int)((r0 + rows - 1) / p.group));
+        W::fetch_tile(x[0], p, places, 0);
+        for (int block = 0; block < blocks; ++block) {
+          const int key0 = wave_key0 + block * kKeys;
+          const bool wide = w.put_keys(raw);
+          // the next block, or the first of the next rows or the next head
+          const bool again = block + 1 == blocks, more_rows = r0 + kChunk < to;
+          fetch(raw, again ? 0 : block + 1, again && !more_rows ? min(head + beside, p.kv_heads - 1) : head);
+          if (most <= key0) continue;        // none of these rows sees it (x[0] still is their first tile)
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) w.sum[h] = 0.f;
+          const auto work = [&](int t, typename W::Tile& here, typename W::Tile& next) {
+            if (tiles > 1) W::fetch_tile(next, p, places, t + 1 < tiles ? t + 1 : 0);
+            const int n = min(rows - t * 32, 32);
+            const bool masked = some_left_out || s.seen((int)((r0 + t * 32) / p.group)) < key0 + kKeys;
+            if (F16 && wide)
+              w.template add<F16, true, false>(here, places, t, n, key0, p.c2);
+            else if (masked)
+              w.template add<false, true, false>(here, places, t, n, key0, p.c2);
+            else if (n == 32)
+              w.template add<false, false, true>(here, places, t, n, key0, p.c2);
+            else
+              w.template add<false, false, false>(here, places, t, n, key0, p.c2);
+          };
+#pragma nounroll
+          for (int t = 0; t < tiles; t += 2) {
+            work(t, x[0], x[1]);
+            if (t + 1 < tiles)
+              work(t + 1, x[1], x[0]);
+            else if (tiles > 1)
+              x[0] = x[1];
+          }
+          // the two halves' rows
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) {
+            const float y = w.sum[h] + __shfl_xor(w.sum[h], 32);
+            if (lane < 32) sums[block * kKeys + h * 32 + lane] += y;
+          }
+        }
       }
     }
   }
-  // the 32 lanes of a key: key i of 16 ends up in lane i of each half
-  float mine = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float x = w.sum[i];
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) x += __shfl_xor(x, off);
-    mine = (lane & 31) == i ? x : mine;
-  }
-  const int i = lane & 31, key = key0 + (i & 3) + 8 * (i >> 2) + 4 * half;
-  if (i < 16 && key < p.max_ctx) {
+  // the heads beside each other
+  __syncthreads();
+  for (int i = tid; i < group_keys; i += kThreads) {
+    const int key = blockIdx.x * group_keys + i;
+    if (key >= p.max_ctx) break;
+    float x = 0.f;
+    for (int j = 0; j < beside; ++j) x += all_sums[i / wave_keys * beside + j][i % wave_keys];
     if (p.part)
-      out[key] = mine;
+      p.part[((int64_t)split * p.batch + b) * p.max_ctx + key] = x;
     else
-      out[key] = key < s.cap ? (p.before ? p.before[b * p.before_stride + key] + mine : mine) : 0.f;
+      p.out[b * p.out_stride + key] = key < s.cap ? (p.before ? p.before[b * p.before_stride + key] + x : x) : 0.f;
   }
 }
 
@@ -254,8 +352,8 @@ weights_join_kernel(const WeightParams p) {
 
 template <int D, bool F16>
 hipError_t launch(const WeightParams& p, hipStream_t s) {
-  constexpr int kKeys = 32 * kWaves;
-  weights_kernel<D, F16><<<dim3((p.max_ctx + kKeys - 1) / kKeys, p.batch, p.splits), kThreads, 0, s>>>(p);
+  const int keys = kWaves / p.heads_beside * kKeys * p.blocks;
+  weights_kernel<D, F16><<<dim3((p.max_ctx + keys - 1) / keys, p.batch, p.splits), kThreads, 0, s>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.part) return e;
   weights_join_kernel<<<dim3((p.max_ctx + 255) / 256, p.batch), 256, 0, s>>>(p);
