@@ -320,20 +320,23 @@ mqa_status check_chunk_cache(mqa_dtype dt, const void* q, mqa_float q_type, int6
 // KV heads that the four waves of a workgroup take beside each other.
 int32_t weight_heads(int32_t hkv) { return hkv >= 4 ? 4 : hkv == 2 ? 2 : 1; }
 
-// A weights call's split: blocks of 64 keys that a wave takes one after the other
-// (what it reads of the rows then serves them all), as many as leave four
-// workgroups for each compute unit; where there are fewer, parts that the rows of a sequence are
-// cut into, as far as there are tiles of 32 rows to share.
+// A weights call's split.  Usual sequences of more than 32 rows a KV head: 256
+// keys a workgroup (blocks 0).  Others: blocks of 64 keys that a wave takes one after the
+// other (what it reads of the rows then serves them all), as many as leave eight
+// workgroups for each compute unit.  Where the keys give fewer, parts that the rows
+// are cut into, as far as there are enough of them.
 struct WeightPlan {
   int32_t heads, blocks, splits;
 };
 WeightPlan plan_weights(int32_t batch, int32_t tokens, int32_t hq, int32_t hkv, int32_t max_context_len) {
   WeightPlan a{};
-  a.heads = weight_heads(hkv);
+  const int64_t rows = ((int64_t)tokens * (hq / hkv) + batch - 1) / batch;   // of a usual sequence and KV head
+  const bool many = rows > 32;
+  a.heads = many ? 1 : weight_heads(hkv);
   const int64_t keys = 256 / a.heads, groups = (int64_t)batch * ((max_context_len + keys - 1) / keys);
-  a.blocks = (int32_t)std::clamp<int64_t>(groups / 2048, 1, mqa::kWeightBlocks);
-  const int64_t tiles = ((int64_t)tokens * (hq / hkv) / batch + 31) / 32;   // of a usual sequence and KV head
-  a.splits = (int32_t)std::clamp<int64_t>(std::min<int64_t>(512 / std::max<int64_t>(groups, 1), tiles / 2), 1, 64);
+  a.blocks = many ? 0 : (int32_t)std::clamp<int64_t>(groups / 2048, 1, mqa::kWeightBlocks);
+  const int64_t most = many ? (rows + 63) / 64 * hkv / 4 : 1;
+  a.splits = (int32_t)std::clamp<int64_t>(std::min<int64_t>(1536 / std::max<int64_t>(groups, 1), most), 1, 64);
   return a;
 }
 

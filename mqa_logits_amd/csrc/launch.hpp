@@ -182,7 +182,7 @@ struct WeightParams {
   int32_t num_blocks, bs_shift, max_ctx;
   int32_t splits;            // of the rows of a sequence
   int32_t heads_beside;      // KV heads that waves of a workgroup take beside each other
-  int32_t blocks;            // of 64 keys that a wave takes, one after the other
+  int32_t blocks;            // of 64 keys that a wave takes, one after the other (0: many rows)
   int32_t negate;
   float c2;
 };

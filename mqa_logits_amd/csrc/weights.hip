@@ -160,7 +160,7 @@ struct Wave {
 
   // rows: that the tile has (FULL: 32).  key0: the first of the keys (MASKED: some
   // row may not see all of them).
-  template <bool WIDE, bool MASKED, bool FULL>
+  template <bool WIDE, bool MASKED, bool FULL, class Places>
   __device__ __forceinline__ void add(const Tile& x, const Places& places, int tile, int rows, int key0, float c2) {
     const int lane = threadIdx.x & 63, half = lane >> 5;
     f32x4 shift[4];
@@ -219,7 +219,13 @@ struct Wave {
   }
 };
 
-// Waves of a workgroup beside each other: on different KV heads (heads of them,
+// Pool slot of key j, the first of 16 of a block (the 16 have slots in a row).
+__device__ __forceinline__ uint32_t slot_of(const WeightParams& p, const int32_t* table, int j) {
+  const int id = min(max(table[j >> p.bs_shift], 0), p.num_blocks - 1);
+  return ((uint32_t)id << p.bs_shift) + (j & (1 << p.bs_shift) - 1);
+}
+
+// Few rows.  Waves of a workgroup beside each other: on different KV heads (heads of them,
 // so that whole rows of the cache are read at about the same time), then on the
 // keys that follow.
 template <int D, bool F16>
@@ -229,6 +235,7 @@ weights_kernel(const WeightParams p) {
   constexpr int kHalves = kKeys / 32;
   __shared__ Places all_places[kWaves];
   __shared__ float all_sums[kWaves][kWeightBlocks * kKeys];
+  __shared__ uint32_t all_slots[kWaves][kWeightBlocks * kKeys / 16];   // of every 16th key
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int b = blockIdx.y, split = blockIdx.z;
@@ -246,14 +253,15 @@ weights_kernel(const WeightParams p) {
   const int blocks = min((s.cap - wave_key0 + kKeys - 1) / kKeys, p.blocks);
   if (blocks > 0 && from < to) {
     const int32_t* table = p.bt + (int64_t)b * p.bt_stride;
+    uint32_t* const slots = all_slots[wave];
+    if (lane < blocks * (kKeys / 16)) slots[lane] = slot_of(p, table, min(wave_key0 + lane * 16, s.cap - 1) & ~15);
+    __builtin_amdgcn_wave_barrier();
     const auto fetch = [&](typename W::RawKeys& raw, int block, int head) {
       uint32_t first[kHalves];
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
-        const int j = min(wave_key0 + block * kKeys + h * 32 + (lane & 31), s.cap - 1);
-        const int id = min(max(table[j >> p.bs_shift], 0), p.num_blocks - 1);
-        const uint32_t slot = ((uint32_t)id << p.bs_shift) + (j & (1 << p.bs_shift) - 1);
-        first[h] = (slot * p.kv_heads + head) * (D / 32);
+        const int i = block * kKeys + h * 32 + (lane & 31);
+        first[h] = ((slots[i >> 4] + (i & 15)) * p.kv_heads + head) * (D / 32);
       }
       W::fetch_keys(raw, p, first);
     };
@@ -336,6 +344,152 @@ weights_kernel(const WeightParams p) {
   }
 }
 
+// Many rows: 64 at a time go through LDS to the workgroup's four waves, which have
+// 64 keys each.  (Read from global memory by every wave for itself, 16 bytes of
+// each of 32 rows at a time, they kept the address unit busy for most of the time.)
+constexpr int kStageRows = 64;
+
+template <int D>
+struct __attribute__((aligned(16))) StageRows {
+  static constexpr int kPitch = D * 2 + 16;  // bytes; free of bank conflicts
+  char q[kStageRows * kPitch];
+  float shift[kStageRows];
+  int seen[kStageRows];
+  int left_out;            // a row that gives nothing, whatever its scores
+};
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 2)
+weights_wide_kernel(const WeightParams p) {
+  using W = Wave<D, F16>;
+  constexpr int kHalves = kKeys / 32, kGroupKeys = kWaves * kKeys;
+  constexpr int kLoads = kStageRows * D * 2 / 16 / kThreads, kRowsALoad = kThreads / 8;
+  __shared__ StageRows<D> stage[2];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int b = blockIdx.y, split = blockIdx.z;
+  const int group_key0 = blockIdx.x * kGroupKeys, key0 = group_key0 + wave * kKeys;
+  const Seq s(p, b);
+  W w;
+#pragma unroll
+  for (int h = 0; h < kHalves; ++h) w.sum[h] = 0.f;
+  // this split's pieces of 64 rows, of all KV heads' end to end
+  const int rows = s.n * p.group, pieces = (rows + kStageRows - 1) / kStageRows;
+  const int64_t all = (int64_t)pieces * p.kv_heads;
+  int64_t at = all * split / p.splits;
+  const int64_t end = all * (split + 1) / p.splits;
+  if (group_key0 < s.cap && at < end) {
+    const int32_t* table = p.bt + (int64_t)b * p.bt_stride;
+    uint32_t slot[kHalves];
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+      const int j = min(key0 + h * 32 + (lane & 31), s.cap - 1);
+      slot[h] = slot_of(p, table, j & ~15) + (j & 15);
+    }
+    int head = (int)(at / pieces), piece = (int)(at - (int64_t)head * pieces);
+    // the first piece whose last row sees some of the keys
+    const auto skip = [&] {
+      while (at < end && s.seen((min(piece * kStageRows + kStageRows, rows) - 1) / p.group) <= group_key0) {
+        ++at;
+        if (++piece == pieces) {
+          piece = 0;
+          ++head;
+        }
+      }
+    };
+    u32x4 raw[kLoads];
+    float lse = 0.f;
+    int seen = 0;
+    const auto fetch = [&] {
+      const int last = rows - 1;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        constexpr int kPieces = D / 64;      // of 128 bytes of a row
+        const int r = min(piece * kStageRows + i / kPieces * kRowsALoad + tid / 8, last), t = r / p.group;
+        const uint16_t* src = p.q + (int64_t)(s.first + t) * p.q_stride + (head * p.group + r - t * p.group) * D;
+        raw[i] = *reinterpret_cast<const u32x4*>(src + (i % kPieces * 8 + tid % 8) * 8);
+      }
+      if (wave == 0) {
+        const int r = piece * kStageRows + lane, t = min(r, last) / p.group;
+        lse = p.lse[(int64_t)(s.first + t) * (p.kv_heads * p.group) + head * p.group + min(r, last) - t * p.group];
+        seen = r <= last ? s.seen(t) : -1;   // (-1: no row)
+      }
+    };
+    const auto put = [&](StageRows<D>& x) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        constexpr int kPieces = D / 64;
+        *reinterpret_cast<u32x4*>(x.q + (i / kPieces * kRowsALoad + tid / 8) * StageRows<D>::kPitch +
+                                  (i % kPieces * 8 + tid % 8) * 16) = raw[i];
+      }
+      if (wave == 0) {
+        const bool gives = seen >= 0 && lse != -__builtin_inff();
+        x.shift[lane] = gives ? -lse * kLog2e : -__builtin_inff();
+        x.seen[lane] = gives ? seen : 0;
+        const bool left_out = __any(seen >= 0 && !gives);
+        if (lane == 0) x.left_out = left_out;
+      }
+    };
+    skip();
+    if (at < end) fetch();
+    int buffer = 0, have = -1;
+    bool wide = false;
+    while (at < end) {
+      if (head != have) {
+        have = head;
+        uint32_t first[kHalves];
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) first[h] = (slot[h] * p.kv_heads + head) * (D / 32);
+        typename W::RawKeys keys;
+        W::fetch_keys(keys, p, first);
+        wide = w.put_keys(keys);
+      }
+      StageRows<D>& x = stage[buffer];
+      put(x);
+      const int n = min(rows - piece * kStageRows, kStageRows), row0 = piece * kStageRows;
+      ++at;
+      if (++piece == pieces) {
+        piece = 0;
+        ++head;
+      }
+      skip();
+      if (at < end) fetch();
+      __syncthreads();
+      // (one barrier a piece: before the buffer is written again, every wave has
+      // passed the next piece's)
+      buffer ^= 1;
+      const bool masked = x.left_out || s.seen(row0 / p.group) < key0 + kKeys;
+#pragma unroll
+      for (int t = 0; t < kStageRows / 32; ++t) {
+        if (t * 32 >= n) break;
+        const char* q = x.q + (t * 32 + (lane & 31)) * StageRows<D>::kPitch + (lane >> 5) * D;
+        typename W::Tile tile;
+#pragma unroll
+        for (int st = 0; st < D / 16; ++st) tile.q[st] = *reinterpret_cast<const u32x4*>(q + st * 16);
+        if (F16 && wide)
+          w.template add<F16, true, false>(tile, x, t, n - t * 32, key0, p.c2);
+        else if (masked)
+          w.template add<false, true, false>(tile, x, t, n - t * 32, key0, p.c2);
+        else if (n - t * 32 >= 32)
+          w.template add<false, false, true>(tile, x, t, 32, key0, p.c2);
+        else
+          w.template add<false, false, false>(tile, x, t, n - t * 32, key0, p.c2);
+      }
+    }
+  }
+  // the two halves' rows
+#pragma unroll
+  for (int h = 0; h < kHalves; ++h) {
+    const float x = w.sum[h] + __shfl_xor(w.sum[h], 32);
+    const int key = key0 + h * 32 + lane;
+    if (lane >= 32 || key >= p.max_ctx) continue;
+    if (p.part)
+      p.part[((int64_t)split * p.batch + b) * p.max_ctx + key] = x;
+    else
+      p.out[b * p.out_stride + key] = key < s.cap ? (p.before ? p.before[b * p.before_stride + key] + x : x) : 0.f;
+  }
+}
+
 // Adds the splits' sums, in their order.
 __global__ void __launch_bounds__(256)
 weights_join_kernel(const WeightParams p) {
@@ -352,8 +506,13 @@ weights_join_kernel(const WeightParams p) {
 
 template <int D, bool F16>
 hipError_t launch(const WeightParams& p, hipStream_t s) {
-  const int keys = kWaves / p.heads_beside * kKeys * p.blocks;
-  weights_kernel<D, F16><<<dim3((p.max_ctx + keys - 1) / keys, p.batch, p.splits), kThreads, 0, s>>>(p);
+  if (p.blocks == 0) {
+    constexpr int keys = kWaves * kKeys;
+    weights_wide_kernel<D, F16><<<dim3((p.max_ctx + keys - 1) / keys, p.batch, p.splits), kThreads, 0, s>>>(p);
+  } else {
+    const int keys = kWaves / p.heads_beside * kKeys * p.blocks;
+    weights_kernel<D, F16><<<dim3((p.max_ctx + keys - 1) / keys, p.batch, p.splits), kThreads, 0, s>>>(p);
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.part) return e;
   weights_join_kernel<<<dim3((p.max_ctx + 255) / 256, p.batch), 256, 0, s>>>(p);
