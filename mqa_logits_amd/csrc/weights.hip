@@ -171,8 +171,13 @@ struct Wave {
     for (int h = 0; h < kHalves; ++h)
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[h][i] = 0.f;
+    // A product must not overlap its operands.  The compiler was seen to let one
+    // with a constant 0 to add to overlap them: the zeros are registers, or the
+    // operands are used once more behind it.
+    if constexpr (WIDE) {
 #pragma unroll
-    for (int h = 0; h < kHalves; ++h) asm volatile("" : "+v"(s[h]));   // (a product must not overlap its operands)
+      for (int h = 0; h < kHalves; ++h) asm volatile("" : "+v"(s[h]));
+    }
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) {
       if constexpr (WIDE) {
@@ -195,6 +200,10 @@ struct Wave {
       } else {
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) s[h] = mma<F16>(x.q[st], k[h][st], s[h]);
+        if (st == 0) {
+          __builtin_amdgcn_sched_barrier(0);
+          asm volatile("" ::"v"(x.q[0]));
+        }
       }
     }
     // (the compiler was seen to read a product's result too early behind a branch)
@@ -214,6 +223,58 @@ struct Wave {
           else
             sum[h] += w;
         }
+      }
+    }
+  }
+};
+
+// A tile's scores whose weights are still to be formed.
+template <int D, bool F16>
+struct Pending {
+  f32x16 s[kKeys / 32];
+  f32x4 shift[4];
+  __device__ __forceinline__ void clear() {  // of no rows
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) shift[a][i] = -__builtin_inff();
+#pragma unroll
+    for (int h = 0; h < kKeys / 32; ++h)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[h][i] = 0.f;
+  }
+  // registers i of 16
+  __device__ __forceinline__ void form(Wave<D, F16>& w, int i, float c2) const {
+#pragma unroll
+    for (int h = 0; h < kKeys / 32; ++h)
+      w.sum[h] += __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][i], c2, shift[i >> 2][i & 3]));
+  }
+  // The products of 32 rows in LDS (32 rows that give to every key), with the weights
+  // of the tile before formed between them: the matrix cores and the vector ALU
+  // work side by side.
+  __device__ __forceinline__ void multiply(Wave<D, F16>& w, const char* q, const float* shifts, const Pending& before, float c2) {
+    constexpr int kSteps = D / 16, kHalves = kKeys / 32, kAhead = 4;
+    u32x4 a[kAhead];
+#pragma unroll
+    for (int st = 0; st < kAhead; ++st) a[st] = *reinterpret_cast<const u32x4*>(q + st * 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) shift[i] = *reinterpret_cast<const f32x4*>(shifts + 8 * i);
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[h][i] = 0.f;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st) {
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        s[h] = mma<F16>(a[st % kAhead], w.k[h][st], s[h]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (st == 0) asm volatile("" ::"v"(a[0]));     // (as in Wave::add)
+#pragma unroll
+        for (int i = 0; i < 16 / kSteps / kHalves; ++i) before.form(w, (st * kHalves + h) * (16 / kSteps / kHalves) + i, c2);
+        if (h == kHalves - 1 && st + kAhead < kSteps) a[st % kAhead] = *reinterpret_cast<const u32x4*>(q + (st + kAhead) * 16);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
@@ -267,7 +328,7 @@ weights_kernel(const WeightParams p) {
     };
     W w;
     typename W::RawKeys raw;
-    typename W::Tile x[2];
+    typename W::Tile x;
     fetch(raw, 0, first_head);
     for (int head = first_head; head < p.kv_heads; head += beside) {
       for (int64_t r0 = from; r0 < to; r0 += kChunk) {
@@ -289,36 +350,29 @@ weights_kernel(const WeightParams p) {
         __builtin_amdgcn_wave_barrier();
         const bool some_left_out = __any(left_out);
         const int most = s.seen((int)((r0 + rows - 1) / p.group));
-        W::fetch_tile(x[0], p, places, 0);
+        W::fetch_tile(x, p, places, 0);
         for (int block = 0; block < blocks; ++block) {
           const int key0 = wave_key0 + block * kKeys;
           const bool wide = w.put_keys(raw);
           // the next block, or the first of the next rows or the next head
           const bool again = block + 1 == blocks, more_rows = r0 + kChunk < to;
           fetch(raw, again ? 0 : block + 1, again && !more_rows ? min(head + beside, p.kv_heads - 1) : head);
-          if (most <= key0) continue;        // none of these rows sees it (x[0] still is their first tile)
+          if (most <= key0) continue;        // none of these rows sees it
 #pragma unroll
           for (int h = 0; h < kHalves; ++h) w.sum[h] = 0.f;
-          const auto work = [&](int t, typename W::Tile& here, typename W::Tile& next) {
-            if (tiles > 1) W::fetch_tile(next, p, places, t + 1 < tiles ? t + 1 : 0);
+#pragma nounroll
+          for (int t = 0; t < tiles; ++t) {
+            if (tiles > 1) W::fetch_tile(x, p, places, t);
             const int n = min(rows - t * 32, 32);
             const bool masked = some_left_out || s.seen((int)((r0 + t * 32) / p.group)) < key0 + kKeys;
             if (F16 && wide)
-              w.template add<F16, true, false>(here, places, t, n, key0, p.c2);
+              w.template add<F16, true, false>(x, places, t, n, key0, p.c2);
             else if (masked)
-              w.template add<false, true, false>(here, places, t, n, key0, p.c2);
+              w.template add<false, true, false>(x, places, t, n, key0, p.c2);
             else if (n == 32)
-              w.template add<false, false, true>(here, places, t, n, key0, p.c2);
+              w.template add<false, false, true>(x, places, t, n, key0, p.c2);
             else
-              w.template add<false, false, false>(here, places, t, n, key0, p.c2);
-          };
-#pragma nounroll
-          for (int t = 0; t < tiles; t += 2) {
-            work(t, x[0], x[1]);
-            if (t + 1 < tiles)
-              work(t + 1, x[1], x[0]);
-            else if (tiles > 1)
-              x[0] = x[1];
+              w.template add<false, false, false>(x, places, t, n, key0, p.c2);
           }
           // the two halves' rows
 #pragma unroll
@@ -376,9 +430,8 @@ weights_wide_kernel(const WeightParams p) {
   // this split's pieces of 64 rows, of all KV heads' end to end
   const int rows = s.n * p.group, pieces = (rows + kStageRows - 1) / kStageRows;
   const int64_t all = (int64_t)pieces * p.kv_heads;
-  int64_t at = all * split / p.splits;
-  const int64_t end = all * (split + 1) / p.splits;
-  if (group_key0 < s.cap && at < end) {
+  const int64_t begin = all * split / p.splits, end = all * (split + 1) / p.splits;
+  if (group_key0 < s.cap && begin < end) {
     const int32_t* table = p.bt + (int64_t)b * p.bt_stride;
     uint32_t slot[kHalves];
 #pragma unroll
@@ -386,33 +439,65 @@ weights_wide_kernel(const WeightParams p) {
       const int j = min(key0 + h * 32 + (lane & 31), s.cap - 1);
       slot[h] = slot_of(p, table, j & ~15) + (j & 15);
     }
-    int head = (int)(at / pieces), piece = (int)(at - (int64_t)head * pieces);
-    // the first piece whose last row sees some of the keys
-    const auto skip = [&] {
-      while (at < end && s.seen((min(piece * kStageRows + kStageRows, rows) - 1) / p.group) <= group_key0) {
-        ++at;
-        if (++piece == pieces) {
-          piece = 0;
-          ++head;
-        }
+    // Rows that see some of the keys follow those that do not: the first such piece.
+    const int64_t blind = min(max((int64_t)group_key0 - s.base, (int64_t)0), (int64_t)s.n);   // tokens
+    const int first_piece = (int)(blind * p.group / kStageRows);
+    int head = (int)(begin / pieces), piece = max((int)(begin - (int64_t)head * pieces), first_piece);
+    const int last_head = (int)((end - 1) / pieces), last_piece = (int)(end - 1 - (int64_t)last_head * pieces);
+    // (token, head of the group) of the rows that this thread loads, and of the one
+    // whose lse wave 0's lanes load: from piece to piece they move by 64 rows
+    const int step_t = kStageRows / p.group, step_h = kStageRows - step_t * p.group;
+    struct Row {
+      int t, h;
+    };
+    Row mine[kStageRows / kRowsALoad], of_lse, front;
+    const auto place = [&](Row& x, int r) {
+      x.t = r / p.group;
+      x.h = r - x.t * p.group;
+    };
+    const auto place_all = [&] {
+#pragma unroll
+      for (int i = 0; i < kStageRows / kRowsALoad; ++i) place(mine[i], piece * kStageRows + i * kRowsALoad + tid / 8);
+      place(of_lse, piece * kStageRows + lane);
+      place(front, piece * kStageRows);
+    };
+    const auto move = [&](Row& x) {
+      x.t += step_t;
+      x.h += step_h;
+      if (x.h >= p.group) {
+        x.h -= p.group;
+        ++x.t;
       }
     };
+    // whether there is a piece at (head, piece); past a head's last, the next one's first
+    bool more = true;
+    const auto settle = [&](bool moved) {
+      if (piece >= pieces) {
+        piece = first_piece;
+        ++head;
+        moved = true;
+      }
+      more = piece < pieces && (head < last_head || (head == last_head && piece <= last_piece));
+      if (more && moved) place_all();
+    };
+    settle(true);
     u32x4 raw[kLoads];
     float lse = 0.f;
     int seen = 0;
     const auto fetch = [&] {
-      const int last = rows - 1;
+      constexpr int kPieces = D / 64;        // of 128 bytes of a row
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        constexpr int kPieces = D / 64;      // of 128 bytes of a row
-        const int r = min(piece * kStageRows + i / kPieces * kRowsALoad + tid / 8, last), t = r / p.group;
-        const uint16_t* src = p.q + (int64_t)(s.first + t) * p.q_stride + (head * p.group + r - t * p.group) * D;
-        raw[i] = *reinterpret_cast<const u32x4*>(src + (i % kPieces * 8 + tid % 8) * 8);
+      for (int i = 0; i < kStageRows / kRowsALoad; ++i) {
+        // (past the last row, the last token's)
+        const int64_t token = s.first + min(mine[i].t, s.n - 1);
+        const uint16_t* src = p.q + token * p.q_stride + (head * p.group + mine[i].h) * D + tid % 8 * 8;
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) raw[i * kPieces + j] = *reinterpret_cast<const u32x4*>(src + j * 64);
       }
       if (wave == 0) {
-        const int r = piece * kStageRows + lane, t = min(r, last) / p.group;
-        lse = p.lse[(int64_t)(s.first + t) * (p.kv_heads * p.group) + head * p.group + min(r, last) - t * p.group];
-        seen = r <= last ? s.seen(t) : -1;   // (-1: no row)
+        const int64_t token = s.first + min(of_lse.t, s.n - 1);
+        lse = p.lse[token * (p.kv_heads * p.group) + head * p.group + of_lse.h];
+        seen = of_lse.t < s.n ? s.seen(of_lse.t) : -1;   // (-1: no row)
       }
     };
     const auto put = [&](StageRows<D>& x) {
@@ -430,11 +515,16 @@ weights_wide_kernel(const WeightParams p) {
         if (lane == 0) x.left_out = left_out;
       }
     };
-    skip();
-    if (at < end) fetch();
+    if (more) fetch();
     int buffer = 0, have = -1;
     bool wide = false;
-    while (at < end) {
+    Pending<D, F16> pending[2];
+    pending[1].clear();
+    const auto finish = [&] {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pending[1].form(w, i, p.c2);
+    };
+    while (more) {
       if (head != have) {
         have = head;
         uint32_t first[kHalves];
@@ -446,19 +536,28 @@ weights_wide_kernel(const WeightParams p) {
       }
       StageRows<D>& x = stage[buffer];
       put(x);
-      const int n = min(rows - piece * kStageRows, kStageRows), row0 = piece * kStageRows;
-      ++at;
-      if (++piece == pieces) {
-        piece = 0;
-        ++head;
-      }
-      skip();
-      if (at < end) fetch();
+      const int n = min(rows - piece * kStageRows, kStageRows), front_seen = s.seen(front.t);
+      ++piece;
+#pragma unroll
+      for (int i = 0; i < kStageRows / kRowsALoad; ++i) move(mine[i]);
+      move(of_lse);
+      move(front);
+      settle(false);
+      if (more) fetch();
       __syncthreads();
       // (one barrier a piece: before the buffer is written again, every wave has
       // passed the next piece's)
       buffer ^= 1;
-      const bool masked = x.left_out || s.seen(row0 / p.group) < key0 + kKeys;
+      const bool masked = x.left_out || front_seen < key0 + kKeys;
+      if (!masked && n == kStageRows && !(F16 && wide)) {
+        const char* q = x.q + (lane & 31) * StageRows<D>::kPitch + (lane >> 5) * D;
+        const float* shifts = x.shift + 4 * (lane >> 5);
+        pending[0].multiply(w, q, shifts, pending[1], p.c2);
+        pending[1].multiply(w, q + 32 * StageRows<D>::kPitch, shifts + 32, pending[0], p.c2);
+        continue;
+      }
+      finish();
+      pending[1].clear();
 #pragma unroll
       for (int t = 0; t < kStageRows / 32; ++t) {
         if (t * 32 >= n) break;
@@ -470,12 +569,11 @@ weights_wide_kernel(const WeightParams p) {
           w.template add<F16, true, false>(tile, x, t, n - t * 32, key0, p.c2);
         else if (masked)
           w.template add<false, true, false>(tile, x, t, n - t * 32, key0, p.c2);
-        else if (n - t * 32 >= 32)
-          w.template add<false, false, true>(tile, x, t, 32, key0, p.c2);
         else
           w.template add<false, false, false>(tile, x, t, n - t * 32, key0, p.c2);
       }
     }
+    finish();
   }
   // the two halves' rows
 #pragma unroll
