@@ -202,7 +202,8 @@ struct Wave {
         for (int h = 0; h < kHalves; ++h) s[h] = mma<F16>(x.q[st], k[h][st], s[h]);
         if (st == 0) {
           __builtin_amdgcn_sched_barrier(0);
-          asm volatile("" ::"v"(x.q[0]));
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) asm volatile("" ::"v"(x.q[0]), "v"(k[h][0]));
         }
       }
     }
@@ -264,18 +265,32 @@ struct Pending {
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[h][i] = 0.f;
     __builtin_amdgcn_sched_barrier(0);
+    // A weight is scaled and shifted beside one product, its exponential taken beside
+    // the next and added beside the one after that, so that none waits for another.
+    constexpr int kSlots = kSteps * kHalves, kEach = 16 / kSlots;
+    float x[kHalves][kEach], y[kHalves][kEach];
 #pragma unroll
-    for (int st = 0; st < kSteps; ++st) {
-#pragma unroll
-      for (int h = 0; h < kHalves; ++h) {
+    for (int n = 0; n < kSlots + 2; ++n) {
+      if (n < kSlots) {
+        const int st = n / kHalves, h = n % kHalves;
         s[h] = mma<F16>(a[st % kAhead], w.k[h][st], s[h]);
         __builtin_amdgcn_sched_barrier(0);
-        if (st == 0) asm volatile("" ::"v"(a[0]));     // (as in Wave::add)
-#pragma unroll
-        for (int i = 0; i < 16 / kSteps / kHalves; ++i) before.form(w, (st * kHalves + h) * (16 / kSteps / kHalves) + i, c2);
-        if (h == kHalves - 1 && st + kAhead < kSteps) a[st % kAhead] = *reinterpret_cast<const u32x4*>(q + (st + kAhead) * 16);
-        __builtin_amdgcn_sched_barrier(0);
+        if (st == 0) asm volatile("" ::"v"(a[0]), "v"(w.k[h][0]));   // (as in Wave::add)
+        if (h == kHalves - 1 && st + kAhead < kSteps)
+          a[st % kAhead] = *reinterpret_cast<const u32x4*>(q + (st + kAhead) * 16);
       }
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+          if (n >= 2) w.sum[h] += y[h][e];
+          if (n >= 1 && n <= kSlots) y[h][e] = __builtin_amdgcn_exp2f(x[h][e]);
+          if (n < kSlots) {
+            const int i = n * kEach + e;
+            x[h][e] = __builtin_fmaf(before.s[h][i], c2, before.shift[i >> 2][i & 3]);
+          }
+        }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 };
@@ -422,7 +437,8 @@ weights_wide_kernel(const WeightParams p) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int b = blockIdx.y, split = blockIdx.z;
-  const int group_key0 = blockIdx.x * kGroupKeys, key0 = group_key0 + wave * kKeys;
+  // (the last keys first: their rows end among them, which takes longer)
+  const int group_key0 = (gridDim.x - 1 - blockIdx.x) * kGroupKeys, key0 = group_key0 + wave * kKeys;
   const Seq s(p, b);
   W w;
 #pragma unroll
@@ -521,6 +537,9 @@ weights_wide_kernel(const WeightParams p) {
     Pending<D, F16> pending[2];
     pending[1].clear();
     const auto finish = [&] {
+      // (nothing of it belongs ahead of the branch, where multiply's own would follow it)
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) asm volatile("" : "+v"(pending[1].s[h]));
 #pragma unroll
       for (int i = 0; i < 16; ++i) pending[1].form(w, i, p.c2);
     };
