@@ -403,8 +403,8 @@ mqa_status paged_attention(mqa_dtype dt, const void* q, mqa_float q_type, int64_
  *            [0, clamp(ctx_b - n + t + 1, 0, min(ctx_b, max_context_len)))
  *   dt, pools, context_lens, block_table, scale, out [tokens, Hq, D], lse
  *            [tokens, Hq]: as paged_attention, but n keys times the largest |v|
- *            must stay below 2^112.  Where they multiply V, weights are rounded
- *            to fp16 (2^-12 of themselves, or 2^-37 of the row's largest); from a
+ *            must stay below 2^111.  Where they multiply V, weights are rounded
+ *            to fp16 (2^-12 of themselves, or 2^-33 of the row's largest); from a
  *            scale of V outside 2^-22 .. 2^9 on (or one of K, for fp16 queries),
  *            which takes longer, to 2^-16.  out is divided by the sum of the
  *            rounded ones, lse is from the others

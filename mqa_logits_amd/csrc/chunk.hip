@@ -32,11 +32,12 @@ constexpr uint32_t kLastScale = 252;         // bytes above could overflow fp32:
 // own end costs, see kRoom.
 constexpr uint32_t kHalfLow = 105, kHalfHigh = 136;
 // The running maximum is set kRoom octaves below the largest score, and follows a
-// new one only when that leaves a weight above 2^kMost (fp16 ends at 65504); most
-// steps rescale nothing.  The largest weight is then between 2^kRoom and 2^kMost,
-// and half a step of fp16's least subnormal is 2^-37 of it at most.  The
-// unnormalised sums of n keys stay within n * 2^15 times the largest value.
-constexpr float kRoom = 12.f, kMost = 15.f;
+// new one when a lane's weights of a step come to more than kMost (so that none is
+// beyond fp16): most steps rescale nothing, and no step looks for its largest score.
+// The row's largest weight is then 2^kRoom at least, and half a step of fp16's least
+// subnormal is 2^-33 of it at most.  The unnormalised sums of n keys stay within
+// n * 2^16 times the largest value.
+constexpr float kRoom = 8.f, kMost = 65000.f;
 constexpr float kLowest = -0x1.fffffep127f;  // a maximum before any key (finite: no inf - inf)
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -252,369 +253,523 @@ template <int D>
 struct Stage {
   static constexpr int kKeyPitch = D * 2 + 16;       // bytes; free of bank conflicts
   static constexpr int kValPitch = kKeys * 2 + 16;
-  static constexpr int kBytes = kKeys * kKeyPitch + D * kValPitch;
+  static constexpr int kKeyBytes = kKeys * kKeyPitch, kValBytes = D * kValPitch;
+  // K's products are a step ahead of V's, and start before other waves' last use
+  // of the step before: three buffers of K, two of V.
+  char k[3][kKeyBytes];
+  char v[2][kValBytes];
+  int flags[4][2];         // [step][V, K]: the step, if it has unusual scales
+  uint8_t nan_marks[2][kKeys][4];
 };
+
+// Global memory, and a wave-uniform address kept in scalar registers, so that
+// the lanes' loads from it take a 32-bit offset each instead of a 64-bit sum.
+typedef const __attribute__((address_space(1))) uint8_t* Bytes;
+template <class T>
+__device__ __forceinline__ T load_from(Bytes p) {
+  return *reinterpret_cast<const __attribute__((address_space(1))) T*>(p);
+}
+__device__ __forceinline__ Bytes scalar(Bytes p) {
+  asm("" : "+s"(p));
+  return p;
+}
+
+__device__ __forceinline__ uint32_t lanes(uint32_t offset) {
+  asm("" : "+v"(offset));
+  return offset;
+}
 
 // What a thread loads of a step.  The first half of the workgroup takes D/8 bytes
 // of codes of a key each and their scale; the second D/32 bytes of V's codes of four
-// keys and their scales.
+// keys and their scales.  A wave's keys are 16 in a row.
 struct Raw {
   u32x4 codes;
   uint32_t scales[4];
 };
 
-template <int D>
-struct Loader {
-  const ChunkParams& p;
-  const uint32_t* places;  // first block (of 32 elements) of every 16th key
-  uint32_t key_blocks;     // blocks from one key of the pool to the next
+// The second half's keys and columns: 16 lanes in a row write all banks.
+__device__ __forceinline__ int value_quad(int tid) { return (tid & 3) | (tid >> 6 & 3) << 2; }
+__device__ __forceinline__ int value_column(int tid) { return tid >> 2 & 15; }
 
-  // key0: the step's first key, from the stage's; n: keys of the context from there on
-  template <bool KEYS>
-  __device__ __forceinline__ void load(Raw& r, int tid, int key0, int n) const {
+template <int D, bool KEYS>
+struct Loader {
+  Bytes codes, scales;     // of the KV head
+  uint32_t code_at, scale_at;      // the lane's offsets from its 16 keys' first block
+  uint32_t key_blocks;             // blocks (of 32 elements) from one key of the pool to the next
+
+  __device__ __forceinline__ Loader(const ChunkParams& p, int tid, int kv_head)
+      : codes((Bytes)(KEYS ? p.k : p.v) + kv_head * (D / 2)), scales((Bytes)(KEYS ? p.k_sf : p.v_sf) + kv_head * (D / 32)),
+        key_blocks(p.kv_heads * (D / 32)) {
+    const uint32_t key = KEYS ? tid >> 2 & 15 : (tid & 3) * 4, c = KEYS ? tid & 3 : value_column(tid);
+    code_at = key * key_blocks * 16 + c * (KEYS ? D / 8 : D / 32);
+    scale_at = key * key_blocks + c * (KEYS ? D / 4 : D / 16) / 32;
+  }
+  // first: block of the wave's 16 keys (wave-uniform)
+  __device__ __forceinline__ void load(Raw& r, uint32_t first) const {
+    const Bytes from = scalar(codes + ((uint64_t)first << 4)), sf = scalar(scales + first);
     if constexpr (KEYS) {
-      const int j = tid >> 2, c = tid & 3;
-      const uint32_t block = places[(key0 + j) >> 4] + (j & 15) * key_blocks;
-      const uint8_t* src = p.k + ((uint64_t)block << 4) + c * (D / 8);
       if constexpr (D == 128) {
-        r.codes = *reinterpret_cast<const u32x4*>(src);
+        r.codes = load_from<u32x4>(from + lanes(code_at));
       } else {
-        const u32x2 x = *reinterpret_cast<const u32x2*>(src);
+        const u32x2 x = load_from<u32x2>(from + lanes(code_at));
         r.codes = u32x4{x[0], x[1], 0u, 0u};
       }
-      const uint32_t s = p.k_sf[(uint64_t)block + c * (D / 4) / 32];
-      r.scales[0] = j < n ? s : 127u;        // (any finite one where nothing is stored)
+      r.scales[0] = load_from<uint8_t>(sf + lanes(scale_at));
     } else {
-      const int j = Values::key(tid), c = Values::column(tid);
-      const uint32_t first = places[(key0 + j) >> 4] + (j & 15) * key_blocks;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t block = first + i * key_blocks;
-        const uint8_t* src = p.v + ((uint64_t)block << 4) + c * (D / 32);
-        r.codes[i] = D == 128 ? *reinterpret_cast<const uint32_t*>(src) : *reinterpret_cast<const uint16_t*>(src);
-        const uint32_t s = p.v_sf[(uint64_t)block + c * (D / 16) / 32];
-        r.scales[i] = j + i < n ? s : 127u;
+        const Bytes at = scalar(from + i * key_blocks * 16);
+        r.codes[i] = D == 128 ? load_from<uint32_t>(at + lanes(code_at)) : load_from<uint16_t>(at + lanes(code_at));
+        r.scales[i] = load_from<uint8_t>(scalar(sf + i * key_blocks) + lanes(scale_at));
       }
     }
   }
-
-  // The second half's keys and columns: 16 lanes in a row write all banks.
-  struct Values {
-    __device__ __forceinline__ static int quad(int tid) { return (tid & 3) | (tid >> 6 & 3) << 2; }
-    __device__ __forceinline__ static int key(int tid) { return quad(tid) * 4; }
-    __device__ __forceinline__ static int column(int tid) { return tid >> 2 & 15; }
-  };
 };
 
-// K as rows of D (KEYS), or V transposed, into a step's LDS.
-template <int D, bool KEYS, bool HALF>
-__device__ __forceinline__ void put(const Raw& r, int tid, char* lds) {
+// Where nothing is stored, behind the n keys of the context from the step's first
+// on, the scales may be anything: they are read as finite.
+template <bool KEYS>
+__device__ __forceinline__ void check_context(Raw& r, int tid, int n) {
   if constexpr (KEYS) {
-    const int c = tid & 3;
-    char* dst = lds + (tid >> 2) * Stage<D>::kKeyPitch + c * (D / 2);
-    const float s = scale_of(r.scales[0]);
-    if constexpr (D == 128) {
-      // half of the lanes the other way round: 8 in a row write all banks
-      const int turn = c & 2;
-      const u32x4 x = turn ? u32x4{r.codes[2], r.codes[3], r.codes[0], r.codes[1]} : r.codes;
-      char* one = dst + turn * 16;
-      char* two = dst + (turn ^ 2) * 16;
+    r.scales[0] = (tid >> 2) < n ? r.scales[0] : 127u;
+  } else {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(one + i * 16) = cvt_eight<HALF>(x[i], s);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(two + i * 16) = cvt_eight<HALF>(x[i + 2], s);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(dst + i * 16) = cvt_eight<HALF>(r.codes[i], s);
-    }
+    for (int i = 0; i < 4; ++i) r.scales[i] = value_quad(tid) * 4 + i < n ? r.scales[i] : 127u;
+  }
+}
+
+// K as rows of D (KEYS), or V transposed, into its LDS: part SEL of D/32.
+template <int D, bool KEYS, bool HALF, int SEL>
+__device__ __forceinline__ void put_part(const Raw& r, int tid, char* lds) {
+  if constexpr (KEYS) {
+    // (half of the lanes the other way round: 8 in a row write all banks)
+    const int c = tid & 3, turn = D == 128 ? c & 2 : 0;
+    char* dst = lds + (tid >> 2) * Stage<D>::kKeyPitch + c * (D / 2) + (SEL ^ turn) * 16;
+    uint32_t word = r.codes[SEL];
+    if constexpr (D == 128) word = turn ? r.codes[SEL ^ 2] : word;
+    *reinterpret_cast<u32x4*>(dst) = cvt_eight<HALF>(word, scale_of(r.scales[0]));
   } else {
     // element e of the thread's D/16 is row e % (D/32) * 32 + 2 c + e / (D/32); four
     // keys are one half of what a lane multiplies of 16
-    const int quad = Loader<D>::Values::quad(tid), c = Loader<D>::Values::column(tid);
-    char* dst = lds + kKeys * Stage<D>::kKeyPitch + 2 * c * Stage<D>::kValPitch + (quad >> 2) * 32 +
+    constexpr int kCols = D / 32;
+    const int quad = value_quad(tid), c = value_column(tid);
+    char* dst = lds + 2 * c * Stage<D>::kValPitch + (quad >> 2) * 32 +
                 (quad & 1) * 16 + (quad >> 1 & 1) * 8;
-    float s[4];
+    uint32_t x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] = scale_of(r.scales[i]);
-    const auto two = [&](auto sel) {
-      constexpr int SEL = decltype(sel)::value;
-      uint32_t x[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = cvt_pair<HALF, SEL>(r.codes[i], s[i]);
-#pragma unroll
-      for (int odd = 0; odd < 2; ++odd) {
-        constexpr int kCols = D / 32;
-        const int e = 2 * SEL + odd, at = e % kCols * 32 + e / kCols;
-        const uint32_t pick = odd ? 0x07060302u : 0x05040100u;
-        *reinterpret_cast<u32x2*>(dst + at * Stage<D>::kValPitch) =
-            u32x2{__builtin_amdgcn_perm(x[1], x[0], pick), __builtin_amdgcn_perm(x[3], x[2], pick)};
-      }
-    };
-    two(std::integral_constant<int, 0>{});
-    two(std::integral_constant<int, 1>{});
-    if constexpr (D == 128) {
-      two(std::integral_constant<int, 2>{});
-      two(std::integral_constant<int, 3>{});
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t word = r.codes[i];
+      x[i] = cvt_pair<HALF, SEL>(word, scale_of(r.scales[i]));
     }
+#pragma unroll
+    for (int odd = 0; odd < 2; ++odd) {
+      const int e = 2 * SEL + odd, at = e % kCols * 32 + e / kCols;
+      const uint32_t pick = odd ? 0x07060302u : 0x05040100u;
+      *reinterpret_cast<u32x2*>(dst + at * Stage<D>::kValPitch) =
+          u32x2{__builtin_amdgcn_perm(x[1], x[0], pick), __builtin_amdgcn_perm(x[3], x[2], pick)};
+    }
+  }
+}
+
+template <int D, bool KEYS, bool HALF>
+__device__ __forceinline__ void put(const Raw& r, int tid, char* lds) {
+  put_part<D, KEYS, HALF, 0>(r, tid, lds);
+  put_part<D, KEYS, HALF, 1>(r, tid, lds);
+  if constexpr (D == 128) {
+    put_part<D, KEYS, HALF, 2>(r, tid, lds);
+    put_part<D, KEYS, HALF, 3>(r, tid, lds);
   }
 }
 
 // Some scale is outside what the fp16 (or, for bf16 queries, K's bf16) products take.
 template <bool KEYS, bool F16>
 __device__ __forceinline__ bool wide_scales(const Raw& r) {
-  const auto wide = [](uint32_t s) { return s - kHalfLow > kHalfHigh - kHalfLow; };
-  if constexpr (KEYS) return F16 ? wide(r.scales[0]) : r.scales[0] > kLastScale;
-  return wide(r.scales[0]) || wide(r.scales[1]) || wide(r.scales[2]) || wide(r.scales[3]);
+  static_assert(kHalfHigh - kHalfLow == 31, "32 scales: the offsets' bits can be joined");
+  const auto off = [&](int i) { return r.scales[i] - kHalfLow; };
+  if constexpr (KEYS) return F16 ? off(0) > 31 : r.scales[0] > kLastScale;
+  return (off(0) | off(1) | off(2) | off(3)) > 31;
 }
 
 // ---------------------------------------------------------------------------
-// A wave's 32 * QT rows
+// A wave's 32 rows
 // ---------------------------------------------------------------------------
 
-template <int D, int QT, bool F16>
+template <int D, bool F16>
 struct Rows {
   static constexpr int kSteps = D / 16, kCols = D / 32;
-  u32x4 q[QT][kSteps];     // row l % 32, elements 16 st + 8 (l / 32) ..
-  f32x16 o[QT][kCols];     // row l % 32; element kCols * m + col, m = i % 4 + 8 (i / 4) + 4 (l / 32)
-  float m[QT], l[QT];      // running maximum (log2), the lane's part of the sum of weights
-  float r[QT];             // and of the sum of the rounded ones
-  int seen[QT];
-  uint32_t nan_blocks[QT];
+  static constexpr int kKeyOps = kSteps, kValOps = 2 * kCols;   // products of 32 keys
+  static constexpr int kAhead = 4;           // operands are read that many products before their use
+  u32x4 q[kSteps];         // row l % 32, elements 16 st + 8 (l / 32) ..
+  f32x16 o[kCols];         // row l % 32; element kCols * m + col, m = i % 4 + 8 (i / 4) + 4 (l / 32)
+  float m, l;              // running maximum (log2), the lane's part of the sum of weights
+  float r;                 // and of the sum of the rounded ones
+  int seen;
+  uint32_t nan_blocks;
 
   __device__ __forceinline__ void clear() {
+    m = kLowest;
+    l = r = 0.f;
+    nan_blocks = 0;
 #pragma unroll
-    for (int t = 0; t < QT; ++t) {
-      m[t] = kLowest;
-      l[t] = r[t] = 0.f;
-      nan_blocks[t] = 0;
+    for (int c = 0; c < kCols; ++c)
 #pragma unroll
-      for (int c = 0; c < kCols; ++c)
+      for (int i = 0; i < 16; ++i) o[c][i] = 0.f;
+  }
+
+  // Operands of half a step: 32 keys' rows of K, V's columns of them.
+  __device__ __forceinline__ static u32x4 key_operand(const char* k, int lane, int n) {
+    return *reinterpret_cast<const u32x4*>(k + (lane & 31) * Stage<D>::kKeyPitch + (lane >> 5) * 16 + n * 32);
+  }
+  __device__ __forceinline__ static u32x4 value_operand(const char* v, int lane, int n) {
+    return *reinterpret_cast<const u32x4*>(v + (n % kCols * 32 + (lane & 31)) * Stage<D>::kValPitch + (lane >> 5) * 16 + n / kCols * 32);
+  }
+  // A product must not overlap its operands.  The compiler was seen to let one with
+  // a constant 0 to add to overlap them: they are used once more behind it.
+  __device__ __forceinline__ static void keep(u32x4 a, u32x4 b) { asm volatile("" ::"v"(a), "v"(b)); }
+
+  // The scores of 32 keys: key i % 4 + 8 (i / 4) + 4 (l / 32) of row l % 32.
+  __device__ __forceinline__ void multiply(f32x16& x, const char* k, int lane) const {
+    u32x4 a[kAhead];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[t][c][i] = 0.f;
+    for (int n = 0; n < kAhead; ++n) a[n] = key_operand(k, lane, n);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = 0.f;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < kKeyOps; ++n) {
+      x = mma<F16>(a[n % kAhead], q[n], x);
+      __builtin_amdgcn_sched_barrier(0);
+      if (n == 0) keep(a[0], q[0]);
+      if (n + kAhead < kKeyOps) a[n % kAhead] = key_operand(k, lane, n + kAhead);
+    }
+    // The compiler was seen to read a product's result right behind a branch,
+    // before it is there; the products end here.
+    asm volatile("s_nop 7\n\ts_nop 7" : "+v"(x));
+  }
+
+  // Keys that a row does not see leave its scores.
+  __device__ __forceinline__ void mask(f32x16& x, int lane, int key0) const {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int key = key0 + (i & 3) + 8 * (i >> 2) + 4 * (lane >> 5);
+      x[i] = key < seen ? x[i] : -__builtin_inff();
     }
   }
 
-  // One step.  WIDE: some scale is outside fp16's range; LDS holds bf16.
-  template <bool MASKED>
-  __device__ __forceinline__ void step(const char* lds, int key0, float c2) {
-    part<false, MASKED, 2>(lds, 0, key0, c2);
-  }
-  __device__ __forceinline__ void wide_step(const char* lds, int key0, float c2) {
-#pragma nounroll
-    for (int h = 0; h < 2; ++h) part<true, true, 1>(lds, h, key0, c2);
+  // The running maximum of rows with `over` in a lane follows their largest score
+  // (others keep theirs: a row's result does not depend on its neighbours).
+  __device__ __forceinline__ void settle(float best, bool over, float c2) {
+    best = fmaxf(best, __shfl_xor(best, 32)) * c2;
+    over |= (bool)__shfl_xor((int)over, 32);
+    const float next = over ? fmaxf(m, best - kRoom) : m;
+    const float f = __builtin_amdgcn_exp2f(m - next);
+    m = next;
+    l *= f;
+    r *= f;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[c][i] *= f;
   }
 
-  // H halves of 32 keys of it.
-  template <bool WIDE, bool MASKED, int H>
-  __device__ __forceinline__ void part(const char* lds, int first, int key0, float c2) {
-    const int lane = WIDE || MASKED ? here_only(threadIdx.x & 63) : threadIdx.x & 63, half = lane >> 5;
-    const char* keys = lds + (first * 32 + (lane & 31)) * Stage<D>::kKeyPitch + half * 16;
-    const char* vals = lds + kKeys * Stage<D>::kKeyPitch + (lane & 31) * Stage<D>::kValPitch + half * 16 + first * 64;
-    f32x16 s[QT][H];
+  // Rounded weights of 32 keys, two in a word, with what the lane's come to.
+  struct Weights {
+    u32x4 w[2];
+    float sum, rounded;
+    __device__ __forceinline__ void clear() { sum = rounded = 0.f; }
+    __device__ __forceinline__ void add(int pair, float x, float y) {
+      const uint32_t word = pack_f16(x, y);
+      w[pair / 4][pair % 4] = word;
+      sum += x;
+      sum += y;
+      rounded = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, word), f16x2{(_Float16)1.f, (_Float16)1.f}, rounded, false);
+    }
+  };
+  __device__ __forceinline__ void form(const f32x16& x, Weights& w, float c2) const {
+    w.clear();
 #pragma unroll
-    for (int t = 0; t < QT; ++t)
+    for (int i = 0; i < 8; ++i)
+      w.add(i, __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * i], c2, -m)), __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * i + 1], c2, -m)));
+  }
+  // Weights that are too large are formed anew.
+  __device__ __forceinline__ void check(f32x16& x, Weights& w, float c2) {
+    if (__builtin_expect(__any(w.sum > kMost), 0)) {
+      asm volatile("" : "+v"(x));            // (rare: nothing of it belongs before the branch)
+      float best = x[0];
 #pragma unroll
-      for (int h = 0; h < H; ++h)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[t][h][i] = 0.f;
-    // A product must not overlap its operands.  The compiler was seen to let one
-    // with a constant 0 to add to overlap them: the operands are used once more
-    // behind it, or (here) the zeros are registers.
-    if (WIDE) asm volatile("" : "+v"(s[0][0]));
-    // operands are read kAhead products before their use
-    constexpr int kAhead = 4;
-    const auto key_operand = [&](int n) {
-      return *reinterpret_cast<const u32x4*>(keys + n % H * 32 * Stage<D>::kKeyPitch + n / H * 32);
-    };
+      for (int i = 1; i < 16; ++i) best = fmaxf(best, x[i]);
+      settle(best, w.sum > kMost, c2);
+      form(x, w, c2);
+    }
+    l += w.sum;
+    r += w.rounded;
+  }
+
+  // The weights of 32 keys, and their V.
+  __device__ __forceinline__ void finish(f32x16& x, const char* v, int lane, float c2) {
+    Weights w;
+    form(x, w, c2);
+    check(x, w, c2);
     u32x4 a[kAhead];
 #pragma unroll
-    for (int n = 0; n < kAhead; ++n) a[n] = key_operand(n);
+    for (int n = 0; n < kAhead; ++n) a[n] = value_operand(v, lane, n);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int n = 0; n < H * kSteps; ++n) {
-      const int st = n / H, h = n % H;
+    for (int n = 0; n < kValOps; ++n) {
+      o[n % kCols] = mma<true>(a[n % kAhead], w.w[n / kCols], o[n % kCols]);
+      if (n + kAhead < kValOps) a[n % kAhead] = value_operand(v, lane, n + kAhead);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+
+  // The same for scores x, with the products of the next 32 keys between the
+  // weights, and other work (0 .. kValOps - 1) between V's: the matrix cores and the
+  // vector ALU work side by side.
+  template <class Work>
+  __device__ __forceinline__ void finish_and_multiply(f32x16& x, f32x16& next, const char* v, const char* k, int lane, float c2,
+                                                      const Work& work) {
+    u32x4 a[kAhead];
+    Weights w;
+    w.clear();
 #pragma unroll
-      for (int t = 0; t < QT; ++t) {
-        if constexpr (WIDE && F16) {
-          // the query's two exact bf16 parts; an infinity stays in the first alone
+    for (int n = 0; n < kAhead; ++n) a[n] = key_operand(k, lane, n);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) next[i] = 0.f;
+    __builtin_amdgcn_sched_barrier(0);
+    // A pair of weights is scaled and shifted beside one product, its exponentials
+    // are taken beside the next, and it is rounded beside the one after that.
+    constexpr int kEach = 8 / kKeyOps;       // pairs beside a product
+    float f[kEach][2], e[kEach][2];
+#pragma unroll
+    for (int n = 0; n < kKeyOps + 2; ++n) {
+      if (n < kKeyOps) {
+        next = mma<F16>(a[n % kAhead], q[n], next);
+        __builtin_amdgcn_sched_barrier(0);
+        if (n == 0) keep(a[0], q[0]);
+        if (n + kAhead < kKeyOps)
+          a[n % kAhead] = key_operand(k, lane, n + kAhead);
+        else
+          a[n % kAhead] = value_operand(v, lane, n + kAhead - kKeyOps);
+      }
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        if (n >= 2) w.add((n - 2) * kEach + j, e[j][0], e[j][1]);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          if (n >= 1 && n <= kKeyOps) e[j][y] = __builtin_amdgcn_exp2f(f[j][y]);
+          if (n < kKeyOps) f[j][y] = __builtin_fmaf(x[2 * (n * kEach + j) + y], c2, -m);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    static_assert(kKeyOps % kAhead == 0, "V's operands follow K's in turn");
+    check(x, w, c2);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < kValOps; ++n) {
+      o[n % kCols] = mma<true>(a[n % kAhead], w.w[n / kCols], o[n % kCols]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (n + kAhead < kValOps) a[n % kAhead] = value_operand(v, lane, n + kAhead);
+      work(n);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+
+  // A step with unusual scales: LDS holds bf16, weights are split into two parts,
+  // and fp16 queries as well.
+  __device__ __forceinline__ void wide_step(const char* k, const char* v, int key0, float c2) {
+#pragma nounroll
+    for (int half_step = 0; half_step < 2; ++half_step) {
+      const int lane = here_only(threadIdx.x & 63);
+      f32x16 s;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] = 0.f;
+      asm volatile("" : "+v"(s));            // (zeros in registers: see keep)
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st) {
+        const u32x4 a = key_operand(k + half_step * 32 * Stage<D>::kKeyPitch, lane, st);
+        if constexpr (F16) {
+          // two exact parts; an infinity stays in the first alone
           u32x4 hi, lo;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const f16x2 x = __builtin_bit_cast(f16x2, here_only(q[t][st][i]));
+            const f16x2 x = __builtin_bit_cast(f16x2, here_only(q[st][i]));
             const float y = (float)x[0], z = (float)x[1];
             hi[i] = pack_bf16(y, z);
             const float ry = y - bf16_lo(hi[i]), rz = z - bf16_hi(hi[i]);
             lo[i] = pack_bf16(__builtin_isfinite(y) ? ry : 0.f, __builtin_isfinite(z) ? rz : 0.f);
           }
-          s[t][h] = mma<false>(a[n % kAhead], hi, s[t][h]);
-          s[t][h] = mma<false>(a[n % kAhead], lo, s[t][h]);
+          s = mma<false>(a, hi, s);
+          s = mma<false>(a, lo, s);
         } else {
-          s[t][h] = mma<F16>(a[n % kAhead], q[t][st], s[t][h]);
+          s = mma<false>(a, q[st], s);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
-      if (n < H) asm volatile("" ::"v"(a[n % kAhead]));   // still its own behind the product
-      if (n + kAhead < H * kSteps) a[n % kAhead] = key_operand(n + kAhead);
-    }
-    const auto value_operand = [&](int n) {
-      return *reinterpret_cast<const u32x4*>(vals + n % kCols * 32 * Stage<D>::kValPitch + n / kCols * 32);
-    };
+      asm volatile("s_nop 7\n\ts_nop 7" : "+v"(s));
+      float best = -__builtin_inff();
 #pragma unroll
-    for (int n = 0; n < kAhead; ++n) a[n] = value_operand(n);
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (MASKED) {
-#pragma unroll
-      for (int t = 0; t < QT; ++t)
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int key = key0 + (first + h) * 32 + (i & 3) + 8 * (i >> 2) + 4 * half;
-            s[t][h][i] = key < seen[t] ? s[t][h][i] : -__builtin_inff();
-          }
-    }
-    u32x4 w[QT][WIDE ? 2 : 1][2 * H];        // [high and low part][16 keys]
-#pragma unroll
-    for (int t = 0; t < QT; ++t) weights<WIDE, H>(s[t], t, c2, w[t]);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int n = 0; n < 2 * H * kCols; ++n) {
-      const int k = n / kCols, c = n % kCols;
-#pragma unroll
-      for (int t = 0; t < QT; ++t)
-#pragma unroll
-        for (int x = 0; x < (WIDE ? 2 : 1); ++x) o[t][c] = mma<!WIDE>(a[n % kAhead], w[t][x][k], o[t][c]);
-      if (n + kAhead < 2 * H * kCols) a[n % kAhead] = value_operand(n + kAhead);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
-
-  // Weights relative to the running maximum m.
-  template <bool WIDE, int H>
-  __device__ __forceinline__ void weights(const f32x16 (&s)[H], int t, float c2, u32x4 (&w)[WIDE ? 2 : 1][2 * H]) {
-    float best = s[0][0];
-#pragma unroll
-    for (int i = 1; i < 16 * H; ++i) best = fmaxf(best, s[i >> 4][i & 15]);
-    if (__builtin_expect(__any(__builtin_fmaf(best, c2, -m[t]) > kMost), 0)) {
-      asm volatile("");                      // rare: nothing of it belongs before the branch
-      best = fmaxf(best, __shfl_xor(best, 32)) * c2;
-      const float next = fmaxf(m[t], best - kRoom);
-      const float f = __builtin_amdgcn_exp2f(m[t] - next);
-      m[t] = next;
-      l[t] *= f;
-      r[t] *= f;
-#pragma unroll
-      for (int c = 0; c < kCols; ++c)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[t][c][i] *= f;
-    }
-    float x[16 * H];
-#pragma unroll
-    for (int i = 0; i < 16 * H; ++i) x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 4][i & 15], c2, -m[t]));
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16 * H; i += 4) sum += (x[i] + x[i + 1]) + (x[i + 2] + x[i + 3]);
-    l[t] += sum;
-    if (WIDE) r[t] += sum;
-#pragma unroll
-    for (int k = 0; k < 2 * H; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = x[8 * k + 2 * i], b = x[8 * k + 2 * i + 1];
-        const uint32_t hi = pack<!WIDE>(a, b);
-        w[0][k][i] = hi;
-        if constexpr (WIDE)
-          w[1][k][i] = pack_bf16(a - bf16_lo(hi), b - bf16_hi(hi));
-        else
-          r[t] = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, hi), f16x2{(_Float16)1.f, (_Float16)1.f}, r[t], false);
+      for (int i = 0; i < 16; ++i) {
+        const int key = key0 + half_step * 32 + (i & 3) + 8 * (i >> 2) + 4 * (lane >> 5);
+        s[i] = key < seen ? s[i] : -__builtin_inff();
+        best = fmaxf(best, s[i]);
       }
+      const bool over = __builtin_fmaf(best, c2, -m) > kRoom;
+      if (__any(over)) settle(best, over, c2);
+      u32x4 w[2][2];                         // [16 keys][part]
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * i], c2, -m));
+        const float z = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * i + 1], c2, -m));
+        const uint32_t hi = pack_bf16(y, z);
+        w[i / 4][0][i % 4] = hi;
+        w[i / 4][1][i % 4] = pack_bf16(y - bf16_lo(hi), z - bf16_hi(hi));
+        l += y + z;
+        r += y + z;
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          const u32x4 a = value_operand(v + half_step * 64, lane, n * kCols + c);
+#pragma unroll
+          for (int part = 0; part < 2; ++part) o[c] = mma<false>(a, w[n][part], o[c]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+    }
   }
 };
 
-// The steps of a stage, for a wave of the half that loads K (KEYS) or V.
-template <bool KEYS, int D, int QT, bool F16, class InContext>
-__device__ __forceinline__ void walk(const Loader<D>& loader, Rows<D, QT, F16>& rows,
-                                     char (&stage)[2][Stage<D>::kBytes], int* flags, uint8_t (&nan_marks)[2][kKeys][4],
-                                     int stage0, int steps, int least, const InContext& in_context, float c2) {
+// The steps of a stretch, for a wave of the half that loads K (KEYS) or V.  While 32
+// keys' weights are formed and multiplied with V, the next ones' scores are
+// computed; K is put into LDS two steps ahead, V one.
+template <bool KEYS, int D, bool F16>
+__device__ __forceinline__ void walk(const ChunkParams& p, Rows<D, F16>& rows, Stage<D>& stage, const uint32_t* places,
+                                     int kv_head, int stage0, int steps, int least, int keys_left) {
+  constexpr int kHalfKeys = 32 * Stage<D>::kKeyPitch, kHalfVals = 64;   // bytes to a step's second half
   const int tid = threadIdx.x & (kThreads / 2 - 1);
+  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   constexpr bool kHalf = KEYS ? F16 : true;
+  constexpr int kLead = KEYS ? 2 : 1;        // steps that this half is ahead
+  const float c2 = p.c2;
+  const Loader<D, KEYS> loader(p, tid, kv_head);
   Raw raw;
+  // first blocks of the wave's keys, of 64 steps from `held` on, one in each lane
+  uint32_t held_places = 0;
+  int held = -64;
+  const auto fetch = [&](int i) {
+    i = min(i, steps - 1);                   // (past the last step, the last again)
+    if (i >= held + 64) {
+      held = i & ~63;
+      held_places = places[min(held + lane, steps - 1) * 4 + wave];
+    }
+    loader.load(raw, __builtin_amdgcn_readlane(held_places, i & 63));
+  };
+  const auto keys = [&](int i) { return stage.k[i % 3]; };
+  const auto values = [&](int i) { return stage.v[i & 1]; };
+  const auto target = [&](int i) { return KEYS ? keys(i) : values(i); };
+  const auto mark_wide = [&](int i) {
+    if (__builtin_expect(__any(wide_scales<KEYS, F16>(raw)), 0)) stage.flags[i & 3][KEYS] = i;
+  };
   const auto store = [&](int i) {
     const int me = here_only(tid);
-    if (wide_scales<KEYS, F16>(raw)) flags[i & 1] = i;
-    put<D, KEYS, kHalf>(raw, me, stage[i & 1]);
+    if (keys_left - i * kKeys < kKeys) check_context<KEYS>(raw, me, keys_left - i * kKeys);
+    mark_wide(i);
+    put<D, KEYS, kHalf>(raw, me, target(i));
   };
-  const auto fetch = [&](int i) { loader.template load<KEYS>(raw, here_only(tid), i * kKeys, in_context(i)); };
+  const auto narrow = [&](int i) {
+    return __builtin_amdgcn_readfirstlane(stage.flags[i & 3][0]) != i && __builtin_amdgcn_readfirstlane(stage.flags[i & 3][1]) != i;
+  };
+
   fetch(0);
   store(0);
-  fetch(min(1, steps - 1));
+  fetch(1);
+  if constexpr (KEYS) {
+    store(1);                                // (a step that is not there: never used)
+    fetch(2);
+  }
   __syncthreads();
-  // Steps whose keys all rows see, then those at the rows' own ends.  (Past the
-  // last step, the last again is stored and never used.)
-  const int clear = min(max(least - stage0, 0) / kKeys, steps);
+  f32x16 x, y;                               // scores of a step's halves
+  rows.multiply(x, keys(0), lane);
+  rows.mask(x, here_only(lane), stage0);
+  // While all rows see this step and the next, and what is stored is whole.
+  const int clear = min(min(max(least - stage0, 0) / kKeys, steps) - 1, keys_left / kKeys - kLead);
   int i = 0;
-  const auto narrow = [&] { return __builtin_amdgcn_readfirstlane(flags[i & 1]) != i; };
-  const auto turn = [&] {
-    store(i + 1);
-    fetch(min(i + 2, steps - 1));
-    ++i;
-    __syncthreads();
-  };
 #pragma nounroll
-  while (i < clear && narrow()) {
-    rows.template step<false>(stage[i & 1], 0, c2);
-    turn();
+  for (; i < clear && narrow(i); ++i) {
+    char* const into = target(i + kLead);
+    rows.finish_and_multiply(x, y, values(i), keys(i) + kHalfKeys, lane, c2, [&](int n) {
+      const int me = here_only(tid);
+      if (n == 1) put_part<D, KEYS, kHalf, 0>(raw, me, into);
+      if constexpr (D == 128)
+        if (n == 5) put_part<D, KEYS, kHalf, 1>(raw, me, into);
+    });
+    rows.finish_and_multiply(y, x, values(i) + kHalfVals, keys(i + 1), lane, c2, [&](int n) {
+      const int me = here_only(tid);
+      if (n == 1) put_part<D, KEYS, kHalf, D / 64>(raw, me, into);
+      if constexpr (D == 128)
+        if (n == 5) put_part<D, KEYS, kHalf, 3>(raw, me, into);
+    });
+    mark_wide(i + kLead);
+    fetch(i + kLead + 1);
+    __syncthreads();
   }
 #pragma nounroll
-  while (i < steps && narrow()) {
-    rows.template step<true>(stage[i & 1], stage0 + i * kKeys, c2);
-    turn();
+  for (; i < steps && narrow(i); ++i) {
+    const int me = here_only(lane), key0 = stage0 + i * kKeys;
+    rows.multiply(y, keys(i) + kHalfKeys, me);
+    rows.mask(y, me, key0 + 32);
+    rows.finish(x, values(i), me, c2);
+    if (i + 1 < steps) {
+      rows.multiply(x, keys(i + 1), me);
+      rows.mask(x, me, key0 + kKeys);
+    }
+    rows.finish(y, values(i) + kHalfVals, me, c2);
+    store(i + kLead);
+    fetch(i + kLead + 1);
+    __syncthreads();
   }
   if (__builtin_expect(i == steps, 1)) return;
   // from a step with unusual scales on, in bf16, NaN scales apart
-  loader.template load<KEYS>(raw, here_only(tid), i * kKeys, in_context(i));
+  fetch(i);
 #pragma nounroll
   for (; i < steps; ++i) {
     const int me = here_only(tid);
+    check_context<KEYS>(raw, me, keys_left - i * kKeys);
     if constexpr (KEYS) {
       if (raw.scales[0] > kLastScale) raw.scales[0] = 255;
     } else {
-      const int c = Loader<D>::Values::column(me), b = c * (D / 16) / 32;
+      const int c = value_column(me), b = c * (D / 16) / 32;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const bool bad = raw.scales[j] > kLastScale;
-        if (c % (512 / D) == 0) nan_marks[i & 1][Loader<D>::Values::key(me) + j][b] = bad;
+        if (c % (512 / D) == 0) stage.nan_marks[i & 1][value_quad(me) * 4 + j][b] = bad;
         raw.scales[j] = bad ? 0u : raw.scales[j];
       }
     }
     __syncthreads();                         // the stage's last use is over
-    put<D, KEYS, false>(raw, me, stage[i & 1]);
+    put<D, KEYS, false>(raw, me, target(i));
     __syncthreads();
-    loader.template load<KEYS>(raw, here_only(tid), min(i + 1, steps - 1) * kKeys, in_context(min(i + 1, steps - 1)));
+    fetch(i + 1);
     const int key0 = stage0 + i * kKeys;
     uint32_t marks = 0;
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b) marks |= (uint32_t)nan_marks[i & 1][me & 63][b] << b;
+    for (int b = 0; b < D / 32; ++b) marks |= (uint32_t)stage.nan_marks[i & 1][me & 63][b] << b;
     if (__builtin_expect(__any(marks != 0), 0))
 #pragma nounroll
       for (int j = 0; j < kKeys; ++j) {
         const uint32_t word = __shfl(marks, j);
-#pragma unroll
-        for (int t = 0; t < QT; ++t)
-          if (key0 + j < rows.seen[t]) rows.nan_blocks[t] |= word;
+        if (key0 + j < rows.seen) rows.nan_blocks |= word;
       }
-    rows.wide_step(stage[i & 1], key0, c2);
+    rows.wide_step(keys(i), values(i), key0, c2);
   }
 }
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 2)
 chunk_kernel(const ChunkParams p) {
-  constexpr int QT = 1;
-  __shared__ __attribute__((aligned(16))) char stage[2][Stage<D>::kBytes];
+  __shared__ __attribute__((aligned(16))) Stage<D> stage;
   __shared__ uint32_t places[kStage / 16];
-  __shared__ uint8_t nan_marks[2][kKeys][4];
-  __shared__ int flags[2];
   __shared__ int64_t sums[kWaves], found[2];
 
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
@@ -628,7 +783,7 @@ chunk_kernel(const ChunkParams p) {
     return;
   }
 
-  Rows<D, QT, F16> rows;
+  Rows<D, F16> rows;
   ChunkNote note{};
   while (piece.at < piece.end) {
     const Seq s = Seq::of<true>(p, piece.b);
@@ -643,25 +798,23 @@ chunk_kernel(const ChunkParams p) {
     const int begin = p.whole ? 0 : (int)(piece.at - piece.tile_begin) * kKeys;
     const int end = p.whole ? tile_seen
                             : (int)min((int64_t)tile_seen, (min(tile_end, piece.end) - piece.tile_begin) * kKeys);
-    const int wave_row = wave * 32 * QT;
+    const int wave_row = wave * 32;
     const int least = s.seen(token0);        // keys that all rows see
     rows.clear();
-#pragma unroll
-    for (int t = 0; t < QT; ++t) {
+    {
       // lanes past the last row repeat it; their results are dropped
-      const int r = min(wave_row + t * 32 + (lane & 31), n_rows - 1);
+      const int r = min(wave_row + (lane & 31), n_rows - 1);
       const int at = r / heads;
-      rows.seen[t] = s.seen(token0 + at);
+      rows.seen = s.seen(token0 + at);
       const uint16_t* src = p.q + (int64_t)(s.first + token0 + at) * p.q_stride + (head0 + r - at * heads) * D + half * 8;
 #pragma unroll
       for (int st = 0; st < D / 16; ++st) {
-        rows.q[t][st] = *reinterpret_cast<const u32x4*>(src + st * 16);
-        if (p.negate) rows.q[t][st] ^= 0x80008000u;
+        rows.q[st] = *reinterpret_cast<const u32x4*>(src + st * 16);
+        if (p.negate) rows.q[st] ^= 0x80008000u;
       }
     }
     const int32_t* table = p.bt + (int64_t)piece.b * p.bt_stride;
     const uint32_t key_blocks = p.kv_heads * (D / 32);
-    const Loader<D> loader{p, places, key_blocks};
     for (int stage0 = begin; stage0 < end; stage0 += kStage) {
       const int stage_end = min(end, stage0 + kStage), n = stage_end - stage0;
       const int steps = (n + kKeys - 1) / kKeys;
@@ -670,31 +823,29 @@ chunk_kernel(const ChunkParams p) {
         const int j = min(stage0 + i * 16, s.cap - 1);
         const int id = min(max(table[j >> p.bs_shift], 0), p.num_blocks - 1);
         const uint32_t slot = ((uint32_t)id << p.bs_shift) + (stage0 + i * 16 & (1 << p.bs_shift) - 1);
-        places[i] = slot * key_blocks + kv_head * (D / 32);
+        places[i] = slot * key_blocks;
       }
-      if (tid < 2) flags[tid] = -1;
+      if (tid < 8) stage.flags[tid >> 1][tid & 1] = -1;
       __syncthreads();
-      const auto in_context = [&](int i) { return s.cap - stage0 - i * kKeys; };
       if (wave < kWaves / 2)
-        walk<true>(loader, rows, stage, flags, nan_marks, stage0, steps, least, in_context, p.c2);
+        walk<true>(p, rows, stage, places, kv_head, stage0, steps, least, s.cap - stage0);
       else
-        walk<false>(loader, rows, stage, flags, nan_marks, stage0, steps, least, in_context, p.c2);
+        walk<false>(p, rows, stage, places, kv_head, stage0, steps, least, s.cap - stage0);
     }
 
     const bool first_part = piece.at == piece.tile_begin, last_part = tile_end <= piece.end;
-#pragma unroll
-    for (int t = 0; t < QT; ++t) {
-      const float m = rows.m[t], l = rows.l[t] + __shfl_xor(rows.l[t], 32);
-      const float rounded = rows.r[t] + __shfl_xor(rows.r[t], 32);
-      const int r = here_only(wave_row + t * 32 + (lane & 31));
+    {
+      const float m = rows.m, l = rows.l + __shfl_xor(rows.l, 32);
+      const float rounded = rows.r + __shfl_xor(rows.r, 32);
+      const int r = here_only(wave_row + (lane & 31));
 #pragma unroll
       for (int c = 0; c < D / 32; ++c)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (rows.nan_blocks[t] >> ((i >> 2) * 8 * (D / 32) / 32) & 1) rows.o[t][c][i] = __builtin_nanf("");
-      if (r >= n_rows) continue;
+          if (rows.nan_blocks >> ((i >> 2) * 8 * (D / 32) / 32) & 1) rows.o[c][i] = __builtin_nanf("");
       constexpr int kCols = D / 32;
-      if (first_part && last_part) {
+      if (r >= n_rows) {
+      } else if (first_part && last_part) {
         const int at = r / heads;
         const int64_t row = (int64_t)(s.first + token0 + at) * p.q_heads + head0 + (r - at * heads);
         const float inv = rounded == 0.f ? 0.f : 1.f / rounded;
@@ -705,7 +856,7 @@ chunk_kernel(const ChunkParams p) {
 #pragma unroll
           for (int i = 0; i < 2 * kCols; ++i) {
             const int e = 2 * i, f = 2 * i + 1;
-            x[i] = pack<F16>(rows.o[t][e % kCols][4 * a + e / kCols] * inv, rows.o[t][f % kCols][4 * a + f / kCols] * inv);
+            x[i] = pack<F16>(rows.o[e % kCols][4 * a + e / kCols] * inv, rows.o[f % kCols][4 * a + f / kCols] * inv);
           }
           u32x4* dst = reinterpret_cast<u32x4*>(p.out + row * D + (8 * a + 4 * half) * kCols);
 #pragma unroll
@@ -721,7 +872,7 @@ chunk_kernel(const ChunkParams p) {
           for (int i = 0; i < kCols; ++i) {
             f32x4 x;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = rows.o[t][(4 * i + j) % kCols][4 * a + (4 * i + j) / kCols];
+            for (int j = 0; j < 4; ++j) x[j] = rows.o[(4 * i + j) % kCols][4 * a + (4 * i + j) / kCols];
             dst[i] = x;
           }
         }
