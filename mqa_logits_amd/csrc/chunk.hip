@@ -765,24 +765,11 @@ __device__ __forceinline__ void walk(const ChunkParams& p, Rows<D, F16>& rows, S
   }
 }
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads, 2)
-chunk_kernel(const ChunkParams p) {
-  __shared__ __attribute__((aligned(16))) Stage<D> stage;
-  __shared__ uint32_t places[kStage / 16];
-  __shared__ int64_t sums[kWaves], found[2];
-
+// A worker's piece, for a wave of the half that loads K (KEYS) or V.
+template <bool KEYS, int D, bool F16>
+__device__ __forceinline__ void work(const ChunkParams& p, Piece piece, int worker, Stage<D>& stage, uint32_t* places) {
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // neighbouring workers, which read the same keys, on one XCD
-  const int worker = (blockIdx.x & 7) * ((p.workers + 7) / 8) + (blockIdx.x >> 3);
-  Piece piece;
-  const bool any = worker < p.workers && piece.find(p, worker, sums, found);
-  if (!any) {
-    if (p.notes && tid == 0 && worker < p.workers) p.notes[worker].parts = 0;
-    return;
-  }
-
   Rows<D, F16> rows;
   ChunkNote note{};
   while (piece.at < piece.end) {
@@ -827,10 +814,7 @@ chunk_kernel(const ChunkParams p) {
       }
       if (tid < 8) stage.flags[tid >> 1][tid & 1] = -1;
       __syncthreads();
-      if (wave < kWaves / 2)
-        walk<true>(p, rows, stage, places, kv_head, stage0, steps, least, s.cap - stage0);
-      else
-        walk<false>(p, rows, stage, places, kv_head, stage0, steps, least, s.cap - stage0);
+      walk<KEYS>(p, rows, stage, places, kv_head, stage0, steps, least, s.cap - stage0);
     }
 
     const bool first_part = piece.at == piece.tile_begin, last_part = tile_end <= piece.end;
@@ -895,6 +879,28 @@ chunk_kernel(const ChunkParams p) {
     }
   }
   if (p.notes && tid == 0) p.notes[worker] = note;
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 2)
+chunk_kernel(const ChunkParams p) {
+  __shared__ __attribute__((aligned(16))) Stage<D> stage;
+  __shared__ uint32_t places[kStage / 16];
+  __shared__ int64_t sums[kWaves], found[2];
+
+  const int tid = threadIdx.x;
+  // neighbouring workers, which read the same keys, on one XCD
+  const int worker = (blockIdx.x & 7) * ((p.workers + 7) / 8) + (blockIdx.x >> 3);
+  Piece piece;
+  const bool any = worker < p.workers && piece.find(p, worker, sums, found);
+  if (!any) {
+    if (p.notes && tid == 0 && worker < p.workers) p.notes[worker].parts = 0;
+    return;
+  }
+  if (__builtin_amdgcn_readfirstlane(tid >> 6) < kWaves / 2)
+    work<true, D, F16>(p, piece, worker, stage, places);
+  else
+    work<false, D, F16>(p, piece, worker, stage, places);
 }
 
 // Joins the parts of the tiles that were cut; a tile's note is its last worker's.
