@@ -6,6 +6,7 @@
 // over the keys j that row r, a (token, head) pair, sees.
 #include <hip/hip_runtime.h>
 
+#include <cstddef>
 #include <type_traits>
 
 #include "launch.hpp"
@@ -417,21 +418,29 @@ struct Rows {
   }
 
   // Operands of half a step: 32 keys' rows of K, V's columns of them.
-  __device__ __forceinline__ static u32x4 key_operand(const char* k, int lane, int n) {
-    return *reinterpret_cast<const u32x4*>(k + (lane & 31) * Stage<D>::kKeyPitch + (lane >> 5) * 16 + n * 32);
+  // (at: the lane's first, as an offset into the stage that the compiler takes as it is)
+  __device__ __forceinline__ static uint32_t key_at(uint32_t buffer, int lane) {
+    return lanes(buffer + (lane & 31) * Stage<D>::kKeyPitch + (lane >> 5) * 16);
   }
-  __device__ __forceinline__ static u32x4 value_operand(const char* v, int lane, int n) {
-    return *reinterpret_cast<const u32x4*>(v + (n % kCols * 32 + (lane & 31)) * Stage<D>::kValPitch + (lane >> 5) * 16 + n / kCols * 32);
+  __device__ __forceinline__ static uint32_t value_at(uint32_t buffer, int lane) {
+    return lanes(buffer + (lane & 31) * Stage<D>::kValPitch + (lane >> 5) * 16);
+  }
+  __device__ __forceinline__ static u32x4 key_operand(const char* lds, uint32_t at, int n) {
+    return *reinterpret_cast<const u32x4*>(lds + at + n * 32);
+  }
+  __device__ __forceinline__ static u32x4 value_operand(const char* lds, uint32_t at, int n) {
+    return *reinterpret_cast<const u32x4*>(lds + at + n % kCols * 32 * Stage<D>::kValPitch + n / kCols * 32);
   }
   // A product must not overlap its operands.  The compiler was seen to let one with
   // a constant 0 to add to overlap them: they are used once more behind it.
   __device__ __forceinline__ static void keep(u32x4 a, u32x4 b) { asm volatile("" ::"v"(a), "v"(b)); }
 
   // The scores of 32 keys: key i % 4 + 8 (i / 4) + 4 (l / 32) of row l % 32.
-  __device__ __forceinline__ void multiply(f32x16& x, const char* k, int lane) const {
+  __device__ __forceinline__ void multiply(f32x16& x, const char* lds, uint32_t keys, int lane) const {
+    const uint32_t k = key_at(keys, lane);
     u32x4 a[kAhead];
 #pragma unroll
-    for (int n = 0; n < kAhead; ++n) a[n] = key_operand(k, lane, n);
+    for (int n = 0; n < kAhead; ++n) a[n] = key_operand(lds, k, n);
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = 0.f;
     __builtin_amdgcn_sched_barrier(0);
@@ -440,7 +449,7 @@ struct Rows {
       x = mma<F16>(a[n % kAhead], q[n], x);
       __builtin_amdgcn_sched_barrier(0);
       if (n == 0) keep(a[0], q[0]);
-      if (n + kAhead < kKeyOps) a[n % kAhead] = key_operand(k, lane, n + kAhead);
+      if (n + kAhead < kKeyOps) a[n % kAhead] = key_operand(lds, k, n + kAhead);
     }
     // The compiler was seen to read a product's result right behind a branch,
     // before it is there; the products end here.
@@ -484,6 +493,12 @@ struct Rows {
       sum += y;
       rounded = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, word), f16x2{(_Float16)1.f, (_Float16)1.f}, rounded, false);
     }
+    // what has been added is there, not put off to where it is used
+    __device__ __forceinline__ void settle(int pair) {
+      uint32_t word = w[pair / 4][pair % 4];
+      asm volatile("" : "+v"(word), "+v"(rounded));
+      w[pair / 4][pair % 4] = word;
+    }
   };
   __device__ __forceinline__ void form(const f32x16& x, Weights& w, float c2) const {
     w.clear();
@@ -506,18 +521,19 @@ struct Rows {
   }
 
   // The weights of 32 keys, and their V.
-  __device__ __forceinline__ void finish(f32x16& x, const char* v, int lane, float c2) {
+  __device__ __forceinline__ void finish(f32x16& x, const char* lds, uint32_t values, int lane, float c2) {
+    const uint32_t v = value_at(values, lane);
     Weights w;
     form(x, w, c2);
     check(x, w, c2);
     u32x4 a[kAhead];
 #pragma unroll
-    for (int n = 0; n < kAhead; ++n) a[n] = value_operand(v, lane, n);
+    for (int n = 0; n < kAhead; ++n) a[n] = value_operand(lds, v, n);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int n = 0; n < kValOps; ++n) {
       o[n % kCols] = mma<true>(a[n % kAhead], w.w[n / kCols], o[n % kCols]);
-      if (n + kAhead < kValOps) a[n % kAhead] = value_operand(v, lane, n + kAhead);
+      if (n + kAhead < kValOps) a[n % kAhead] = value_operand(lds, v, n + kAhead);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -526,13 +542,14 @@ struct Rows {
   // weights, and other work (0 .. kValOps - 1) between V's: the matrix cores and the
   // vector ALU work side by side.
   template <class Work>
-  __device__ __forceinline__ void finish_and_multiply(f32x16& x, f32x16& next, const char* v, const char* k, int lane, float c2,
-                                                      const Work& work) {
+  __device__ __forceinline__ void finish_and_multiply(f32x16& x, f32x16& next, const char* lds, uint32_t values, uint32_t keys,
+                                                      int lane, float c2, const Work& work) {
+    const uint32_t k = key_at(keys, lane), v = value_at(values, lane);
     u32x4 a[kAhead];
     Weights w;
     w.clear();
 #pragma unroll
-    for (int n = 0; n < kAhead; ++n) a[n] = key_operand(k, lane, n);
+    for (int n = 0; n < kAhead; ++n) a[n] = key_operand(lds, k, n);
 #pragma unroll
     for (int i = 0; i < 16; ++i) next[i] = 0.f;
     __builtin_amdgcn_sched_barrier(0);
@@ -547,13 +564,16 @@ struct Rows {
         __builtin_amdgcn_sched_barrier(0);
         if (n == 0) keep(a[0], q[0]);
         if (n + kAhead < kKeyOps)
-          a[n % kAhead] = key_operand(k, lane, n + kAhead);
+          a[n % kAhead] = key_operand(lds, k, n + kAhead);
         else
-          a[n % kAhead] = value_operand(v, lane, n + kAhead - kKeyOps);
+          a[n % kAhead] = value_operand(lds, v, n + kAhead - kKeyOps);
       }
 #pragma unroll
       for (int j = 0; j < kEach; ++j) {
-        if (n >= 2) w.add((n - 2) * kEach + j, e[j][0], e[j][1]);
+        if (n >= 2) {
+          w.add((n - 2) * kEach + j, e[j][0], e[j][1]);
+          w.settle((n - 2) * kEach + j);
+        }
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           if (n >= 1 && n <= kKeyOps) e[j][y] = __builtin_amdgcn_exp2f(f[j][y]);
@@ -569,7 +589,7 @@ struct Rows {
     for (int n = 0; n < kValOps; ++n) {
       o[n % kCols] = mma<true>(a[n % kAhead], w.w[n / kCols], o[n % kCols]);
       __builtin_amdgcn_sched_barrier(0);
-      if (n + kAhead < kValOps) a[n % kAhead] = value_operand(v, lane, n + kAhead);
+      if (n + kAhead < kValOps) a[n % kAhead] = value_operand(lds, v, n + kAhead);
       work(n);
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -577,17 +597,18 @@ struct Rows {
 
   // A step with unusual scales: LDS holds bf16, weights are split into two parts,
   // and fp16 queries as well.
-  __device__ __forceinline__ void wide_step(const char* k, const char* v, int key0, float c2) {
+  __device__ __forceinline__ void wide_step(const char* lds, uint32_t keys, uint32_t values, int key0, float c2) {
 #pragma nounroll
     for (int half_step = 0; half_step < 2; ++half_step) {
       const int lane = here_only(threadIdx.x & 63);
+      const uint32_t k = key_at(keys + half_step * 32 * Stage<D>::kKeyPitch, lane), v = value_at(values + half_step * 64, lane);
       f32x16 s;
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = 0.f;
       asm volatile("" : "+v"(s));            // (zeros in registers: see keep)
 #pragma unroll
       for (int st = 0; st < kSteps; ++st) {
-        const u32x4 a = key_operand(k + half_step * 32 * Stage<D>::kKeyPitch, lane, st);
+        const u32x4 a = key_operand(lds, k, st);
         if constexpr (F16) {
           // two exact parts; an infinity stays in the first alone
           u32x4 hi, lo;
@@ -631,7 +652,7 @@ struct Rows {
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
-          const u32x4 a = value_operand(v + half_step * 64, lane, n * kCols + c);
+          const u32x4 a = value_operand(lds, v, n * kCols + c);
 #pragma unroll
           for (int part = 0; part < 2; ++part) o[c] = mma<false>(a, w[n][part], o[c]);
           __builtin_amdgcn_sched_barrier(0);
@@ -653,85 +674,92 @@ __device__ __forceinline__ void walk(const ChunkParams& p, Rows<D, F16>& rows, S
   constexpr int kLead = KEYS ? 2 : 1;        // steps that this half is ahead
   const float c2 = p.c2;
   const Loader<D, KEYS> loader(p, tid, kv_head);
-  Raw raw;
+  char* const lds = reinterpret_cast<char*>(&stage);
+  Raw raw, ahead;                            // the step to store next, and the one after it
   // first blocks of the wave's keys, of 64 steps from `held` on, one in each lane
   uint32_t held_places = 0;
   int held = -64;
-  const auto fetch = [&](int i) {
+  const auto fetch = [&](Raw& r, int i) {
     i = min(i, steps - 1);                   // (past the last step, the last again)
     if (i >= held + 64) {
       held = i & ~63;
       held_places = places[min(held + lane, steps - 1) * 4 + wave];
     }
-    loader.load(raw, __builtin_amdgcn_readlane(held_places, i & 63));
+    loader.load(r, __builtin_amdgcn_readlane(held_places, i & 63));
   };
-  const auto keys = [&](int i) { return stage.k[i % 3]; };
-  const auto values = [&](int i) { return stage.v[i & 1]; };
-  const auto target = [&](int i) { return KEYS ? keys(i) : values(i); };
-  const auto mark_wide = [&](int i) {
-    if (__builtin_expect(__any(wide_scales<KEYS, F16>(raw)), 0)) stage.flags[i & 3][KEYS] = i;
+  const auto keys = [&](int i) { return (uint32_t)offsetof(Stage<D>, k) + i % 3 * Stage<D>::kKeyBytes; };
+  const auto values = [&](int i) { return (uint32_t)offsetof(Stage<D>, v) + (i & 1) * Stage<D>::kValBytes; };
+  const auto target = [&](int i) { return lds + (KEYS ? keys(i) : values(i)); };
+  // step i is in r
+  const auto check_step = [&](Raw& r, int i) {
+    if (keys_left - i * kKeys < kKeys) check_context<KEYS>(r, here_only(tid), keys_left - i * kKeys);
+    if (__builtin_expect(__any(wide_scales<KEYS, F16>(r)), 0)) stage.flags[i & 3][KEYS] = i;
   };
-  const auto store = [&](int i) {
-    const int me = here_only(tid);
-    if (keys_left - i * kKeys < kKeys) check_context<KEYS>(raw, me, keys_left - i * kKeys);
-    mark_wide(i);
-    put<D, KEYS, kHalf>(raw, me, target(i));
+  // to the next step: it is marked two barriers ahead of its products
+  const auto advance = [&](int i) {
+    raw = ahead;
+    check_step(raw, i + kLead + 1);
+    fetch(ahead, i + kLead + 2);
   };
   const auto narrow = [&](int i) {
-    return __builtin_amdgcn_readfirstlane(stage.flags[i & 3][0]) != i && __builtin_amdgcn_readfirstlane(stage.flags[i & 3][1]) != i;
+    const int v = __builtin_amdgcn_readfirstlane(stage.flags[i & 3][0]), k = __builtin_amdgcn_readfirstlane(stage.flags[i & 3][1]);
+    return v != i && k != i;
   };
 
-  fetch(0);
-  store(0);
-  fetch(1);
+  fetch(raw, 0);
+  fetch(ahead, 1);
+  check_step(raw, 0);
+  put<D, KEYS, kHalf>(raw, here_only(tid), target(0));
   if constexpr (KEYS) {
-    store(1);                                // (a step that is not there: never used)
-    fetch(2);
+    advance(-2);
+    put<D, KEYS, kHalf>(raw, here_only(tid), target(1));    // (a step that is not there: never used)
   }
+  advance(-1);
   __syncthreads();
   f32x16 x, y;                               // scores of a step's halves
-  rows.multiply(x, keys(0), lane);
+  rows.multiply(x, lds, keys(0), lane);
   rows.mask(x, here_only(lane), stage0);
-  // While all rows see this step and the next, and what is stored is whole.
-  const int clear = min(min(max(least - stage0, 0) / kKeys, steps) - 1, keys_left / kKeys - kLead);
+  // While all rows see this step and the next.
+  const int clear = min(max(least - stage0, 0) / kKeys, steps) - 1;
   int i = 0;
+  bool good = narrow(0);
 #pragma nounroll
-  for (; i < clear && narrow(i); ++i) {
+  for (; i < clear && good; ++i) {
     char* const into = target(i + kLead);
-    rows.finish_and_multiply(x, y, values(i), keys(i) + kHalfKeys, lane, c2, [&](int n) {
-      const int me = here_only(tid);
-      if (n == 1) put_part<D, KEYS, kHalf, 0>(raw, me, into);
+    const int next_v = stage.flags[i + 1 & 3][0], next_k = stage.flags[i + 1 & 3][1];
+    rows.finish_and_multiply(x, y, lds, values(i), keys(i) + kHalfKeys, lane, c2, [&](int n) {
+      if (n == 1) put_part<D, KEYS, kHalf, 0>(raw, tid, into);
       if constexpr (D == 128)
-        if (n == 5) put_part<D, KEYS, kHalf, 1>(raw, me, into);
+        if (n == 5) put_part<D, KEYS, kHalf, 1>(raw, tid, into);
     });
-    rows.finish_and_multiply(y, x, values(i) + kHalfVals, keys(i + 1), lane, c2, [&](int n) {
-      const int me = here_only(tid);
-      if (n == 1) put_part<D, KEYS, kHalf, D / 64>(raw, me, into);
+    rows.finish_and_multiply(y, x, lds, values(i) + kHalfVals, keys(i + 1), lane, c2, [&](int n) {
+      if (n == 1) put_part<D, KEYS, kHalf, D / 64>(raw, tid, into);
       if constexpr (D == 128)
-        if (n == 5) put_part<D, KEYS, kHalf, 3>(raw, me, into);
+        if (n == 5) put_part<D, KEYS, kHalf, 3>(raw, tid, into);
     });
-    mark_wide(i + kLead);
-    fetch(i + kLead + 1);
+    advance(i);
+    good = __builtin_amdgcn_readfirstlane(next_v) != i + 1 && __builtin_amdgcn_readfirstlane(next_k) != i + 1;
     __syncthreads();
   }
 #pragma nounroll
-  for (; i < steps && narrow(i); ++i) {
+  for (; i < steps && good; ++i) {
     const int me = here_only(lane), key0 = stage0 + i * kKeys;
-    rows.multiply(y, keys(i) + kHalfKeys, me);
+    rows.multiply(y, lds, keys(i) + kHalfKeys, me);
     rows.mask(y, me, key0 + 32);
-    rows.finish(x, values(i), me, c2);
+    rows.finish(x, lds, values(i), me, c2);
     if (i + 1 < steps) {
-      rows.multiply(x, keys(i + 1), me);
+      rows.multiply(x, lds, keys(i + 1), me);
       rows.mask(x, me, key0 + kKeys);
     }
-    rows.finish(y, values(i) + kHalfVals, me, c2);
-    store(i + kLead);
-    fetch(i + kLead + 1);
+    rows.finish(y, lds, values(i) + kHalfVals, me, c2);
+    put<D, KEYS, kHalf>(raw, here_only(tid), target(i + kLead));
+    advance(i);
+    good = narrow(i + 1);
     __syncthreads();
   }
   if (__builtin_expect(i == steps, 1)) return;
   // from a step with unusual scales on, in bf16, NaN scales apart
-  fetch(i);
+  fetch(raw, i);
 #pragma nounroll
   for (; i < steps; ++i) {
     const int me = here_only(tid);
@@ -750,7 +778,7 @@ __device__ __forceinline__ void walk(const ChunkParams& p, Rows<D, F16>& rows, S
     __syncthreads();                         // the stage's last use is over
     put<D, KEYS, false>(raw, me, target(i));
     __syncthreads();
-    fetch(i + 1);
+    fetch(raw, i + 1);
     const int key0 = stage0 + i * kKeys;
     uint32_t marks = 0;
 #pragma unroll
@@ -761,7 +789,7 @@ __device__ __forceinline__ void walk(const ChunkParams& p, Rows<D, F16>& rows, S
         const uint32_t word = __shfl(marks, j);
         if (key0 + j < rows.seen) rows.nan_blocks |= word;
       }
-    rows.wide_step(keys(i), values(i), key0, c2);
+    rows.wide_step(lds, keys(i), values(i), key0, c2);
   }
 }
 
