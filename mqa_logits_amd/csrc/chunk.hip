@@ -541,15 +541,13 @@ struct Rows {
   // The same for scores x, with the products of the next 32 keys between the
   // weights, and other work (0 .. kValOps - 1) between V's: the matrix cores and the
   // vector ALU work side by side.
+  // a: the first operands of `keys`, and then of `then`.
   template <class Work>
-  __device__ __forceinline__ void finish_and_multiply(f32x16& x, f32x16& next, const char* lds, uint32_t values, uint32_t keys,
-                                                      int lane, float c2, const Work& work) {
-    const uint32_t k = key_at(keys, lane), v = value_at(values, lane);
-    u32x4 a[kAhead];
+  __device__ __forceinline__ void finish_and_multiply(f32x16& x, f32x16& next, u32x4 (&a)[kAhead], const char* lds, uint32_t values,
+                                                      uint32_t keys, uint32_t then, int lane, float c2, const Work& work) {
+    const uint32_t k = key_at(keys, lane), v = value_at(values, lane), after = key_at(then, lane);
     Weights w;
     w.clear();
-#pragma unroll
-    for (int n = 0; n < kAhead; ++n) a[n] = key_operand(lds, k, n);
 #pragma unroll
     for (int i = 0; i < 16; ++i) next[i] = 0.f;
     __builtin_amdgcn_sched_barrier(0);
@@ -582,14 +580,17 @@ struct Rows {
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    static_assert(kKeyOps % kAhead == 0, "V's operands follow K's in turn");
+    static_assert(kKeyOps % kAhead == 0 && kValOps % kAhead == 0, "operands follow each other in turn");
     check(x, w, c2);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int n = 0; n < kValOps; ++n) {
       o[n % kCols] = mma<true>(a[n % kAhead], w.w[n / kCols], o[n % kCols]);
       __builtin_amdgcn_sched_barrier(0);
-      if (n + kAhead < kValOps) a[n % kAhead] = value_operand(lds, v, n + kAhead);
+      if (n + kAhead < kValOps)
+        a[n % kAhead] = value_operand(lds, v, n + kAhead);
+      else
+        a[n % kAhead] = key_operand(lds, after, n + kAhead - kValOps);
       work(n);
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -723,16 +724,20 @@ __device__ __forceinline__ void walk(const ChunkParams& p, Rows<D, F16>& rows, S
   const int clear = min(max(least - stage0, 0) / kKeys, steps) - 1;
   int i = 0;
   bool good = narrow(0);
+  u32x4 a[Rows<D, F16>::kAhead];
+#pragma unroll
+  for (int n = 0; n < Rows<D, F16>::kAhead; ++n)
+    a[n] = Rows<D, F16>::key_operand(lds, Rows<D, F16>::key_at(keys(0) + kHalfKeys, lane), n);
 #pragma nounroll
   for (; i < clear && good; ++i) {
     char* const into = target(i + kLead);
     const int next_v = stage.flags[i + 1 & 3][0], next_k = stage.flags[i + 1 & 3][1];
-    rows.finish_and_multiply(x, y, lds, values(i), keys(i) + kHalfKeys, lane, c2, [&](int n) {
+    rows.finish_and_multiply(x, y, a, lds, values(i), keys(i) + kHalfKeys, keys(i + 1), lane, c2, [&](int n) {
       if (n == 1) put_part<D, KEYS, kHalf, 0>(raw, tid, into);
       if constexpr (D == 128)
         if (n == 5) put_part<D, KEYS, kHalf, 1>(raw, tid, into);
     });
-    rows.finish_and_multiply(y, x, lds, values(i) + kHalfVals, keys(i + 1), lane, c2, [&](int n) {
+    rows.finish_and_multiply(y, x, a, lds, values(i) + kHalfVals, keys(i + 1), keys(i + 1) + kHalfKeys, lane, c2, [&](int n) {
       if (n == 1) put_part<D, KEYS, kHalf, D / 64>(raw, tid, into);
       if constexpr (D == 128)
         if (n == 5) put_part<D, KEYS, kHalf, 3>(raw, tid, into);
