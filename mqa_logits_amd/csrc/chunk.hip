@@ -283,9 +283,14 @@ __device__ __forceinline__ uint32_t lanes(uint32_t offset) {
 // What a thread loads of a step.  The first half of the workgroup takes D/8 bytes
 // of codes of a key each and their scale; the second D/32 bytes of V's codes of four
 // keys and their scales.  A wave's keys are 16 in a row.
+//
+// Whole words are loaded, and what a thread needs of them is taken out when they
+// have arrived: of narrower loads the compiler cut the upper bits off at once,
+// and waited for them.
 struct Raw {
   u32x4 codes;
   uint32_t scales[4];
+  uint32_t first;          // block of the wave's 16 keys (wave-uniform)
 };
 
 // The second half's keys and columns: 16 lanes in a row write all banks.
@@ -294,20 +299,20 @@ __device__ __forceinline__ int value_column(int tid) { return tid >> 2 & 15; }
 
 template <int D, bool KEYS>
 struct Loader {
-  Bytes codes, scales;     // of the KV head
+  Bytes codes, scales;
   uint32_t code_at, scale_at;      // the lane's offsets from its 16 keys' first block
   uint32_t key_blocks;             // blocks (of 32 elements) from one key of the pool to the next
 
-  __device__ __forceinline__ Loader(const ChunkParams& p, int tid, int kv_head)
-      : codes((Bytes)(KEYS ? p.k : p.v) + kv_head * (D / 2)), scales((Bytes)(KEYS ? p.k_sf : p.v_sf) + kv_head * (D / 32)),
-        key_blocks(p.kv_heads * (D / 32)) {
+  __device__ __forceinline__ Loader(const ChunkParams& p, int tid)
+      : codes((Bytes)(KEYS ? p.k : p.v)), scales((Bytes)(KEYS ? p.k_sf : p.v_sf)), key_blocks(p.kv_heads * (D / 32)) {
     const uint32_t key = KEYS ? tid >> 2 & 15 : (tid & 3) * 4, c = KEYS ? tid & 3 : value_column(tid);
     code_at = key * key_blocks * 16 + c * (KEYS ? D / 8 : D / 32);
     scale_at = key * key_blocks + c * (KEYS ? D / 4 : D / 16) / 32;
   }
-  // first: block of the wave's 16 keys (wave-uniform)
+  // (pools are whole words, the words of the heads' scales in it whatever the head)
   __device__ __forceinline__ void load(Raw& r, uint32_t first) const {
-    const Bytes from = scalar(codes + ((uint64_t)first << 4)), sf = scalar(scales + first);
+    r.first = first;
+    const Bytes from = scalar(codes + ((uint64_t)first << 4));
     if constexpr (KEYS) {
       if constexpr (D == 128) {
         r.codes = load_from<u32x4>(from + lanes(code_at));
@@ -315,15 +320,36 @@ struct Loader {
         const u32x2 x = load_from<u32x2>(from + lanes(code_at));
         r.codes = u32x4{x[0], x[1], 0u, 0u};
       }
-      r.scales[0] = load_from<uint8_t>(sf + lanes(scale_at));
+      r.scales[0] = load_from<uint32_t>(word_of(first));
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const Bytes at = scalar(from + i * key_blocks * 16);
-        r.codes[i] = D == 128 ? load_from<uint32_t>(at + lanes(code_at)) : load_from<uint16_t>(at + lanes(code_at));
-        r.scales[i] = load_from<uint8_t>(scalar(sf + i * key_blocks) + lanes(scale_at));
+        r.codes[i] = load_from<uint32_t>(at + lanes(code_at & ~3u));
+        r.scales[i] = load_from<uint32_t>(word_of(first + i * key_blocks));
       }
     }
+  }
+  // Of what has arrived: the thread's codes lowest, its scale bytes alone.
+  __device__ __forceinline__ void take(Raw& r) const {
+    if constexpr (KEYS) {
+      r.scales[0] = r.scales[0] >> byte_at(r.first) & 0xffu;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (D == 64) r.codes[i] >>= (code_at & 2) * 8;
+        r.scales[i] = r.scales[i] >> byte_at(r.first + i * key_blocks) & 0xffu;
+      }
+    }
+  }
+  // The word of the scales of block `first` + scale_at; where its byte is in it.  With
+  // D = 128 a head's four scales are a word.
+  __device__ __forceinline__ Bytes word_of(uint32_t first) const {
+    if constexpr (D == 128) return scalar(scales + first) + lanes(scale_at & ~3u);
+    return scalar(scales + (first & ~3u)) + lanes((first & 3u) + scale_at & ~3u);
+  }
+  __device__ __forceinline__ uint32_t byte_at(uint32_t first) const {
+    return ((D == 128 ? 0 : first & 3u) + scale_at & 3u) * 8;
   }
 };
 
@@ -667,14 +693,14 @@ struct Rows {
 // computed; K is put into LDS two steps ahead, V one.
 template <bool KEYS, int D, bool F16>
 __device__ __forceinline__ void walk(const ChunkParams& p, Rows<D, F16>& rows, Stage<D>& stage, const uint32_t* places,
-                                     int kv_head, int stage0, int steps, int least, int keys_left) {
+                                     int stage0, int steps, int least, int keys_left) {
   constexpr int kHalfKeys = 32 * Stage<D>::kKeyPitch, kHalfVals = 64;   // bytes to a step's second half
   const int tid = threadIdx.x & (kThreads / 2 - 1);
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   constexpr bool kHalf = KEYS ? F16 : true;
   constexpr int kLead = KEYS ? 2 : 1;        // steps that this half is ahead
   const float c2 = p.c2;
-  const Loader<D, KEYS> loader(p, tid, kv_head);
+  const Loader<D, KEYS> loader(p, tid);
   char* const lds = reinterpret_cast<char*>(&stage);
   Raw raw, ahead;                            // the step to store next, and the one after it
   // first blocks of the wave's keys, of 64 steps from `held` on, one in each lane
@@ -693,6 +719,7 @@ __device__ __forceinline__ void walk(const ChunkParams& p, Rows<D, F16>& rows, S
   const auto target = [&](int i) { return lds + (KEYS ? keys(i) : values(i)); };
   // step i is in r
   const auto check_step = [&](Raw& r, int i) {
+    loader.take(r);
     if (keys_left - i * kKeys < kKeys) check_context<KEYS>(r, here_only(tid), keys_left - i * kKeys);
     if (__builtin_expect(__any(wide_scales<KEYS, F16>(r)), 0)) stage.flags[i & 3][KEYS] = i;
   };
@@ -768,6 +795,7 @@ __device__ __forceinline__ void walk(const ChunkParams& p, Rows<D, F16>& rows, S
 #pragma nounroll
   for (; i < steps; ++i) {
     const int me = here_only(tid);
+    loader.take(raw);
     check_context<KEYS>(raw, me, keys_left - i * kKeys);
     if constexpr (KEYS) {
       if (raw.scales[0] > kLastScale) raw.scales[0] = 255;
@@ -843,11 +871,11 @@ __device__ __forceinline__ void work(const ChunkParams& p, Piece piece, int work
         const int j = min(stage0 + i * 16, s.cap - 1);
         const int id = min(max(table[j >> p.bs_shift], 0), p.num_blocks - 1);
         const uint32_t slot = ((uint32_t)id << p.bs_shift) + (stage0 + i * 16 & (1 << p.bs_shift) - 1);
-        places[i] = slot * key_blocks;
+        places[i] = slot * key_blocks + kv_head * (D / 32);
       }
       if (tid < 8) stage.flags[tid >> 1][tid & 1] = -1;
       __syncthreads();
-      walk<KEYS>(p, rows, stage, places, kv_head, stage0, steps, least, s.cap - stage0);
+      walk<KEYS>(p, rows, stage, places, stage0, steps, least, s.cap - stage0);
     }
 
     const bool first_part = piece.at == piece.tile_begin, last_part = tile_end <= piece.end;
