@@ -27,6 +27,8 @@ constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kKeys = 64;                    // of a step
 constexpr int kStage = 16384;                // keys whose places LDS holds at a time
+// Steps that beginning and ending a tile takes as long as (about 8 us; a step 2).
+constexpr int kTileSteps = 4;
 constexpr uint32_t kLastScale = 252;         // bytes above could overflow fp32: they count as NaN
 // Scale bytes (2^-22 .. 2^9) whose steps are worked on in fp16.  Every e2m1 value
 // under 2^-23 .. 2^13 is exact there; large ones are left out for what the weights'
@@ -123,19 +125,20 @@ struct Seq {
   __device__ __forceinline__ int tile_seen(const ChunkParams& p, int i) const {
     return seen(min((int64_t)(i + 1) * p.tile_tokens, (int64_t)n) - 1);
   }
+  // What a tile counts for in the split: its steps, and kTileSteps to begin and end it.
   __device__ __forceinline__ int steps(const ChunkParams& p, int i) const {
-    return p.whole ? 1 : max((tile_seen(p, i) + kKeys - 1) / kKeys, 1);
+    return p.whole ? 1 : (tile_seen(p, i) + kKeys - 1) / kKeys + kTileSteps;
   }
-  // steps of its first k tiles: one each while a step is enough, then
-  // sum of floor((tile_tokens * i + c) / 64), then the context's
+  // The same for its first k tiles: none while no keys are seen, then the sum of
+  // floor((tile_tokens * i + c) / 64), then the context's.
   __device__ __forceinline__ int64_t before(const ChunkParams& p, int k) const {
     if (p.whole) return k;
     const int a = p.tile_tokens;
-    const int64_t room = kKeys - base, full = cap - base;
-    const int64_t few = room < a ? 0 : room / a;                    // tiles that see at most 64 keys
+    const int64_t full = cap - base;
+    const int64_t none = base >= 0 ? 0 : -base / a;                 // tiles that see nothing
     const int64_t until = full <= a ? 0 : (full + a - 1) / a - 1;   // tiles below the cap
-    const int64_t i1 = min(few, (int64_t)k), i2 = min(max(until, i1), (int64_t)k);
-    int64_t sum = i1 + (k - i2) * (int64_t)max((cap + kKeys - 1) / kKeys, 1);
+    const int64_t i1 = min(none, (int64_t)k), i2 = min(max(until, i1), (int64_t)k);
+    int64_t sum = (int64_t)k * kTileSteps + (k - i2) * (int64_t)((cap + kKeys - 1) / kKeys);
     const int64_t m = i2 - i1, turns = m / kKeys;
     if (m > 0) {
       const int64_t c = base + (i1 + 1) * a + kKeys - 1;
@@ -259,7 +262,7 @@ struct Stage {
   // of the step before: three buffers of K, two of V.
   char k[3][kKeyBytes];
   char v[2][kValBytes];
-  int flags[4][2];         // [step][V, K]: the step, if it has unusual scales
+  int flags[4][2];         // [step][V, K]: the piece's step, if it has unusual scales
   uint8_t nan_marks[2][kKeys][4];
 };
 
@@ -693,7 +696,7 @@ struct Rows {
 // computed; K is put into LDS two steps ahead, V one.
 template <bool KEYS, int D, bool F16>
 __device__ __forceinline__ void walk(const ChunkParams& p, Rows<D, F16>& rows, Stage<D>& stage, const uint32_t* places,
-                                     int stage0, int steps, int least, int keys_left) {
+                                     int walked, int stage0, int steps, int least, int keys_left) {
   constexpr int kHalfKeys = 32 * Stage<D>::kKeyPitch, kHalfVals = 64;   // bytes to a step's second half
   const int tid = threadIdx.x & (kThreads / 2 - 1);
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -721,7 +724,7 @@ __device__ __forceinline__ void walk(const ChunkParams& p, Rows<D, F16>& rows, S
   const auto check_step = [&](Raw& r, int i) {
     loader.take(r);
     if (keys_left - i * kKeys < kKeys) check_context<KEYS>(r, here_only(tid), keys_left - i * kKeys);
-    if (__builtin_expect(__any(wide_scales<KEYS, F16>(r)), 0)) stage.flags[i & 3][KEYS] = i;
+    if (__builtin_expect(__any(wide_scales<KEYS, F16>(r)), 0)) stage.flags[i & 3][KEYS] = walked + i;
   };
   // to the next step: it is marked two barriers ahead of its products
   const auto advance = [&](int i) {
@@ -731,7 +734,7 @@ __device__ __forceinline__ void walk(const ChunkParams& p, Rows<D, F16>& rows, S
   };
   const auto narrow = [&](int i) {
     const int v = __builtin_amdgcn_readfirstlane(stage.flags[i & 3][0]), k = __builtin_amdgcn_readfirstlane(stage.flags[i & 3][1]);
-    return v != i && k != i;
+    return v != walked + i && k != walked + i;
   };
 
   fetch(raw, 0);
@@ -770,7 +773,7 @@ __device__ __forceinline__ void walk(const ChunkParams& p, Rows<D, F16>& rows, S
         if (n == 5) put_part<D, KEYS, kHalf, 3>(raw, tid, into);
     });
     advance(i);
-    good = __builtin_amdgcn_readfirstlane(next_v) != i + 1 && __builtin_amdgcn_readfirstlane(next_k) != i + 1;
+    good = __builtin_amdgcn_readfirstlane(next_v) != walked + i + 1 && __builtin_amdgcn_readfirstlane(next_k) != walked + i + 1;
     __syncthreads();
   }
 #pragma nounroll
@@ -824,6 +827,7 @@ __device__ __forceinline__ void walk(const ChunkParams& p, Rows<D, F16>& rows, S
       }
     rows.wide_step(lds, keys(i), values(i), key0, c2);
   }
+  __syncthreads();                           // (as at the end of other steps)
 }
 
 // A worker's piece, for a wave of the half that loads K (KEYS) or V.
@@ -833,8 +837,11 @@ __device__ __forceinline__ void work(const ChunkParams& p, Piece piece, int work
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   Rows<D, F16> rows;
   ChunkNote note{};
+  Seq s = Seq::of<true>(p, piece.b);
+  // what `places` holds: keys [held_from, held_until) of a sequence and KV head
+  int held_b = -1, held_head = -1, held_from = 0, held_until = 0;
+  int walked = 0;                            // steps of this piece so far
   while (piece.at < piece.end) {
-    const Seq s = Seq::of<true>(p, piece.b);
     const int kv_head = piece.member / p.head_groups;
     const int head0 = kv_head * p.group + piece.member % p.head_groups * p.tile_heads;
     const int heads = min(p.tile_heads, (kv_head + 1) * p.group - head0);
@@ -843,9 +850,10 @@ __device__ __forceinline__ void work(const ChunkParams& p, Piece piece, int work
     const int n_rows = tokens * heads;
     const int tile_seen = s.tile_seen(p, piece.tile);
     const int64_t tile_end = piece.tile_begin + s.steps(p, piece.tile);
-    const int begin = p.whole ? 0 : (int)(piece.at - piece.tile_begin) * kKeys;
-    const int end = p.whole ? tile_seen
-                            : (int)min((int64_t)tile_seen, (min(tile_end, piece.end) - piece.tile_begin) * kKeys);
+    // steps [begin, end) of this part, past the kTileSteps that a tile begins with
+    const auto step_at = [&](int64_t at) { return (int)max(at - piece.tile_begin - kTileSteps, (int64_t)0); };
+    const int begin = p.whole ? 0 : step_at(piece.at) * kKeys;
+    const int end = p.whole ? tile_seen : (int)min((int64_t)tile_seen, (int64_t)step_at(min(tile_end, piece.end)) * kKeys);
     const int wave_row = wave * 32;
     const int least = s.seen(token0);        // keys that all rows see
     rows.clear();
@@ -863,19 +871,28 @@ __device__ __forceinline__ void work(const ChunkParams& p, Piece piece, int work
     }
     const int32_t* table = p.bt + (int64_t)piece.b * p.bt_stride;
     const uint32_t key_blocks = p.kv_heads * (D / 32);
-    for (int stage0 = begin; stage0 < end; stage0 += kStage) {
-      const int stage_end = min(end, stage0 + kStage), n = stage_end - stage0;
-      const int steps = (n + kKeys - 1) / kKeys;
-      __syncthreads();                       // the last use of `places` and the stages is over
-      for (int i = tid; i < steps * (kKeys / 16); i += kThreads) {
-        const int j = min(stage0 + i * 16, s.cap - 1);
-        const int id = min(max(table[j >> p.bs_shift], 0), p.num_blocks - 1);
-        const uint32_t slot = ((uint32_t)id << p.bs_shift) + (stage0 + i * 16 & (1 << p.bs_shift) - 1);
-        places[i] = slot * key_blocks + kv_head * (D / 32);
+    for (int stage0 = begin; stage0 < end;) {
+      const int window = stage0 & -kStage, stage_end = min(end, window + kStage);
+      const int steps = (stage_end - stage0 + kKeys - 1) / kKeys;
+      // (every wave is past the last step's barrier: nothing reads `places` or the stage)
+      if (held_b != piece.b || held_head != kv_head || held_from < window || held_from > stage0 || held_until < stage0) {
+        held_b = piece.b;
+        held_head = kv_head;
+        held_from = held_until = stage0;
       }
-      if (tid < 8) stage.flags[tid >> 1][tid & 1] = -1;
-      __syncthreads();
-      walk<KEYS>(p, rows, stage, places, stage0, steps, least, s.cap - stage0);
+      const int until = stage0 + steps * kKeys;
+      if (held_until < until) {
+        for (int key = held_until + tid * 16; key < until; key += kThreads * 16) {
+          const int id = min(max(table[min(key, s.cap - 1) >> p.bs_shift], 0), p.num_blocks - 1);
+          const uint32_t slot = ((uint32_t)id << p.bs_shift) + (key & (1 << p.bs_shift) - 1);
+          places[(key - window) / 16] = slot * key_blocks + kv_head * (D / 32);
+        }
+        held_until = until;
+        __syncthreads();
+      }
+      walk<KEYS>(p, rows, stage, places + (stage0 - window) / 16, walked, stage0, steps, least, s.cap - stage0);
+      walked += steps + 4;
+      stage0 = stage_end;
     }
 
     const bool first_part = piece.at == piece.tile_begin, last_part = tile_end <= piece.end;
@@ -936,7 +953,8 @@ __device__ __forceinline__ void work(const ChunkParams& p, Piece piece, int work
           piece.b = 0;
           ++piece.member;
         }
-      } while (Seq::of<true>(p, piece.b).tiles == 0);
+        s = Seq::of<true>(p, piece.b);
+      } while (s.tiles == 0);
     }
   }
   if (p.notes && tid == 0) p.notes[worker] = note;
@@ -952,7 +970,8 @@ chunk_kernel(const ChunkParams p) {
   const int tid = threadIdx.x;
   // neighbouring workers, which read the same keys, on one XCD
   const int worker = (blockIdx.x & 7) * ((p.workers + 7) / 8) + (blockIdx.x >> 3);
-  Piece piece;
+  if (tid < 8) stage.flags[tid >> 1][tid & 1] = -1;
+  Piece piece;                               // (find has barriers)
   const bool any = worker < p.workers && piece.find(p, worker, sums, found);
   if (!any) {
     if (p.notes && tid == 0 && worker < p.workers) p.notes[worker].parts = 0;
