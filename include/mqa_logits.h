@@ -491,14 +491,15 @@ typedef struct {
  *            -1 behind them (a block that two of them share is listed twice)
  *   counts   [2] int32: blocks asked of the free list (more than num_free: it did
  *            not suffice), blocks in freed_blocks
- *   workspace of at least paged_kv_evict_workspace_size bytes, 16-byte aligned.
+ *   workspace of at least paged_kv_evict_workspace_size bytes for the same sizes,
+ *            16-byte aligned.
  * Tokens whose old or new block id lies outside [0, num_blocks) are not copied.
  * Nothing that is written may overlap anything else, free blocks no block of a
  * sequence.  Requires 1 <= batch <= 8192, block_size in {16, 32, 64}, 1 <= keep,
  * 0 <= recent <= keep, batch * max_context_len and batch * keep below 2^31,
  * num_blocks * block_size < 2^31.
  */
-int64_t paged_kv_evict_workspace_size(int32_t batch);  /* bytes; negative on error */
+int64_t paged_kv_evict_workspace_size(int32_t batch, int32_t max_context_len);  /* bytes; negative on error */
 mqa_status paged_kv_evict(const float* weights, int64_t weights_stride, const int32_t* context_lens,
                           const int32_t* block_table, int64_t block_table_stride,
                           const int32_t* free_blocks, int32_t num_free, const mqa_pool* pools,

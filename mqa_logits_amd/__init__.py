@@ -94,7 +94,7 @@ def _load():
     lib.paged_chunk_attention_workspace_size.restype = I64
     lib.paged_attention_weights_workspace_size.argtypes = [I32] * 6
     lib.paged_attention_weights_workspace_size.restype = I64
-    lib.paged_kv_evict_workspace_size.argtypes = [I32]
+    lib.paged_kv_evict_workspace_size.argtypes = [I32, I32]
     lib.paged_kv_evict_workspace_size.restype = I64
     lib.mqa_num_cus.argtypes = [I32]
     lib.mqa_num_cus.restype = I32
@@ -858,10 +858,6 @@ def _want_rows(a, t, name, batch, width):
         raise ValueError(f"{name} rows must hold max_context_len = {width} values, got {t.shape[1]}")
 
 
-class _Pool(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("token_bytes", ctypes.c_int64)]
-
-
 Eviction = collections.namedtuple("Eviction", "context_lens block_table weights kept freed counts")
 
 
@@ -880,14 +876,15 @@ def paged_kv_evict(weights, context_lens, block_table, free_blocks, pools, keep,
     and blocks in freed); `out` may hold these.  Where the first count exceeds
     len(free_blocks), the sequences that the list did not reach stay as they are.  Sequences of
     up to `keep` tokens stay as they are.  workspace: a uint8 tensor of
-    paged_kv_evict_workspace_size(batch) bytes to keep between calls on one stream, or None."""
+    paged_kv_evict_workspace_size bytes to keep between calls on one stream, or None."""
     if weights is None or context_lens is None or free_blocks is None or pools is None:
         _required(weights=weights, context_lens=context_lens, free_blocks=free_blocks, pools=pools)
     if not pools:
         raise ValueError("pools must hold at least one tensor")
     if len(pools[0].shape) < 2:
         raise ValueError(f"pools must be [num_blocks, block_size, ...], got {tuple(pools[0].shape)}")
-    num_blocks, block_size = pools[0].shape[:2]
+    lead = pools[0].shape[:2]
+    num_blocks, block_size = lead
     _block_size(block_size)
     if not (1 <= keep < 2 ** 31 and 0 <= recent <= keep and 0 <= max_context_len < 2 ** 31
             and num_blocks < 2 ** 31):
@@ -900,9 +897,10 @@ def paged_kv_evict(weights, context_lens, block_table, free_blocks, pools, keep,
         out = Eviction(new(batch, dtype=i32), new((batch, width), dtype=i32),
                        new((batch, max_context_len), dtype=torch.float32), new((batch, keep), dtype=i32),
                        new(batch * width, dtype=i32), new(2, dtype=i32))
+        strides = max(width, 1), max(max_context_len, 1), keep
     else:
         out = Eviction(*out)
-    size = paged_kv_evict_workspace_size(batch)
+    size = paged_kv_evict_workspace_size(batch, max_context_len)
     if workspace is None:
         workspace, given_workspace = context_lens.new_empty(size, dtype=torch.uint8), False
     else:
@@ -910,8 +908,7 @@ def paged_kv_evict(weights, context_lens, block_table, free_blocks, pools, keep,
     if not (dev >= 0 and _rows_fit(weights, batch, max_context_len, dev)
             and _fits(context_lens, (batch,), i32, dev) and _table_fits(block_table, batch, width, dev)
             and _fits(free_blocks, (free_blocks.numel(),), i32, dev)
-            and all(p.get_device() == dev and p.shape[:2] == pools[0].shape[:2] and p.is_contiguous()
-                    for p in pools)
+            and all([p.get_device() == dev and p.shape[:2] == lead and p.is_contiguous() for p in pools])
             and (not given or (_fits(out.context_lens, (batch,), i32, dev)
                                and _table_fits(out.block_table, batch, width, dev)
                                and _rows_fit(out.weights, batch, max_context_len, dev)
@@ -938,23 +935,27 @@ def paged_kv_evict(weights, context_lens, block_table, free_blocks, pools, keep,
         a.want(out.counts, "out.counts", (2,), I32_T)
         a.want(workspace, "workspace", (None,), itemsize=1)
         a.on_gpu()
-    described = (_Pool * len(pools))()
-    for p, d in zip(pools, described):
-        d.data, d.token_bytes = p.data_ptr(), p[0, 0].numel() * p.element_size() if num_blocks else 0
+    if given:
+        strides = [_row_stride(t, t.shape[1]) for t in (out.block_table, out.weights, out.kept)]
+    # the C structs {data, bytes of a token}, as words: of a contiguous tensor, the stride
+    # of a token is its size
+    words = []
+    for p in pools:
+        words += p.data_ptr(), p.stride(1) * p.itemsize
+    described = (ctypes.c_int64 * len(words))(*words)
     _call(lib.paged_kv_evict, dev, weights.data_ptr(), _row_stride(weights, weights.shape[1]),
           context_lens.data_ptr(), block_table.data_ptr(), _row_stride(block_table, block_table.shape[1]),
           free_blocks.data_ptr(), free_blocks.shape[0], described, len(pools), out.context_lens.data_ptr(),
-          out.block_table.data_ptr(), _row_stride(out.block_table, out.block_table.shape[1]),
-          out.weights.data_ptr(), _row_stride(out.weights, out.weights.shape[1]), out.kept.data_ptr(),
-          _row_stride(out.kept, out.kept.shape[1]), out.freed.data_ptr(), out.counts.data_ptr(),
+          out.block_table.data_ptr(), strides[0], out.weights.data_ptr(), strides[1], out.kept.data_ptr(),
+          strides[2], out.freed.data_ptr(), out.counts.data_ptr(),
           workspace.data_ptr(), size, batch, block_size, num_blocks, max_context_len, keep, recent)
     return out
 
 
 @functools.lru_cache(maxsize=1024)
-def paged_kv_evict_workspace_size(batch):
-    """Bytes of workspace of a paged_kv_evict call for this many sequences."""
-    n = lib.paged_kv_evict_workspace_size(batch)
+def paged_kv_evict_workspace_size(batch, max_context_len):
+    """Bytes of workspace of a paged_kv_evict call of these sizes."""
+    n = lib.paged_kv_evict_workspace_size(batch, max_context_len)
     if n < 0:
         raise MqaError(2, lib.mqa_last_error().decode())
     return n

@@ -907,12 +907,13 @@ mqa_status paged_attention_weights(mqa_dtype dt, const void* q, mqa_float q_type
   return hip_status(mqa::launch_weights(d, q_type == MQA_F16, p, stream), who);
 }
 
-int64_t paged_kv_evict_workspace_size(int32_t batch) {
-  if (batch < 1 || batch > 8192) {
-    fail(MQA_ERR_UNSUPPORTED, "paged_kv_evict_workspace_size: batch=%d not in [1, 8192]", batch);
+int64_t paged_kv_evict_workspace_size(int32_t batch, int32_t max_context_len) {
+  if (batch < 1 || batch > 8192 || max_context_len < 0) {
+    fail(MQA_ERR_UNSUPPORTED, "paged_kv_evict_workspace_size: batch=%d not in [1, 8192], or negative max_context_len=%d",
+         batch, max_context_len);
     return -1;
   }
-  return (int64_t)batch * (int64_t)(sizeof(mqa::EvictPlan) + 8);
+  return mqa::evict_workspace(batch, max_context_len);
 }
 
 mqa_status paged_kv_evict(const float* weights, int64_t weights_stride, const int32_t* context_lens,
@@ -955,9 +956,9 @@ mqa_status paged_kv_evict(const float* weights, int64_t weights_stride, const in
   if (weights_stride < max_context_len || new_weights_stride < max_context_len || kept_stride < keep ||
       block_table_stride < width || new_block_table_stride < width)
     return fail(MQA_ERR_INVALID_ARG, "%s: rows shorter than what they hold", who);
-  if (workspace_bytes < paged_kv_evict_workspace_size(batch))
+  if (workspace_bytes < mqa::evict_workspace(batch, max_context_len))
     return fail(MQA_ERR_INVALID_ARG, "%s: workspace of %lld bytes, %lld needed", who,
-                (long long)workspace_bytes, (long long)paged_kv_evict_workspace_size(batch));
+                (long long)workspace_bytes, (long long)mqa::evict_workspace(batch, max_context_len));
   mqa::EvictParams p{};
   for (int i = 0; i < num_pools; ++i) {
     if (!pools[i].data || pools[i].token_bytes < 1)
@@ -983,9 +984,7 @@ mqa_status paged_kv_evict(const float* weights, int64_t weights_stride, const in
   p.kept_stride = kept_stride;
   p.freed = freed_blocks;
   p.counts = counts;
-  p.plan = static_cast<mqa::EvictPlan*>(workspace);
-  p.k_start = reinterpret_cast<int32_t*>(p.plan + batch);
-  p.k_end = p.k_start + batch;
+  p.workspace = workspace;
   p.batch = batch;
   p.num_free = num_free;
   p.num_blocks = num_blocks;

@@ -194,15 +194,15 @@ struct Piece {
   }
 
   __device__ __forceinline__ bool find(const ChunkParams& p, int worker, int64_t* sums, int64_t* found) {
-    int64_t all = 0, part;
+    int64_t all = 0, part, mine = 0, before = 0;
+    const auto weigh = [&](int i) {
+      if (i >= p.batch) return (int64_t)0;
+      const Seq s = Seq::of<false>(p, i);
+      return s.before(p, s.tiles);
+    };
     for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
-      const int i = b0 + threadIdx.x;
-      int64_t mine = 0;
-      if (i < p.batch) {
-        const Seq s = Seq::of<false>(p, i);
-        mine = s.before(p, s.tiles);
-      }
-      scan(mine, sums, part);
+      mine = weigh(b0 + threadIdx.x);
+      before = scan(mine, sums, part);
       all += part;
     }
     all = uniform(all);
@@ -217,15 +217,14 @@ struct Piece {
     const int64_t want = begin - member * all;
     int64_t base = 0;
     for (int b0 = 0; base <= want; b0 += kThreads) {
-      const int i = b0 + threadIdx.x;
-      int64_t mine = 0;
-      if (i < p.batch) {
-        const Seq s = Seq::of<false>(p, i);
-        mine = s.before(p, s.tiles);
+      // (up to 512 sequences: as they are)
+      if (p.batch > kThreads) {
+        mine = weigh(b0 + threadIdx.x);
+        before = scan(mine, sums, part);
       }
-      const int64_t here = base + scan(mine, sums, part);
+      const int64_t here = base + before;
       if (here <= want && want < here + mine) {
-        found[0] = i;
+        found[0] = b0 + threadIdx.x;
         found[1] = here;
       }
       base += part;

@@ -218,9 +218,10 @@ struct EvictParams {
   int64_t kept_stride;
   int32_t* freed;            // [batch * blocks of max_ctx]
   int32_t* counts;           // [2] blocks taken, blocks freed
-  int32_t* k_start;          // [batch]
+  void* workspace;
+  EvictPlan* plan;           // [batch], in the workspace
+  int32_t* k_start;          // [batch] where the choice is made, in the workspace
   int32_t* k_end;            // [batch]
-  EvictPlan* plan;           // [batch]
   int32_t batch, num_free, num_blocks, bs_shift, max_ctx, keep, recent, num_pools;
   EvictPool pools[kEvictPools];
 };
@@ -252,7 +253,8 @@ struct SlotParams {
 hipError_t launch_attention(int d, int f16, const AttnParams& p, hipStream_t s);
 hipError_t launch_chunk(int d, int f16, const ChunkParams& p, hipStream_t s);
 hipError_t launch_weights(int d, int f16, const WeightParams& p, hipStream_t s);
-hipError_t launch_evict(const EvictParams& p, hipStream_t s);
+int64_t evict_workspace(int32_t batch, int32_t max_ctx);
+hipError_t launch_evict(EvictParams p, hipStream_t s);
 hipError_t launch_kv_write(int fmt, int d, int in_type, const WriteParams& p, hipStream_t s);
 hipError_t launch_kv_slots(const SlotParams& p, hipStream_t s);
 hipError_t launch_topk(int in_type, const TopkParams& p, hipStream_t s);

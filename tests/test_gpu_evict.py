@@ -92,6 +92,25 @@ def test_long():
     check(case([9000, 20, 5000], 1030, 100, 64, "mqa", seed=2))
 
 
+@pytest.mark.parametrize("keep,recent", [(16000, 1000), (1, 0), (40000, 39999), (300, 300), (30000, 5)])
+def test_long_rows(keep, recent):
+    """Rows beyond what one workgroup selects from."""
+    check(case([40960, 33000, 9000, 40000], keep, recent, 64, "one", seed=keep))
+
+
+def test_long_rows_of_equal_and_unusual_weights():
+    c = case([50000] * 7 + [100], 20000, 50, 64, "one", seed=6)
+    w, n = c["weights"], 50000
+    w[0] = 1.0
+    w[1, ::2], w[1, 1::2] = np.inf, -0.0
+    w[2, :40000] = -np.inf                   # fewer than keep can stay
+    w[3] = -np.inf                           # the recent ones alone
+    w[4, 5::3000] = np.nan
+    w[5] = np.random.default_rng(1).integers(0, 2 ** 32, w.shape[1], dtype=np.uint32).view(np.float32)
+    w[6] = np.float32(1.0) + np.arange(w.shape[1], dtype=np.float32) % 3 * np.float32(2.0 ** -23)
+    check(c)
+
+
 def test_limits_of_lengths():
     check(case([900, -4, 40], 64, 20, 16, max_ctx=600, seed=3))
     check(case([10, 20], 300, 20, 16, seed=3))                  # keep beyond every sequence
@@ -138,7 +157,7 @@ def test_again_and_given_outputs():
     i32 = dict(dtype=torch.int32, device="cuda")
     out = (torch.empty(3, **i32), torch.full((3, 20), 9, **i32), torch.full((3, 210), 9.0, device="cuda"),
            torch.full((3, 50), 9, **i32), torch.empty(3 * 13, **i32), torch.empty(2, **i32))
-    ws = torch.empty(mq.paged_kv_evict_workspace_size(3), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(mq.paged_kv_evict_workspace_size(3, c["max_context_len"]), dtype=torch.uint8, device="cuda")
     again = mq.paged_kv_evict(**args, out=out, workspace=ws)
     for name, a, b in zip(NAMES, got, again):
         b = b[:, :a.shape[1]] if a.dim() == 2 else b
