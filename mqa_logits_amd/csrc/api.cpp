@@ -320,23 +320,34 @@ mqa_status check_chunk_cache(mqa_dtype dt, const void* q, mqa_float q_type, int6
 // KV heads that the four waves of a workgroup take beside each other.
 int32_t weight_heads(int32_t hkv) { return hkv >= 4 ? 4 : hkv == 2 ? 2 : 1; }
 
-// A weights call's split.  Usual sequences of more than 32 rows a KV head: 256
-// keys a workgroup (blocks 0).  Others: blocks of 64 keys that a wave takes one after the
-// other (what it reads of the rows then serves them all), as many as leave eight
-// workgroups for each compute unit.  Where the keys give fewer, parts that the rows
-// are cut into, as far as there are enough of them.
+// A weights call's division.  Workers, as many as the chip holds workgroups, share the
+// blocks of 64 keys; where those give a worker less than sixteen, the rows are cut up
+// too (wide: usual sequences of more than 32 rows a KV head).
 struct WeightPlan {
-  int32_t heads, blocks, splits;
+  int32_t wide, heads, workers, apart, splits, fixed;
 };
 WeightPlan plan_weights(int32_t batch, int32_t tokens, int32_t hq, int32_t hkv, int32_t max_context_len) {
   WeightPlan a{};
   const int64_t rows = ((int64_t)tokens * (hq / hkv) + batch - 1) / batch;   // of a usual sequence and KV head
-  const bool many = rows > 32;
-  a.heads = many ? 1 : weight_heads(hkv);
-  const int64_t keys = 256 / a.heads, groups = (int64_t)batch * ((max_context_len + keys - 1) / keys);
-  a.blocks = many ? 0 : (int32_t)std::clamp<int64_t>(groups / 2048, 1, mqa::kWeightBlocks);
-  const int64_t most = many ? (rows + 63) / 64 * hkv / 4 : 1;
-  a.splits = (int32_t)std::clamp<int64_t>(std::min<int64_t>(1536 / std::max<int64_t>(groups, 1), most), 1, 64);
+  const int64_t blocks = std::max<int64_t>((int64_t)batch * ((max_context_len + 63) / 64), 1);
+  a.wide = rows > 32;
+  a.heads = a.wide ? 1 : weight_heads(hkv);
+  a.splits = 1;
+  const int64_t slots = 512;
+  if (a.wide) {
+    const int64_t units = (rows + 255) / 256 * hkv;   // (a few rows' heads share one: fewer)
+    a.splits = (int32_t)std::clamp<int64_t>(std::min(slots * 16 / blocks, units), 1, 64);
+  }
+  a.workers = (int32_t)std::clamp<int64_t>(blocks * a.heads / 4, 1, slots / a.splits);
+  a.fixed = a.wide ? 32 : 96;
+  // Little work: a workgroup for each handful of blocks of a sequence, which needs not
+  // find out what its share is.
+  const int32_t handful = 4 / a.heads;
+  const int64_t direct = batch * (((int64_t)max_context_len + 64 * handful - 1) / (64 * handful));
+  if (!a.wide && direct <= 1024) {
+    a.apart = handful;
+    a.workers = (int32_t)std::max<int64_t>(direct, batch);
+  }
   return a;
 }
 
@@ -897,13 +908,16 @@ mqa_status paged_attention_weights(mqa_dtype dt, const void* q, mqa_float q_type
   p.bs_shift = block_shift(block_size);
   p.max_ctx = max_context_len;
   p.splits = splits;
+  p.wide = a.wide;
+  p.workers = a.workers;
+  p.apart = a.apart;
   p.heads_beside = a.heads;
-  p.blocks = a.blocks;
+  p.fixed = a.fixed;
   p.negate = scale < 0.f;
   p.c2 = positive_c2(scale);
   if (debug_enabled())
-    fprintf(stderr, "[mqa_logits] %s Hq=%d Hkv=%d D=%d batch=%d tokens=%d bs=%d blocks=%d splits=%d\n", who, hq, hkv, d,
-            batch, tokens, block_size, a.blocks, splits);
+    fprintf(stderr, "[mqa_logits] %s Hq=%d Hkv=%d D=%d batch=%d tokens=%d bs=%d wide=%d workers=%d splits=%d\n", who, hq, hkv,
+            d, batch, tokens, block_size, a.wide, a.workers, splits);
   return hip_status(mqa::launch_weights(d, q_type == MQA_F16, p, stream), who);
 }
 

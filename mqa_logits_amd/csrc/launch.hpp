@@ -160,7 +160,7 @@ struct ChunkParams {
 };
 
 // Blocks of 64 keys that a wave of the weights kernel takes at most.
-constexpr int kWeightBlocks = 8;
+
 
 struct WeightParams {
   const uint16_t* q;         // [tokens, Hq, D] bf16 or fp16 bits
@@ -180,9 +180,12 @@ struct WeightParams {
   int32_t batch, tokens, next_n;
   int32_t kv_heads, group;
   int32_t num_blocks, bs_shift, max_ctx;
-  int32_t splits;            // of the rows of a sequence
-  int32_t heads_beside;      // KV heads that waves of a workgroup take beside each other
-  int32_t blocks;            // of 64 keys that a wave takes, one after the other (0: many rows)
+  int32_t wide;              // many rows a KV head
+  int32_t workers;           // among which the keys are divided
+  int32_t apart;             // blocks of 64 keys of one sequence for a worker (0: equal shares of all)
+  int32_t splits;            // among which the rows of a sequence are (wide)
+  int32_t heads_beside;      // KV heads that waves of a workgroup take beside each other (not wide)
+  int32_t fixed;             // a block of keys costs as much as this many rows' products, besides theirs
   int32_t negate;
   float c2;
 };

@@ -23,6 +23,8 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
+constexpr int kFewResident = 2;              // workgroups for each CU, few rows
+constexpr int kKeys = 64;                    // of a block: a wave's at a time
 constexpr uint32_t kLastScale = 252;         // bytes above count as NaN
 constexpr uint32_t kHalfLow = 105, kHalfHigh = 136;   // scale bytes under which e2m1 is exact in fp16
 constexpr float kLog2e = 1.4426950408889634f;
@@ -44,6 +46,12 @@ __device__ __forceinline__ u32x4 cvt_eight(uint32_t w, float scale) {
   return u32x4{cvt_pair<HALF, 0>(w, scale), cvt_pair<HALF, 1>(w, scale), cvt_pair<HALF, 2>(w, scale),
                cvt_pair<HALF, 3>(w, scale)};
 }
+// x, as the compiler does not know it: what is computed from it is computed where it
+// is used, not ahead of all loops and kept (out of registers) until then.
+__device__ __forceinline__ int fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
 __device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
 
 template <bool HALF>
@@ -58,25 +66,175 @@ __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
 struct Seq {
   int64_t base;            // keys before its first new token (may be negative)
   int cap;                 // keys of the context
-  int first, n;            // its rows of q
-  __device__ __forceinline__ Seq(const WeightParams& p, int b) {
+  int first, n;            // its new tokens in q
+  int blocks;              // of 64 keys
+
+  template <bool UNIFORM>
+  __device__ __forceinline__ static Seq of(const WeightParams& p, int b) {
+    const auto load = [](const int32_t* x) { return UNIFORM ? __builtin_amdgcn_readfirstlane(*x) : *x; };
     int64_t lo = (int64_t)b * p.next_n, hi = lo + p.next_n;
     if (p.offsets) {
-      lo = __builtin_amdgcn_readfirstlane(p.offsets[b]);
-      hi = __builtin_amdgcn_readfirstlane(p.offsets[b + 1]);
+      lo = load(p.offsets + b);
+      hi = load(p.offsets + b + 1);
     }
-    const int ctx = __builtin_amdgcn_readfirstlane(p.ctx[b]);
-    cap = min(max(ctx, 0), p.max_ctx);
+    const int ctx = load(p.ctx + b);
+    Seq s;
+    s.cap = min(max(ctx, 0), p.max_ctx);
     const int64_t from = min(max(lo, (int64_t)0), (int64_t)p.tokens);
     const int64_t to = min(max(hi, from), (int64_t)p.tokens);
-    base = (int64_t)ctx - (hi - lo) + (from - lo);
-    first = (int)from;
-    n = (int)(to - from);
+    s.base = (int64_t)ctx - (hi - lo) + (from - lo);
+    s.first = (int)from;
+    s.n = (int)(to - from);
+    s.blocks = (s.cap + kKeys - 1) / kKeys;
+    return s;
   }
   __device__ __forceinline__ int seen(int t) const {
     return (int)min(max(base + 1 + t, (int64_t)0), (int64_t)cap);
   }
+  // sum over i < k of max(64 i - a, 0)
+  __device__ __forceinline__ static int64_t ramp(int64_t k, int64_t a) {
+    const int64_t j = a < 0 ? 0 : (a >> 6) + 1, m = max(k - j, (int64_t)0);
+    return kKeys * (m * (2 * j + m - 1) / 2) - a * m;
+  }
+  // What the first k blocks cost: a block costs `fixed`, and 1 for each row that
+  // sees its first key (the token at base + i sees the keys up to itself).
+  __device__ __forceinline__ int64_t cost(const WeightParams& p, int64_t k) const {
+    return k * (p.fixed + (int64_t)n * p.group) - p.group * (ramp(k, base) - ramp(k, base + n));
+  }
 };
+
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32 |
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)x));
+}
+
+// A worker's share of the blocks of all sequences, laid end to end and cut where they
+// cost the same: those that begin within [begin, end).
+struct Share {
+  int64_t begin, end, at;  // at: where sequence b begins
+  int b;                   // the sequence that `begin` lies in
+  Seq first;
+
+  // Every thread; false: nothing.
+  __device__ __forceinline__ bool find(const WeightParams& p, int worker) {
+    __shared__ int64_t sums[kWaves], found;
+    __shared__ Seq found_seq;
+    __shared__ int found_b;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int64_t mine = 0, before = 0, part = 0, all = 0;
+    Seq s;
+    const auto scan = [&](int b0) {
+      mine = 0;
+      if (b0 + (int)threadIdx.x < p.batch) {
+        s = Seq::of<false>(p, b0 + threadIdx.x);
+        mine = s.cost(p, s.blocks);
+      }
+      int64_t x = mine;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int64_t y = __shfl_up((long long)x, off);
+        if (lane >= off) x += y;
+      }
+      __syncthreads();
+      if (lane == 63) sums[wave] = x;
+      __syncthreads();
+      before = x - mine;
+      part = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) before += sums[w];
+        part += sums[w];
+      }
+    };
+    for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+      scan(b0);
+      all += part;
+    }
+    all = uniform(all);
+    // (64 bits divided by a word's worth only where they are needed)
+    const int64_t each = all >> 32 ? all / p.workers : (int64_t)((uint32_t)all / (uint32_t)p.workers);
+    const int64_t more = all - each * p.workers;
+    begin = each * worker + min((int64_t)worker, more);
+    end = begin + each + (worker < more);
+    if (begin >= end) return false;
+    int64_t base = 0;
+    for (int b0 = 0; base <= begin; b0 += kThreads) {
+      if (p.batch > kThreads) scan(b0);      // (up to 256 sequences: as they are)
+      const int64_t here = base + before;
+      if (here <= begin && begin < here + mine) {
+        found_b = b0 + threadIdx.x;
+        found = here;
+        found_seq = s;
+      }
+      base += part;
+    }
+    __syncthreads();
+    b = __builtin_amdgcn_readfirstlane(found_b);
+    at = uniform(found);
+    first.base = uniform(found_seq.base);
+    first.cap = __builtin_amdgcn_readfirstlane(found_seq.cap);
+    first.first = __builtin_amdgcn_readfirstlane(found_seq.first);
+    first.n = __builtin_amdgcn_readfirstlane(found_seq.n);
+    first.blocks = __builtin_amdgcn_readfirstlane(found_seq.blocks);
+    return true;
+  }
+  // The first of s's blocks that begins at or behind `want` (64 candidates at a time).
+  __device__ __forceinline__ int first_block(const WeightParams& p, const Seq& s, int64_t want) const {
+    int lo = 0, hi = want <= at ? 0 : s.blocks;
+    while (lo < hi) {
+      const int step = (hi - lo + 63) / 64, i = lo + (threadIdx.x & 63) * step;
+      const int n = __popcll(__ballot(i < hi && at + s.cost(p, i) < want));
+      if (n == 0) return lo;
+      hi = min(lo + n * step, hi);
+      lo += (n - 1) * step + 1;
+    }
+    return lo;
+  }
+  // For each sequence of worker's share: work(b, sequence, first block, last).
+  template <class Work>
+  __device__ __forceinline__ void each(const WeightParams& p, int worker, Work work) {
+    int from, to;
+    const bool one = p.apart > 0;            // `apart` blocks of one sequence
+    if (one) {
+      const int of = p.workers / p.batch;
+      b = worker / of;
+      first = Seq::of<true>(p, b);
+      from = (worker - b * of) * p.apart;
+      to = min(from + p.apart, first.blocks);
+    } else if (!find(p, worker)) {
+      return;
+    }
+    Seq s = first;
+    while (true) {
+      if (!one) {
+        from = first_block(p, s, begin);
+        to = first_block(p, s, end);
+      }
+      if (from < to) work(b, s, from, to);
+      if (one) break;
+      at += s.cost(p, s.blocks);
+      if (++b >= p.batch || at >= end) break;
+      s = Seq::of<true>(p, b);
+    }
+  }
+};
+
+// Columns behind the contexts: this worker's.
+__device__ __forceinline__ void clear_columns(const WeightParams& p, int worker) {
+  const int each = max(p.workers / p.batch, 1);   // workers of a sequence
+  for (int b = worker / each; b < p.batch; b += p.workers / each) {
+    const int cap = min(max(__builtin_amdgcn_readfirstlane(p.ctx[b]), 0), p.max_ctx);
+    for (int64_t j = cap + worker % each * kThreads + (int64_t)threadIdx.x; j < p.max_ctx; j += each * kThreads)
+      p.out[b * p.out_stride + j] = 0.f;
+  }
+}
+
+__device__ __forceinline__ void give(const WeightParams& p, int split, int b, int key, float x) {
+  if (p.part)
+    p.part[((int64_t)split * p.batch + b) * p.max_ctx + key] = x;
+  else
+    p.out[b * p.out_stride + key] = p.before ? p.before[b * p.before_stride + key] + x : x;
+}
 
 // A wave has 64 keys of a sequence and KV head in registers, and goes through the
 // head's rows, 32 at a time:
@@ -88,7 +246,7 @@ struct Seq {
 // The order of the contracted index is free: half l / 32 of the lanes carries the
 // D/2 elements from l / 32 * D/2 on.
 constexpr int kChunk = 256;                  // rows whose places LDS holds at a time, for a wave
-constexpr int kKeys = 64;                    // of a wave
+constexpr int kSpan = 16;                    // blocks that a wave takes before their sums are written
 
 struct __attribute__((aligned(16))) Places {
   int64_t at[kChunk];      // first element of a row's query
@@ -102,52 +260,65 @@ struct Wave {
 
   struct RawKeys {
     u32x4 x[kHalves][D / 64];
-    uint32_t s[kHalves];
+    uint32_t s[kHalves];     // the word that holds the scales
+    uint32_t at;             // D = 64: bit h, whether half h's are its upper two bytes
   };
   u32x4 k[kHalves][kSteps];
   float sum[kHalves];
 
-  // block: of the lane's key of each half
-  __device__ __forceinline__ static void fetch_keys(RawKeys& r, const WeightParams& p, const uint32_t (&block)[kHalves]) {
-    const int half = (threadIdx.x & 63) >> 5;
+  // row: (slot, head) of the lane's key of each half
+  __device__ __forceinline__ static void fetch_keys(RawKeys& r, const WeightParams& p, const uint32_t (&row)[kHalves]) {
+    const int half = fresh(threadIdx.x & 63) >> 5;
+    r.at = 0;
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
-      const uint8_t* src = p.k + ((uint64_t)block[h] << 4) + half * (D / 4);
+      const uint8_t* src = p.k + (uint64_t)row[h] * (D / 2) + half * (D / 4);
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) r.x[h][i] = *reinterpret_cast<const u32x4*>(src + i * 16);
-      const uint8_t* sf = p.k_sf + (uint64_t)block[h] + half * (D / 64);
-      r.s[h] = D == 128 ? *reinterpret_cast<const uint16_t*>(sf) : *sf;
+      // (whole words: a narrower load would be waited for where it is issued)
+      const uint64_t at = (uint64_t)row[h] * (D / 32);
+      r.s[h] = *reinterpret_cast<const uint32_t*>(p.k_sf + (at & ~(uint64_t)3));
+      if (D == 64) r.at |= (row[h] & 1) << h;
     }
   }
 
   // Whether some scale needs the wide products (fp16 queries).
-  __device__ __forceinline__ bool put_keys(const RawKeys& r) {
+  __device__ __forceinline__ bool put_keys(const RawKeys& r, uint32_t sign) {
     bool wide = false;
+    const int half = fresh(threadIdx.x & 63) >> 5;
     float s[kHalves][D / 64];
 #pragma unroll
-    for (int h = 0; h < kHalves; ++h)
+    for (int h = 0; h < kHalves; ++h) {
+      const uint32_t bytes = D == 128 ? r.s[h] >> (16 * half) : r.s[h] >> (16 * (r.at >> h & 1) + 8 * half);
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
-        const uint32_t byte = r.s[h] >> (8 * i) & 0xffu;
+        const uint32_t byte = bytes >> (8 * i) & 0xffu;
         wide |= byte - kHalfLow > kHalfHigh - kHalfLow;
         s[h][i] = scale_of(byte > kLastScale ? 255u : byte);
       }
+    }
     wide = F16 && __any(wide);
     if (F16 && !wide)
-      convert<true>(r, s);
+      convert<true>(r, s, sign);
     else
-      convert<false>(r, s);
+      convert<false>(r, s, sign);
     return wide;
   }
   template <bool HALF>
-  __device__ __forceinline__ void convert(const RawKeys& r, const float (&s)[kHalves][D / 64]) {
+  __device__ __forceinline__ void convert(const RawKeys& r, const float (&s)[kHalves][D / 64], uint32_t sign) {
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
 #pragma unroll
       for (int st = 0; st < kSteps; ++st) {
         const uint32_t word = r.x[h][st / 4][st % 4];
-        k[h][st] = cvt_eight<HALF>(word, s[h][st / 4]);
+        k[h][st] = cvt_eight<HALF>(word ^ sign, s[h][st / 4]);
       }
+  }
+  // The keys' sums over both halves' rows; lane: of key `lane`.
+  __device__ __forceinline__ float take_sums() {
+    const float a = sum[0] + __shfl_xor(sum[0], 32), b = sum[1] + __shfl_xor(sum[1], 32);
+    sum[0] = sum[1] = 0.f;
+    return (threadIdx.x & 63) < 32 ? a : b;
   }
 
   struct Tile { u32x4 q[kSteps]; };
@@ -162,7 +333,7 @@ struct Wave {
   // row may not see all of them).
   template <bool WIDE, bool MASKED, bool FULL, class Places>
   __device__ __forceinline__ void add(const Tile& x, const Places& places, int tile, int rows, int key0, float c2) {
-    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int lane = fresh(threadIdx.x & 63), half = lane >> 5;
     f32x4 shift[4];
 #pragma unroll
     for (int a = 0; a < 4; ++a) shift[a] = *reinterpret_cast<const f32x4*>(&places.shift[tile * 32 + 8 * a + 4 * half]);
@@ -233,33 +404,36 @@ struct Wave {
 template <int D, bool F16>
 struct Pending {
   f32x16 s[kKeys / 32];
-  f32x4 shift[4];
-  __device__ __forceinline__ void clear() {  // of no rows
-#pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) shift[a][i] = -__builtin_inff();
+  const float* shifts;     // of the lane's rows, in LDS: row 8 a + i at 8 a + i
+  __device__ __forceinline__ void clear(const float* none) {  // of rows that give nothing
+    shifts = none;
 #pragma unroll
     for (int h = 0; h < kKeys / 32; ++h)
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[h][i] = 0.f;
   }
-  // registers i of 16
-  __device__ __forceinline__ void form(Wave<D, F16>& w, int i, float c2) const {
+  __device__ __forceinline__ void form(Wave<D, F16>& w, float c2) const {
 #pragma unroll
-    for (int h = 0; h < kKeys / 32; ++h)
-      w.sum[h] += __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][i], c2, shift[i >> 2][i & 3]));
+    for (int a = 0; a < 4; ++a) {
+      const f32x4 shift = *reinterpret_cast<const f32x4*>(shifts + 8 * a);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < kKeys / 32; ++h)
+          w.sum[h] += __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][4 * a + i], c2, shift[i]));
+    }
   }
-  // The products of 32 rows in LDS (32 rows that give to every key), with the weights
-  // of the tile before formed between them: the matrix cores and the vector ALU
-  // work side by side.
-  __device__ __forceinline__ void multiply(Wave<D, F16>& w, const char* q, const float* shifts, const Pending& before, float c2) {
+  // The products of 32 rows in LDS (rows that give to every key, or zeros), with the
+  // weights of the tile before formed between them: the matrix cores and the vector
+  // ALU work side by side.
+  __device__ __forceinline__ void multiply(Wave<D, F16>& w, const char* q, const float* own_shifts, const Pending& before, float c2) {
     constexpr int kSteps = D / 16, kHalves = kKeys / 32, kAhead = 4;
     u32x4 a[kAhead];
+    f32x4 shift[4];
 #pragma unroll
     for (int st = 0; st < kAhead; ++st) a[st] = *reinterpret_cast<const u32x4*>(q + st * 16);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) shift[i] = *reinterpret_cast<const f32x4*>(shifts + 8 * i);
+    shift[0] = *reinterpret_cast<const f32x4*>(before.shifts);
+    shifts = own_shifts;
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
 #pragma unroll
@@ -278,6 +452,8 @@ struct Pending {
         if (st == 0) asm volatile("" ::"v"(a[0]), "v"(w.k[h][0]));   // (as in Wave::add)
         if (h == kHalves - 1 && st + kAhead < kSteps)
           a[st % kAhead] = *reinterpret_cast<const u32x4*>(q + (st + kAhead) * 16);
+        const int i = n * kEach;
+        if (i % 4 == 0 && i < 12) shift[i / 4 + 1] = *reinterpret_cast<const f32x4*>(before.shifts + 2 * i + 8);
       }
 #pragma unroll
       for (int h = 0; h < kHalves; ++h)
@@ -287,7 +463,7 @@ struct Pending {
           if (n >= 1 && n <= kSlots) y[h][e] = __builtin_amdgcn_exp2f(x[h][e]);
           if (n < kSlots) {
             const int i = n * kEach + e;
-            x[h][e] = __builtin_fmaf(before.s[h][i], c2, before.shift[i >> 2][i & 3]);
+            x[h][e] = __builtin_fmaf(before.s[h][i], c2, shift[i >> 2][i & 3]);
           }
         }
       __builtin_amdgcn_sched_barrier(0);
@@ -302,309 +478,302 @@ __device__ __forceinline__ uint32_t slot_of(const WeightParams& p, const int32_t
 }
 
 // Few rows.  Waves of a workgroup beside each other: on different KV heads (heads of them,
-// so that whole rows of the cache are read at about the same time), then on the
-// keys that follow.
+// so that whole rows of the cache are read at about the same time), then on every
+// so manieth block of keys.
 template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kFewResident)
 weights_kernel(const WeightParams p) {
   using W = Wave<D, F16>;
   constexpr int kHalves = kKeys / 32;
   __shared__ Places all_places[kWaves];
-  __shared__ float all_sums[kWaves][kWeightBlocks * kKeys];
-  __shared__ uint32_t all_slots[kWaves][kWeightBlocks * kKeys / 16];   // of every 16th key
+  __shared__ float all_sums[kWaves][kSpan * kKeys];
+  __shared__ uint32_t all_slots[kWaves][kSpan * kKeys / 16];   // of every 16th key
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int b = blockIdx.y, split = blockIdx.z;
-  const int beside = p.heads_beside, first_head = wave % beside;
-  const int wave_keys = p.blocks * kKeys, group_keys = kWaves / beside * wave_keys;   // of the workgroup
-  const int wave_key0 = blockIdx.x * group_keys + wave / beside * wave_keys;
-  const Seq s(p, b);
+  const int beside = p.heads_beside, apart = kWaves / beside, first_head = wave % beside, mine = wave / beside;
+  const uint32_t sign = p.negate ? 0x88888888u : 0u;
   Places& places = all_places[wave];
   float* const sums = all_sums[wave];
-  for (int i = lane; i < wave_keys; i += 64) sums[i] = 0.f;
-  // this split's rows of each head
-  const int64_t rows_all = (int64_t)s.n * p.group, tiles_all = (rows_all + 31) / 32;
-  const int64_t from = tiles_all * split / p.splits * 32;
-  const int64_t to = min(rows_all, tiles_all * (split + 1) / p.splits * 32);
-  const int blocks = min((s.cap - wave_key0 + kKeys - 1) / kKeys, p.blocks);
-  if (blocks > 0 && from < to) {
+  uint32_t* const slots = all_slots[wave];
+  Share share;
+  share.each(p, blockIdx.x, [&](int b, const Seq& s, int from, int to) {
     const int32_t* table = p.bt + (int64_t)b * p.bt_stride;
-    uint32_t* const slots = all_slots[wave];
-    if (lane < blocks * (kKeys / 16)) slots[lane] = slot_of(p, table, min(wave_key0 + lane * 16, s.cap - 1) & ~15);
-    __builtin_amdgcn_wave_barrier();
-    const auto fetch = [&](typename W::RawKeys& raw, int block, int head) {
-      uint32_t first[kHalves];
+    const int64_t rows_all = (int64_t)s.n * p.group;
+    for (int b0 = from; b0 < to; b0 += kSpan * apart) {
+      const int here = min(to - b0, kSpan * apart), blocks = (here - mine + apart - 1) / apart;
+      const auto key_of = [&](int block) { return (b0 + mine + block * apart) * kKeys; };
+      for (int i = lane; i < blocks * kKeys; i += 64) sums[i] = 0.f;
+      if (lane < blocks * (kKeys / 16))
+        slots[lane] = slot_of(p, table, min(key_of(lane / 4) + lane % 4 * 16, s.cap - 1) & ~15);
+      __builtin_amdgcn_wave_barrier();
+      const auto fetch = [&](typename W::RawKeys& raw, int block, int head) {
+        uint32_t row[kHalves];
+        const int key = fresh(lane) & 31;
 #pragma unroll
-      for (int h = 0; h < kHalves; ++h) {
-        const int i = block * kKeys + h * 32 + (lane & 31);
-        first[h] = ((slots[i >> 4] + (i & 15)) * p.kv_heads + head) * (D / 32);
-      }
-      W::fetch_keys(raw, p, first);
-    };
-    W w;
-    typename W::RawKeys raw;
-    typename W::Tile x;
-    fetch(raw, 0, first_head);
-    for (int head = first_head; head < p.kv_heads; head += beside) {
-      for (int64_t r0 = from; r0 < to; r0 += kChunk) {
-        const int rows = (int)min(to - r0, (int64_t)kChunk), tiles = (rows + 31) / 32;
-        __builtin_amdgcn_wave_barrier();
-        bool left_out = false;               // a row that gives nothing, whatever its scores
-        for (int i = 0; i < tiles * 32; i += 64) {
-          const int r = min(i + lane, rows - 1);
-          const int t = (int)((r0 + r) / p.group);
-          const int q_head = head * p.group + (int)(r0 + r - (int64_t)t * p.group);
-          const int64_t token = s.first + t;
-          const float lse = p.lse[token * (p.kv_heads * p.group) + q_head];
-          const bool gives = i + lane < rows && lse != -__builtin_inff();
-          left_out |= i + lane < rows && !gives;
-          places.at[i + lane] = token * p.q_stride + q_head * D;
-          places.shift[i + lane] = gives ? -lse * kLog2e : -__builtin_inff();
-          places.seen[i + lane] = gives ? s.seen(t) : 0;
+        for (int h = 0; h < kHalves; ++h) {
+          const int i = block * kKeys + h * 32 + key;
+          row[h] = (slots[i >> 4] + (i & 15)) * p.kv_heads + head;
         }
-        __builtin_amdgcn_wave_barrier();
-        const bool some_left_out = __any(left_out);
-        const int most = s.seen((int)((r0 + rows - 1) / p.group));
-        W::fetch_tile(x, p, places, 0);
-        for (int block = 0; block < blocks; ++block) {
-          const int key0 = wave_key0 + block * kKeys;
-          const bool wide = w.put_keys(raw);
-          // the next block, or the first of the next rows or the next head
-          const bool again = block + 1 == blocks, more_rows = r0 + kChunk < to;
-          fetch(raw, again ? 0 : block + 1, again && !more_rows ? min(head + beside, p.kv_heads - 1) : head);
-          if (most <= key0) continue;        // none of these rows sees it
-#pragma unroll
-          for (int h = 0; h < kHalves; ++h) w.sum[h] = 0.f;
+        W::fetch_keys(raw, p, row);
+      };
+      W w;
+      typename W::RawKeys raw;
+      typename W::Tile x;
+      if (blocks > 0 && rows_all > 0) {
+        fetch(raw, 0, first_head);
+        for (int head = first_head; head < p.kv_heads; head += beside) {
+          for (int64_t r0 = 0; r0 < rows_all; r0 += kChunk) {
+            const int rows = (int)min(rows_all - r0, (int64_t)kChunk), tiles = (rows + 31) / 32;
+            __builtin_amdgcn_wave_barrier();
+            bool left_out = false;           // a row that gives nothing, whatever its scores
+            for (int i = 0; i < tiles * 32; i += 64) {
+              const int lane = fresh(tid) & 63, r = min(i + lane, rows - 1);
+              const int t = (int)((r0 + r) / p.group);
+              const int q_head = head * p.group + (int)(r0 + r - (int64_t)t * p.group);
+              const int64_t token = s.first + t;
+              const float lse = p.lse[token * (p.kv_heads * p.group) + q_head];
+              const bool gives = i + lane < rows && lse != -__builtin_inff();
+              left_out |= i + lane < rows && !gives;
+              places.at[i + lane] = token * p.q_stride + q_head * D;
+              places.shift[i + lane] = gives ? -lse * kLog2e : -__builtin_inff();
+              places.seen[i + lane] = gives ? s.seen(t) : 0;
+            }
+            __builtin_amdgcn_wave_barrier();
+            const bool some_left_out = __any(left_out);
+            const int most = s.seen((int)((r0 + rows - 1) / p.group));
+            W::fetch_tile(x, p, places, 0);
+            for (int block = 0; block < blocks; ++block) {
+              const int key0 = key_of(block);
+              const bool wide = w.put_keys(raw, sign);
+              // the next block, or the first of the next rows or the next head
+              const bool again = block + 1 == blocks, more_rows = r0 + kChunk < rows_all;
+              fetch(raw, again ? 0 : block + 1, again && !more_rows ? min(head + beside, p.kv_heads - 1) : head);
+              if (most <= key0) continue;    // none of these rows sees it
+              w.sum[0] = w.sum[1] = 0.f;
 #pragma nounroll
-          for (int t = 0; t < tiles; ++t) {
-            if (tiles > 1) W::fetch_tile(x, p, places, t);
-            const int n = min(rows - t * 32, 32);
-            const bool masked = some_left_out || s.seen((int)((r0 + t * 32) / p.group)) < key0 + kKeys;
-            if (F16 && wide)
-              w.template add<F16, true, false>(x, places, t, n, key0, p.c2);
-            else if (masked)
-              w.template add<false, true, false>(x, places, t, n, key0, p.c2);
-            else if (n == 32)
-              w.template add<false, false, true>(x, places, t, n, key0, p.c2);
-            else
-              w.template add<false, false, false>(x, places, t, n, key0, p.c2);
-          }
-          // the two halves' rows
-#pragma unroll
-          for (int h = 0; h < kHalves; ++h) {
-            const float y = w.sum[h] + __shfl_xor(w.sum[h], 32);
-            if (lane < 32) sums[block * kKeys + h * 32 + lane] += y;
+              for (int t = 0; t < tiles; ++t) {
+                if (tiles > 1) W::fetch_tile(x, p, places, t);
+                const int n = min(rows - t * 32, 32);
+                const bool masked = some_left_out || s.seen((int)((r0 + t * 32) / p.group)) < key0 + kKeys;
+                if (F16 && wide)
+                  w.template add<F16, true, false>(x, places, t, n, key0, p.c2);
+                else if (masked)
+                  w.template add<false, true, false>(x, places, t, n, key0, p.c2);
+                else
+                  w.template add<false, false, false>(x, places, t, n, key0, p.c2);
+              }
+              sums[block * kKeys + lane] += w.take_sums();
+            }
           }
         }
       }
+      // the heads beside each other
+      __syncthreads();
+      for (int i = tid; i < here * kKeys; i += kThreads) {
+        const int key = b0 * kKeys + i, block = i / kKeys;
+        if (key >= s.cap) break;
+        float x = 0.f;
+        for (int j = 0; j < beside; ++j)
+          x += all_sums[block % apart * beside + j][block / apart * kKeys + i % kKeys];
+        give(p, 0, b, key, x);
+      }
+      __syncthreads();
     }
-  }
-  // the heads beside each other
-  __syncthreads();
-  for (int i = tid; i < group_keys; i += kThreads) {
-    const int key = blockIdx.x * group_keys + i;
-    if (key >= p.max_ctx) break;
-    float x = 0.f;
-    for (int j = 0; j < beside; ++j) x += all_sums[i / wave_keys * beside + j][i % wave_keys];
-    if (p.part)
-      p.part[((int64_t)split * p.batch + b) * p.max_ctx + key] = x;
-    else
-      p.out[b * p.out_stride + key] = key < s.cap ? (p.before ? p.before[b * p.before_stride + key] + x : x) : 0.f;
-  }
+  });
+  clear_columns(p, blockIdx.x);
 }
 
-// Many rows: 64 at a time go through LDS to the workgroup's four waves, which have
-// 64 keys each.  (Read from global memory by every wave for itself, 16 bytes of
-// each of 32 rows at a time, they kept the address unit busy for most of the time.)
-constexpr int kStageRows = 64;
+// Many rows: up to 256 lie in LDS, a part of one head's or all of a few heads'
+// (a unit), and every wave passes its blocks of keys by them, without a barrier.
+// What a span's keys gathered from one unit waits in LDS for the next.
+// (The rows read by every wave from global memory, 16 bytes of each of 32 at a time, kept
+// the address unit busy for most of the time; through LDS 64 at a time, past keys that
+// stayed, a piece cost a barrier and the rows' places again, and a workgroup of 256
+// keys was gone before it had paid for its beginning: 64 sequences of 256 rows took
+// 110 us, 256 rows past 32768 keys 186.)
+constexpr int kTiles = 8, kWideSpan = 24;
 
 template <int D>
-struct __attribute__((aligned(16))) StageRows {
+struct __attribute__((aligned(16))) Rows {
   static constexpr int kPitch = D * 2 + 16;  // bytes; free of bank conflicts
-  char q[kStageRows * kPitch];
-  float shift[kStageRows];
-  int seen[kStageRows];
-  int left_out;            // a row that gives nothing, whatever its scores
+  char q[kTiles * 32 * kPitch];
+  int64_t at[kTiles * 32];   // first element of a row's query; -1: no row
+  float shift[kTiles * 32];
+  int seen[kTiles * 32];
+  float sums[kWideSpan * kKeys];
+  uint32_t slots[kWideSpan * kKeys / 16];    // of every 16th key
+  int left_out[kWaves];    // a row that gives nothing, whatever its scores
+  float none[32];          // shifts of rows that give nothing
 };
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 2)
 weights_wide_kernel(const WeightParams p) {
   using W = Wave<D, F16>;
-  constexpr int kHalves = kKeys / 32, kGroupKeys = kWaves * kKeys;
-  constexpr int kLoads = kStageRows * D * 2 / 16 / kThreads, kRowsALoad = kThreads / 8;
-  __shared__ StageRows<D> stage[2];
-  const int tid = threadIdx.x, lane = tid & 63;
+  constexpr int kHalves = kKeys / 32, kPitch = Rows<D>::kPitch;
+  __shared__ Rows<D> x;
+  const int tid = threadIdx.x, lane = tid & 63, split = blockIdx.y;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int b = blockIdx.y, split = blockIdx.z;
-  // (the last keys first: their rows end among them, which takes longer)
-  const int group_key0 = (gridDim.x - 1 - blockIdx.x) * kGroupKeys, key0 = group_key0 + wave * kKeys;
-  const Seq s(p, b);
-  W w;
-#pragma unroll
-  for (int h = 0; h < kHalves; ++h) w.sum[h] = 0.f;
-  // this split's pieces of 64 rows, of all KV heads' end to end
-  const int rows = s.n * p.group, pieces = (rows + kStageRows - 1) / kStageRows;
-  const int64_t all = (int64_t)pieces * p.kv_heads;
-  const int64_t begin = all * split / p.splits, end = all * (split + 1) / p.splits;
-  if (group_key0 < s.cap && begin < end) {
+  const uint32_t sign = p.negate ? 0x88888888u : 0u;
+  const float* const none = x.none + 4 * (lane >> 5);
+  if (tid < 32) x.none[tid] = -__builtin_inff();   // (read behind barriers)
+  Share share;
+  share.each(p, blockIdx.x, [&](int b, const Seq& s, int from, int to) {
     const int32_t* table = p.bt + (int64_t)b * p.bt_stride;
-    uint32_t slot[kHalves];
-#pragma unroll
-    for (int h = 0; h < kHalves; ++h) {
-      const int j = min(key0 + h * 32 + (lane & 31), s.cap - 1);
-      slot[h] = slot_of(p, table, j & ~15) + (j & 15);
-    }
-    // Rows that see some of the keys follow those that do not: the first such piece.
-    const int64_t blind = min(max((int64_t)group_key0 - s.base, (int64_t)0), (int64_t)s.n);   // tokens
-    const int first_piece = (int)(blind * p.group / kStageRows);
-    int head = (int)(begin / pieces), piece = max((int)(begin - (int64_t)head * pieces), first_piece);
-    const int last_head = (int)((end - 1) / pieces), last_piece = (int)(end - 1 - (int64_t)last_head * pieces);
-    // (token, head of the group) of the rows that this thread loads, and of the one
-    // whose lse wave 0's lanes load: from piece to piece they move by 64 rows
-    const int step_t = kStageRows / p.group, step_h = kStageRows - step_t * p.group;
-    struct Row {
-      int t, h;
-    };
-    Row mine[kStageRows / kRowsALoad], of_lse, front;
-    const auto place = [&](Row& x, int r) {
-      x.t = r / p.group;
-      x.h = r - x.t * p.group;
-    };
-    const auto place_all = [&] {
-#pragma unroll
-      for (int i = 0; i < kStageRows / kRowsALoad; ++i) place(mine[i], piece * kStageRows + i * kRowsALoad + tid / 8);
-      place(of_lse, piece * kStageRows + lane);
-      place(front, piece * kStageRows);
-    };
-    const auto move = [&](Row& x) {
-      x.t += step_t;
-      x.h += step_h;
-      if (x.h >= p.group) {
-        x.h -= p.group;
-        ++x.t;
-      }
-    };
-    // whether there is a piece at (head, piece); past a head's last, the next one's first
-    bool more = true;
-    const auto settle = [&](bool moved) {
-      if (piece >= pieces) {
-        piece = first_piece;
-        ++head;
-        moved = true;
-      }
-      more = piece < pieces && (head < last_head || (head == last_head && piece <= last_piece));
-      if (more && moved) place_all();
-    };
-    settle(true);
-    u32x4 raw[kLoads];
-    float lse = 0.f;
-    int seen = 0;
-    const auto fetch = [&] {
-      constexpr int kPieces = D / 64;        // of 128 bytes of a row
-#pragma unroll
-      for (int i = 0; i < kStageRows / kRowsALoad; ++i) {
-        // (past the last row, the last token's)
-        const int64_t token = s.first + min(mine[i].t, s.n - 1);
-        const uint16_t* src = p.q + token * p.q_stride + (head * p.group + mine[i].h) * D + tid % 8 * 8;
-#pragma unroll
-        for (int j = 0; j < kPieces; ++j) raw[i * kPieces + j] = *reinterpret_cast<const u32x4*>(src + j * 64);
-      }
-      if (wave == 0) {
-        const int64_t token = s.first + min(of_lse.t, s.n - 1);
-        lse = p.lse[token * (p.kv_heads * p.group) + head * p.group + of_lse.h];
-        seen = of_lse.t < s.n ? s.seen(of_lse.t) : -1;   // (-1: no row)
-      }
-    };
-    const auto put = [&](StageRows<D>& x) {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        constexpr int kPieces = D / 64;
-        *reinterpret_cast<u32x4*>(x.q + (i / kPieces * kRowsALoad + tid / 8) * StageRows<D>::kPitch +
-                                  (i % kPieces * 8 + tid % 8) * 16) = raw[i];
-      }
-      if (wave == 0) {
-        const bool gives = seen >= 0 && lse != -__builtin_inff();
-        x.shift[lane] = gives ? -lse * kLog2e : -__builtin_inff();
-        x.seen[lane] = gives ? seen : 0;
-        const bool left_out = __any(seen >= 0 && !gives);
-        if (lane == 0) x.left_out = left_out;
-      }
-    };
-    if (more) fetch();
-    int buffer = 0, have = -1;
-    bool wide = false;
-    Pending<D, F16> pending[2];
-    pending[1].clear();
-    const auto finish = [&] {
-      // (nothing of it belongs ahead of the branch, where multiply's own would follow it)
-#pragma unroll
-      for (int h = 0; h < kHalves; ++h) asm volatile("" : "+v"(pending[1].s[h]));
-#pragma unroll
-      for (int i = 0; i < 16; ++i) pending[1].form(w, i, p.c2);
-    };
-    while (more) {
-      if (head != have) {
-        have = head;
-        uint32_t first[kHalves];
-#pragma unroll
-        for (int h = 0; h < kHalves; ++h) first[h] = (slot[h] * p.kv_heads + head) * (D / 32);
-        typename W::RawKeys keys;
-        W::fetch_keys(keys, p, first);
-        wide = w.put_keys(keys);
-      }
-      StageRows<D>& x = stage[buffer];
-      put(x);
-      const int n = min(rows - piece * kStageRows, kStageRows), front_seen = s.seen(front.t);
-      ++piece;
-#pragma unroll
-      for (int i = 0; i < kStageRows / kRowsALoad; ++i) move(mine[i]);
-      move(of_lse);
-      move(front);
-      settle(false);
-      if (more) fetch();
-      __syncthreads();
-      // (one barrier a piece: before the buffer is written again, every wave has
-      // passed the next piece's)
-      buffer ^= 1;
-      const bool masked = x.left_out || front_seen < key0 + kKeys;
-      if (!masked && n == kStageRows && !(F16 && wide)) {
-        const char* q = x.q + (lane & 31) * StageRows<D>::kPitch + (lane >> 5) * D;
-        const float* shifts = x.shift + 4 * (lane >> 5);
-        pending[0].multiply(w, q, shifts, pending[1], p.c2);
-        pending[1].multiply(w, q + 32 * StageRows<D>::kPitch, shifts + 32, pending[0], p.c2);
+    const int rows = s.n * p.group;          // of a head
+    const int tiles_all = (rows + 31) / 32, heads = max(min(kTiles / max(tiles_all, 1), p.kv_heads), 1);   // of a unit
+    const int groups = (p.kv_heads + heads - 1) / heads, units = (tiles_all + kTiles - 1) / kTiles * groups;
+    for (int b0 = from; b0 < to; b0 += kWideSpan) {
+      const int here = min(to - b0, kWideSpan), key_base = b0 * kKeys;
+      if (split >= units) {
+        for (int i = tid; i < here * kKeys && key_base + i < s.cap; i += kThreads) give(p, split, b, key_base + i, 0.f);
         continue;
       }
-      finish();
-      pending[1].clear();
+      __syncthreads();
+      if (tid < here * (kKeys / 16)) x.slots[tid] = slot_of(p, table, min(key_base + tid * 16, s.cap - 1) & ~15);
+      W w;
+      typename W::RawKeys raw;
+      Pending<D, F16> pending[2];
+      w.sum[0] = w.sum[1] = 0.f;
+      for (int unit = split; unit < units; unit += p.splits) {
+        const int part = unit / groups, head0 = (unit - part * groups) * heads;
+        const int r0 = part * kTiles * 32, n = min(rows - r0, kTiles * 32), tiles = (n + 31) / 32;
+        const int n_heads = min(heads, p.kv_heads - head0);
+        const bool first_unit = unit == split, last_unit = unit + p.splits >= units;
+        const auto fetch = [&](int block, int head) {
+          uint32_t row[kHalves];
+          const int key = fresh(lane) & 31;
 #pragma unroll
-      for (int t = 0; t < kStageRows / 32; ++t) {
-        if (t * 32 >= n) break;
-        const char* q = x.q + (t * 32 + (lane & 31)) * StageRows<D>::kPitch + (lane >> 5) * D;
-        typename W::Tile tile;
+          for (int h = 0; h < kHalves; ++h) {
+            const int i = block * kKeys + h * 32 + key;
+            row[h] = (x.slots[i >> 4] + (i & 15)) * p.kv_heads + head;
+          }
+          W::fetch_keys(raw, p, row);
+        };
+        __syncthreads();                     // (the rows before are done with, the slots are there)
+        if (first_unit && wave < here) fetch(wave, head0);
+        {
+          const int tid = fresh(threadIdx.x), head = tid / 32 / tiles, r = tid - head * tiles * 32, t = (r0 + r) / p.group;
+          const bool is = head < n_heads && r < n;
+          float lse = 0.f;
+          int64_t at = -1;
+          if (is) {
+            const int q_head = (head0 + head) * p.group + (r0 + r - t * p.group);
+            lse = p.lse[(int64_t)(s.first + t) * (p.kv_heads * p.group) + q_head];
+            at = (s.first + t) * p.q_stride + q_head * D;
+          }
+          const bool gives = is && lse != -__builtin_inff();
+          x.at[tid] = at;
+          x.shift[tid] = gives ? -lse * kLog2e : -__builtin_inff();
+          x.seen[tid] = gives ? s.seen(t) : 0;
+          const bool left_out = __any(is && !gives);
+          if (lane == 0) x.left_out[wave] = left_out;
+        }
+        __syncthreads();
+        // (rows that are none: zeros, whose weight is 0)
+        constexpr int kPieces = D / 8, kPass = kThreads / kPieces, kLoads = 8;
+        const int tid = fresh(threadIdx.x);
+        for (int i = tid / kPieces; i < n_heads * tiles * 32; i += kPass * kLoads) {
+          u32x4 piece[kLoads];
 #pragma unroll
-        for (int st = 0; st < D / 16; ++st) tile.q[st] = *reinterpret_cast<const u32x4*>(q + st * 16);
-        if (F16 && wide)
-          w.template add<F16, true, false>(tile, x, t, n - t * 32, key0, p.c2);
-        else if (masked)
-          w.template add<false, true, false>(tile, x, t, n - t * 32, key0, p.c2);
-        else
-          w.template add<false, false, false>(tile, x, t, n - t * 32, key0, p.c2);
+          for (int j = 0; j < kLoads; ++j) {
+            const int row = i + j * kPass;
+            const int64_t at = row < kTiles * 32 ? x.at[row] : -1;
+            piece[j] = u32x4{0, 0, 0, 0};
+            if (at >= 0) piece[j] = *reinterpret_cast<const u32x4*>(p.q + at + tid % kPieces * 8);
+          }
+#pragma unroll
+          for (int j = 0; j < kLoads; ++j)
+            if (i + j * kPass < kTiles * 32)
+              *reinterpret_cast<u32x4*>(x.q + (i + j * kPass) * kPitch + tid % kPieces * 16) = piece[j];
+        }
+        __syncthreads();
+        const bool left_out = x.left_out[0] || x.left_out[1] || x.left_out[2] || x.left_out[3];
+        const int clear_to = left_out ? 0 : s.seen(r0 / p.group);        // keys that every row sees
+        const int most = s.seen((r0 + n - 1) / p.group);
+        int owed = -1;                       // block whose last tile is pending
+        const auto flush = [&](int block) {
+          const int i = block * kKeys + fresh(lane);
+          float y = w.take_sums();
+          if (!first_unit) y += x.sums[i];
+          if (!last_unit)
+            x.sums[i] = y;
+          else if (key_base + i < s.cap)
+            give(p, split, b, key_base + i, y);
+        };
+        const auto drain = [&] {
+          // (nothing of it belongs ahead of the branch, where multiply's own would follow it)
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) asm volatile("" : "+v"(pending[1].s[h]));
+          pending[1].form(w, p.c2);
+          if (owed >= 0) flush(owed);
+          owed = -1;
+        };
+        pending[1].clear(none);
+        for (int block = wave; block < here; block += kWaves) {
+          const int key0 = key_base + block * kKeys;
+          bool open = false;                 // the pending tile is this block's
+          for (int head = 0; head < n_heads; ++head) {
+            const bool wide = w.put_keys(raw, sign);
+            if (head + 1 < n_heads)
+              fetch(block, head0 + head + 1);
+            else if (block + kWaves < here)
+              fetch(block + kWaves, head0);
+            else if (!last_unit)
+              fetch(wave, ((unit + p.splits) % groups) * heads);
+            if (most <= key0) continue;
+            const int tile0 = head * tiles;
+            if (key0 + kKeys <= clear_to && !(F16 && wide)) {
+              const int of = fresh(lane);
+              const char* q = x.q + (tile0 * 32 + (of & 31)) * kPitch + (of >> 5) * D;
+              const float* shifts = x.shift + tile0 * 32 + 4 * (of >> 5);
+              for (int t = 0; t + 1 < tiles; t += 2) {
+                pending[0].multiply(w, q, shifts, pending[1], p.c2);
+                if (owed >= 0) flush(owed);
+                owed = -1;
+                pending[1].multiply(w, q + 32 * kPitch, shifts + 32, pending[0], p.c2);
+                q += 64 * kPitch;
+                shifts += 64;
+              }
+              if (tiles & 1) {
+                pending[0].multiply(w, q, shifts, pending[1], p.c2);
+                if (owed >= 0) flush(owed);
+                owed = -1;
+                pending[1] = pending[0];
+              }
+              open = true;
+              continue;
+            }
+            drain();
+            open = false;
+            for (int t = 0; t < tiles; ++t) {
+              const int of = fresh(lane);
+              const char* q = x.q + ((tile0 + t) * 32 + (of & 31)) * kPitch + (of >> 5) * D;
+              typename W::Tile tile;
+#pragma unroll
+              for (int st = 0; st < D / 16; ++st) tile.q[st] = *reinterpret_cast<const u32x4*>(q + st * 16);
+              if (F16 && wide)
+                w.template add<F16, true, false>(tile, x, tile0 + t, n - t * 32, key0, p.c2);
+              else
+                w.template add<false, true, false>(tile, x, tile0 + t, n - t * 32, key0, p.c2);
+            }
+            pending[1].clear(none);
+          }
+          if (open)
+            owed = block;
+          else {
+            if (owed >= 0) {
+              drain();
+              pending[1].clear(none);
+            }
+            flush(block);
+          }
+        }
+        if (owed >= 0) drain();
       }
     }
-    finish();
-  }
-  // the two halves' rows
-#pragma unroll
-  for (int h = 0; h < kHalves; ++h) {
-    const float x = w.sum[h] + __shfl_xor(w.sum[h], 32);
-    const int key = key0 + h * 32 + lane;
-    if (lane >= 32 || key >= p.max_ctx) continue;
-    if (p.part)
-      p.part[((int64_t)split * p.batch + b) * p.max_ctx + key] = x;
-    else
-      p.out[b * p.out_stride + key] = key < s.cap ? (p.before ? p.before[b * p.before_stride + key] + x : x) : 0.f;
-  }
+  });
+  if (!p.part) clear_columns(p, blockIdx.x);
 }
 
 // Adds the splits' sums, in their order.
@@ -623,13 +792,10 @@ weights_join_kernel(const WeightParams p) {
 
 template <int D, bool F16>
 hipError_t launch(const WeightParams& p, hipStream_t s) {
-  if (p.blocks == 0) {
-    constexpr int keys = kWaves * kKeys;
-    weights_wide_kernel<D, F16><<<dim3((p.max_ctx + keys - 1) / keys, p.batch, p.splits), kThreads, 0, s>>>(p);
-  } else {
-    const int keys = kWaves / p.heads_beside * kKeys * p.blocks;
-    weights_kernel<D, F16><<<dim3((p.max_ctx + keys - 1) / keys, p.batch, p.splits), kThreads, 0, s>>>(p);
-  }
+  if (p.wide)
+    weights_wide_kernel<D, F16><<<dim3(p.workers, p.splits), kThreads, 0, s>>>(p);
+  else
+    weights_kernel<D, F16><<<p.workers, kThreads, 0, s>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.part) return e;
   weights_join_kernel<<<dim3((p.max_ctx + 255) / 256, p.batch), 256, 0, s>>>(p);
