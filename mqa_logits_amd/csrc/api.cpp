@@ -324,7 +324,7 @@ int32_t weight_heads(int32_t hkv) { return hkv >= 4 ? 4 : hkv == 2 ? 2 : 1; }
 // blocks of 64 keys; where those give a worker less than sixteen, the rows are cut up
 // too (wide: usual sequences of more than 32 rows a KV head).
 struct WeightPlan {
-  int32_t wide, heads, workers, apart, splits, fixed;
+  int32_t wide, heads, workers, apart, splits, fixed, start;
 };
 WeightPlan plan_weights(int32_t batch, int32_t tokens, int32_t hq, int32_t hkv, int32_t max_context_len) {
   WeightPlan a{};
@@ -334,12 +334,15 @@ WeightPlan plan_weights(int32_t batch, int32_t tokens, int32_t hq, int32_t hkv, 
   a.heads = a.wide ? 1 : weight_heads(hkv);
   a.splits = 1;
   const int64_t slots = 512;
+  // parts of 256 rows that a worker goes through, of one head or of a few
+  const int64_t tiles = std::max<int64_t>((rows + 31) / 32, 1), beside = std::max<int64_t>(8 / tiles, 1);
+  const int64_t units = tiles > 8 ? (tiles + 7) / 8 * hkv : (hkv + beside - 1) / beside;
   if (a.wide) {
-    const int64_t units = (rows + 255) / 256 * hkv;   // (a few rows' heads share one: fewer)
     a.splits = (int32_t)std::clamp<int64_t>(std::min(slots * 16 / blocks, units), 1, 64);
   }
   a.workers = (int32_t)std::clamp<int64_t>(blocks * a.heads / 4, 1, slots / a.splits);
   a.fixed = a.wide ? 32 : 96;
+  a.start = (int32_t)std::min<int64_t>(a.wide ? 1800 * units / hkv : 1200 / hkv, 1 << 20);
   // Little work: a workgroup for each handful of blocks of a sequence, which needs not
   // find out what its share is.
   const int32_t handful = 4 / a.heads;
@@ -913,6 +916,7 @@ mqa_status paged_attention_weights(mqa_dtype dt, const void* q, mqa_float q_type
   p.apart = a.apart;
   p.heads_beside = a.heads;
   p.fixed = a.fixed;
+  p.start = a.start;
   p.negate = scale < 0.f;
   p.c2 = positive_c2(scale);
   if (debug_enabled())

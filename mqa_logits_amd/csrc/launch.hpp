@@ -185,7 +185,8 @@ struct WeightParams {
   int32_t apart;             // blocks of 64 keys of one sequence for a worker (0: equal shares of all)
   int32_t splits;            // among which the rows of a sequence are (wide)
   int32_t heads_beside;      // KV heads that waves of a workgroup take beside each other (not wide)
-  int32_t fixed;             // a block of keys costs as much as this many rows' products, besides theirs
+  int32_t fixed;             // a block of keys costs as much as this many rows' products, besides theirs,
+  int32_t start;             // and the beginning of a sequence as this many
   int32_t negate;
   float c2;
 };

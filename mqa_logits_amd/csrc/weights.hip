@@ -97,9 +97,10 @@ struct Seq {
     return kKeys * (m * (2 * j + m - 1) / 2) - a * m;
   }
   // What the first k blocks cost: a block costs `fixed`, and 1 for each row that
-  // sees its first key (the token at base + i sees the keys up to itself).
+  // sees its first key (the token at base + i sees the keys up to itself); the first one
+  // `start` more, which is what a worker pays that goes on to the sequence.
   __device__ __forceinline__ int64_t cost(const WeightParams& p, int64_t k) const {
-    return k * (p.fixed + (int64_t)n * p.group) - p.group * (ramp(k, base) - ramp(k, base + n));
+    return (k > 0 ? p.start : 0) + k * (p.fixed + (int64_t)n * p.group) - p.group * (ramp(k, base) - ramp(k, base + n));
   }
 };
 
@@ -178,9 +179,17 @@ struct Share {
     first.blocks = __builtin_amdgcn_readfirstlane(found_seq.blocks);
     return true;
   }
-  // The first of s's blocks that begins at or behind `want` (64 candidates at a time).
+  // The first of s's blocks that begins at or behind `want` (searched for: 64
+  // candidates at a time).
   __device__ __forceinline__ int first_block(const WeightParams& p, const Seq& s, int64_t want) const {
-    int lo = 0, hi = want <= at ? 0 : s.blocks;
+    if (want <= at) return 0;
+    int lo = 0, hi = s.blocks;
+    // (as long as every row sees a block's first key: a division)
+    const int64_t each = p.fixed + (int64_t)s.n * p.group;
+    if (each >> 31 == 0 && (want - at) >> 31 == 0) {
+      const uint32_t i = want - at <= p.start ? 1 : ((uint32_t)(want - at - p.start) - 1) / (uint32_t)each + 1;
+      if (i < (uint32_t)hi && (int64_t)i * kKeys <= s.base) return (int)i;
+    }
     while (lo < hi) {
       const int step = (hi - lo + 63) / 64, i = lo + (threadIdx.x & 63) * step;
       const int n = __popcll(__ballot(i < hi && at + s.cost(p, i) < want));
@@ -229,11 +238,13 @@ __device__ __forceinline__ void clear_columns(const WeightParams& p, int worker)
   }
 }
 
+// BEFORE: x lacks what the key had.
+template <bool BEFORE = true>
 __device__ __forceinline__ void give(const WeightParams& p, int split, int b, int key, float x) {
   if (p.part)
     p.part[((int64_t)split * p.batch + b) * p.max_ctx + key] = x;
   else
-    p.out[b * p.out_stride + key] = p.before ? p.before[b * p.before_stride + key] + x : x;
+    p.out[b * p.out_stride + key] = BEFORE && p.before ? p.before[b * p.before_stride + key] + x : x;
 }
 
 // A wave has 64 keys of a sequence and KV head in registers, and goes through the
@@ -471,10 +482,13 @@ struct Pending {
   }
 };
 
-// Pool slot of key j, the first of 16 of a block (the 16 have slots in a row).
-__device__ __forceinline__ uint32_t slot_of(const WeightParams& p, const int32_t* table, int j) {
-  const int id = min(max(table[j >> p.bs_shift], 0), p.num_blocks - 1);
-  return ((uint32_t)id << p.bs_shift) + (j & (1 << p.bs_shift) - 1);
+// Pool slot of key j, whose block is `id`.
+__device__ __forceinline__ uint32_t slot_of(const WeightParams& p, int id, int j) {
+  return ((uint32_t)min(max(id, 0), p.num_blocks - 1) << p.bs_shift) + (j & (1 << p.bs_shift) - 1);
+}
+
+__device__ __forceinline__ uint32_t slot_at(const WeightParams& p, const int32_t* table, int j) {
+  return slot_of(p, table[j >> p.bs_shift], j);
 }
 
 // Few rows.  Waves of a workgroup beside each other: on different KV heads (heads of them,
@@ -504,7 +518,7 @@ weights_kernel(const WeightParams p) {
       const auto key_of = [&](int block) { return (b0 + mine + block * apart) * kKeys; };
       for (int i = lane; i < blocks * kKeys; i += 64) sums[i] = 0.f;
       if (lane < blocks * (kKeys / 16))
-        slots[lane] = slot_of(p, table, min(key_of(lane / 4) + lane % 4 * 16, s.cap - 1) & ~15);
+        slots[lane] = slot_at(p, table, min(key_of(lane / 4) + lane % 4 * 16, s.cap - 1) & ~15);
       __builtin_amdgcn_wave_barrier();
       const auto fetch = [&](typename W::RawKeys& raw, int block, int head) {
         uint32_t row[kHalves];
@@ -591,17 +605,15 @@ weights_kernel(const WeightParams p) {
 // stayed, a piece cost a barrier and the rows' places again, and a workgroup of 256
 // keys was gone before it had paid for its beginning: 64 sequences of 256 rows took
 // 110 us, 256 rows past 32768 keys 186.)
-constexpr int kTiles = 8, kWideSpan = 24;
+constexpr int kTiles = 8, kWideSpan = 32;
 
 template <int D>
 struct __attribute__((aligned(16))) Rows {
   static constexpr int kPitch = D * 2 + 16;  // bytes; free of bank conflicts
   char q[kTiles * 32 * kPitch];
-  int64_t at[kTiles * 32];   // first element of a row's query; -1: no row
   float shift[kTiles * 32];
   int seen[kTiles * 32];
   float sums[kWideSpan * kKeys];
-  uint32_t slots[kWideSpan * kKeys / 16];    // of every 16th key
   int left_out[kWaves];    // a row that gives nothing, whatever its scores
   float none[32];          // shifts of rows that give nothing
 };
@@ -623,16 +635,42 @@ weights_wide_kernel(const WeightParams p) {
     const int rows = s.n * p.group;          // of a head
     const int tiles_all = (rows + 31) / 32, heads = max(min(kTiles / max(tiles_all, 1), p.kv_heads), 1);   // of a unit
     const int groups = (p.kv_heads + heads - 1) / heads, units = (tiles_all + kTiles - 1) / kTiles * groups;
-    for (int b0 = from; b0 < to; b0 += kWideSpan) {
-      const int here = min(to - b0, kWideSpan), key_base = b0 * kKeys;
+    int staged = -1;                         // unit whose rows are in LDS
+    // (the sums of one unit need not wait for another's: all blocks at once)
+    const int spans = units - split > p.splits ? (to - from + kWideSpan - 1) / kWideSpan : 1;
+    for (int span = 0; span < spans; ++span) {
+      const int b0 = from + (int)((int64_t)(to - from) * span / spans);
+      const int here = from + (int)((int64_t)(to - from) * (span + 1) / spans) - b0, key_base = b0 * kKeys;
       if (split >= units) {
         for (int i = tid; i < here * kKeys && key_base + i < s.cap; i += kThreads) give(p, split, b, key_base + i, 0.f);
         continue;
       }
-      __syncthreads();
-      if (tid < here * (kKeys / 16)) x.slots[tid] = slot_of(p, table, min(key_base + tid * 16, s.cap - 1) & ~15);
       W w;
       typename W::RawKeys raw;
+      // Blocks are fetched in the order in which they are used, their entries of the
+      // table a block earlier.
+      int coming = wave;                     // block whose entries are on their way
+      int entry[kHalves];
+      uint32_t slot[kHalves];                // of the lane's keys of the block before it
+      const auto look_up = [&] {
+        const int key = (b0 + coming) * kKeys + (fresh(lane) & 31);
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) entry[h] = table[min(key + h * 32, s.cap - 1) >> p.bs_shift];
+      };
+      const auto next_block = [&] {
+        const int key = (b0 + coming) * kKeys + (fresh(lane) & 31);
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) slot[h] = slot_of(p, entry[h], min(key + h * 32, s.cap - 1));
+        coming = coming + kWaves < here ? coming + kWaves : wave;
+        look_up();
+      };
+      const auto fetch = [&](int head) {
+        uint32_t row[kHalves];
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) row[h] = slot[h] * p.kv_heads + head;
+        W::fetch_keys(raw, p, row);
+      };
+      if (wave < here) look_up();
       Pending<D, F16> pending[2];
       w.sum[0] = w.sum[1] = 0.f;
       for (int unit = split; unit < units; unit += p.splits) {
@@ -640,58 +678,61 @@ weights_wide_kernel(const WeightParams p) {
         const int r0 = part * kTiles * 32, n = min(rows - r0, kTiles * 32), tiles = (n + 31) / 32;
         const int n_heads = min(heads, p.kv_heads - head0);
         const bool first_unit = unit == split, last_unit = unit + p.splits >= units;
-        const auto fetch = [&](int block, int head) {
-          uint32_t row[kHalves];
-          const int key = fresh(lane) & 31;
-#pragma unroll
-          for (int h = 0; h < kHalves; ++h) {
-            const int i = block * kKeys + h * 32 + key;
-            row[h] = (x.slots[i >> 4] + (i & 15)) * p.kv_heads + head;
-          }
-          W::fetch_keys(raw, p, row);
-        };
-        __syncthreads();                     // (the rows before are done with, the slots are there)
-        if (first_unit && wave < here) fetch(wave, head0);
-        {
-          const int tid = fresh(threadIdx.x), head = tid / 32 / tiles, r = tid - head * tiles * 32, t = (r0 + r) / p.group;
-          const bool is = head < n_heads && r < n;
+        __syncthreads();                     // (the rows before are done with)
+        if (unit != staged) {
+          staged = unit;
+          const int tid = fresh(threadIdx.x);
+          // Quotients by products: of at most 7 by at most 8, and of less than 2^16
+          // by a group of less than 2^16 (the factors too large by less than 1).
+          const int t0 = r0 / p.group, of0 = r0 - t0 * p.group, per_tile = 63 / tiles + 1;
+          const uint32_t per_group = 0xffffffffu / (uint32_t)p.group + 1;
+          const auto place = [&](int i, int& head, int& t, int& of) {   // of the i-th row in LDS; is there one?
+            head = (i / 32 * per_tile) >> 6;
+            const int r = i - head * tiles * 32, q = p.group == 1 ? of0 + r : (int)__umulhi((uint32_t)(of0 + r), per_group);
+            t = t0 + q;
+            of = of0 + r - q * p.group;
+            return head < n_heads && r < n;
+          };
+          int head, t, of;
+          const bool is = place(tid, head, t, of);
           float lse = 0.f;
-          int64_t at = -1;
-          if (is) {
-            const int q_head = (head0 + head) * p.group + (r0 + r - t * p.group);
-            lse = p.lse[(int64_t)(s.first + t) * (p.kv_heads * p.group) + q_head];
-            at = (s.first + t) * p.q_stride + q_head * D;
-          }
-          const bool gives = is && lse != -__builtin_inff();
-          x.at[tid] = at;
-          x.shift[tid] = gives ? -lse * kLog2e : -__builtin_inff();
-          x.seen[tid] = gives ? s.seen(t) : 0;
-          const bool left_out = __any(is && !gives);
-          if (lane == 0) x.left_out[wave] = left_out;
-        }
-        __syncthreads();
-        // (rows that are none: zeros, whose weight is 0)
-        constexpr int kPieces = D / 8, kPass = kThreads / kPieces, kLoads = 8;
-        const int tid = fresh(threadIdx.x);
-        for (int i = tid / kPieces; i < n_heads * tiles * 32; i += kPass * kLoads) {
+          if (is) lse = p.lse[(int64_t)(s.first + t) * (p.kv_heads * p.group) + (head0 + head) * p.group + of];
+          const int seen = s.seen(t);
+          // (rows that are none: zeros, whose weight is 0)
+          constexpr int kPieces = D / 8, kPass = kThreads / kPieces, kLoads = kTiles * 32 / kPass;
           u32x4 piece[kLoads];
 #pragma unroll
           for (int j = 0; j < kLoads; ++j) {
-            const int row = i + j * kPass;
-            const int64_t at = row < kTiles * 32 ? x.at[row] : -1;
             piece[j] = u32x4{0, 0, 0, 0};
-            if (at >= 0) piece[j] = *reinterpret_cast<const u32x4*>(p.q + at + tid % kPieces * 8);
+            if (place(tid / kPieces + j * kPass, head, t, of))
+              piece[j] = *reinterpret_cast<const u32x4*>(p.q + (s.first + t) * p.q_stride + ((head0 + head) * p.group + of) * D + tid % kPieces * 8);
+          }
+          if (first_unit && wave < here) {
+            next_block();
+            fetch(head0);
           }
 #pragma unroll
           for (int j = 0; j < kLoads; ++j)
-            if (i + j * kPass < kTiles * 32)
-              *reinterpret_cast<u32x4*>(x.q + (i + j * kPass) * kPitch + tid % kPieces * 16) = piece[j];
+            *reinterpret_cast<u32x4*>(x.q + (tid / kPieces + j * kPass) * kPitch + tid % kPieces * 16) = piece[j];
+          const bool gives = is && lse != -__builtin_inff();
+          x.shift[tid] = gives ? -lse * kLog2e : -__builtin_inff();
+          x.seen[tid] = gives ? seen : 0;
+          const bool left_out = __any(is && !gives);
+          if (lane == 0) x.left_out[wave] = left_out;
+        } else if (first_unit && wave < here) {
+          next_block();
+          fetch(head0);
         }
         __syncthreads();
         const bool left_out = x.left_out[0] || x.left_out[1] || x.left_out[2] || x.left_out[3];
         const int clear_to = left_out ? 0 : s.seen(r0 / p.group);        // keys that every row sees
         const int most = s.seen((r0 + n - 1) / p.group);
         int owed = -1;                       // block whose last tile is pending
+        float prior = 0.f;                   // what a block's keys had before
+        const auto look = [&](int block) {
+          const int key = key_base + block * kKeys + fresh(lane);
+          if (p.before && !p.part && last_unit && key < s.cap) prior = p.before[b * p.before_stride + key];
+        };
         const auto flush = [&](int block) {
           const int i = block * kKeys + fresh(lane);
           float y = w.take_sums();
@@ -699,7 +740,7 @@ weights_wide_kernel(const WeightParams p) {
           if (!last_unit)
             x.sums[i] = y;
           else if (key_base + i < s.cap)
-            give(p, split, b, key_base + i, y);
+            give<false>(p, split, b, key_base + i, prior + y);
         };
         const auto drain = [&] {
           // (nothing of it belongs ahead of the branch, where multiply's own would follow it)
@@ -713,14 +754,25 @@ weights_wide_kernel(const WeightParams p) {
         for (int block = wave; block < here; block += kWaves) {
           const int key0 = key_base + block * kKeys;
           bool open = false;                 // the pending tile is this block's
+          if (owed >= 0) look(owed);
+          // The wave that got further gives way to the other one of its SIMD.  (Otherwise
+          // the older one is served first, and the chip is half empty at the end.)
+          if (block * 4 < here)
+            __builtin_amdgcn_s_setprio(3);
+          else if (block * 2 < here)
+            __builtin_amdgcn_s_setprio(2);
+          else if (block * 4 < here * 3)
+            __builtin_amdgcn_s_setprio(1);
+          else
+            __builtin_amdgcn_s_setprio(0);
           for (int head = 0; head < n_heads; ++head) {
             const bool wide = w.put_keys(raw, sign);
-            if (head + 1 < n_heads)
-              fetch(block, head0 + head + 1);
-            else if (block + kWaves < here)
-              fetch(block + kWaves, head0);
-            else if (!last_unit)
-              fetch(wave, ((unit + p.splits) % groups) * heads);
+            if (head + 1 < n_heads) {
+              fetch(head0 + head + 1);
+            } else if (block + kWaves < here || !last_unit) {
+              next_block();
+              fetch(block + kWaves < here ? head0 : (unit + p.splits) % groups * heads);
+            }
             if (most <= key0) continue;
             const int tile0 = head * tiles;
             if (key0 + kKeys <= clear_to && !(F16 && wide)) {
@@ -766,10 +818,14 @@ weights_wide_kernel(const WeightParams p) {
               drain();
               pending[1].clear(none);
             }
+            look(block);
             flush(block);
           }
         }
-        if (owed >= 0) drain();
+        if (owed >= 0) {
+          look(owed);
+          drain();
+        }
       }
     }
   });
@@ -777,14 +833,23 @@ weights_wide_kernel(const WeightParams p) {
 }
 
 // Adds the splits' sums, in their order.
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(64)
 weights_join_kernel(const WeightParams p) {
-  const int key = blockIdx.x * 256 + threadIdx.x, b = blockIdx.y;
+  const int key = blockIdx.x * 64 + threadIdx.x, b = blockIdx.y;
   if (key >= p.max_ctx) return;
   const int cap = min(max(p.ctx[b], 0), p.max_ctx);
   float x = 0.f;
   if (key < cap) {
-    for (int i = 0; i < p.splits; ++i) x += p.part[((int64_t)i * p.batch + b) * p.max_ctx + key];
+    const float* part = p.part + (int64_t)b * p.max_ctx + key;
+    const int64_t stride = (int64_t)p.batch * p.max_ctx;
+    constexpr int kAhead = 16;
+    for (int i = 0; i < p.splits; i += kAhead) {
+      float y[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) y[j] = part[min(i + j, p.splits - 1) * stride];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) x += i + j < p.splits ? y[j] : 0.f;
+    }
     if (p.before) x += p.before[b * p.before_stride + key];
   }
   p.out[b * p.out_stride + key] = x;
@@ -798,7 +863,7 @@ hipError_t launch(const WeightParams& p, hipStream_t s) {
     weights_kernel<D, F16><<<p.workers, kThreads, 0, s>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !p.part) return e;
-  weights_join_kernel<<<dim3((p.max_ctx + 255) / 256, p.batch), 256, 0, s>>>(p);
+  weights_join_kernel<<<dim3((p.max_ctx + 63) / 64, p.batch), 64, 0, s>>>(p);
   return hipGetLastError();
 }
 
