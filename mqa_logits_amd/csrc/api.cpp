@@ -971,6 +971,9 @@ mqa_status paged_kv_evict(const float* weights, int64_t weights_stride, const in
                         (const void*)counts})
     if (!aligned(a, 4)) return fail(MQA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
   if (!aligned(workspace, 16)) return fail(MQA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+  if (new_context_lens == context_lens || (some && (new_block_table == block_table || new_weights == weights)) ||
+      (free_blocks && freed_blocks == free_blocks))
+    return fail(MQA_ERR_INVALID_ARG, "%s: an output is an input (which is read while outputs are written)", who);
   if (weights_stride < max_context_len || new_weights_stride < max_context_len || kept_stride < keep ||
       block_table_stride < width || new_block_table_stride < width)
     return fail(MQA_ERR_INVALID_ARG, "%s: rows shorter than what they hold", who);
