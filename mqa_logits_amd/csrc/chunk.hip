@@ -695,7 +695,7 @@ struct Rows {
 // computed; K is put into LDS two steps ahead, V one.
 template <bool KEYS, int D, bool F16>
 __device__ __forceinline__ void walk(const ChunkParams& p, Rows<D, F16>& rows, Stage<D>& stage, const uint32_t* places,
-                                     int walked, int stage0, int steps, int least, int keys_left) {
+                                     int walked, int stage0, int steps, int least, int keys_left, bool negate) {
   constexpr int kHalfKeys = 32 * Stage<D>::kKeyPitch, kHalfVals = 64;   // bytes to a step's second half
   const int tid = threadIdx.x & (kThreads / 2 - 1);
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -747,18 +747,27 @@ __device__ __forceinline__ void walk(const ChunkParams& p, Rows<D, F16>& rows, S
   advance(-1);
   __syncthreads();
   f32x16 x, y;                               // scores of a step's halves
+  // (where the queries are there anyway; not a selection, which would wait for them
+  // where they are loaded)
+  if (negate) {
+#pragma unroll
+    for (int st = 0; st < D / 16; ++st) {
+      asm volatile("" : "+v"(rows.q[st]));
+      rows.q[st] ^= 0x80008000u;
+    }
+  }
   rows.multiply(x, lds, keys(0), lane);
   rows.mask(x, here_only(lane), stage0);
-  // While all rows see this step and the next.
-  const int clear = min(max(least - stage0, 0) / kKeys, steps) - 1;
+  const int clear = max(least - stage0, 0) / kKeys;      // steps that all rows see whole
   int i = 0;
   bool good = narrow(0);
   u32x4 a[Rows<D, F16>::kAhead];
 #pragma unroll
   for (int n = 0; n < Rows<D, F16>::kAhead; ++n)
     a[n] = Rows<D, F16>::key_operand(lds, Rows<D, F16>::key_at(keys(0) + kHalfKeys, lane), n);
+  // (the last step's second half is multiplied by keys of no step, for nothing)
 #pragma nounroll
-  for (; i < clear && good; ++i) {
+  for (; i < steps && good; ++i) {
     char* const into = target(i + kLead);
     const int next_v = stage.flags[i + 1 & 3][0], next_k = stage.flags[i + 1 & 3][1];
     rows.finish_and_multiply(x, y, a, lds, values(i), keys(i) + kHalfKeys, keys(i + 1), lane, c2, [&](int n) {
@@ -766,29 +775,15 @@ __device__ __forceinline__ void walk(const ChunkParams& p, Rows<D, F16>& rows, S
       if constexpr (D == 128)
         if (n == 5) put_part<D, KEYS, kHalf, 1>(raw, tid, into);
     });
+    if (__builtin_expect(i >= clear, 0)) rows.mask(y, here_only(lane), stage0 + i * kKeys + 32);
     rows.finish_and_multiply(y, x, a, lds, values(i) + kHalfVals, keys(i + 1), keys(i + 1) + kHalfKeys, lane, c2, [&](int n) {
       if (n == 1) put_part<D, KEYS, kHalf, D / 64>(raw, tid, into);
       if constexpr (D == 128)
         if (n == 5) put_part<D, KEYS, kHalf, 3>(raw, tid, into);
     });
+    if (__builtin_expect(i + 1 >= clear, 0)) rows.mask(x, here_only(lane), stage0 + (i + 1) * kKeys);
     advance(i);
     good = __builtin_amdgcn_readfirstlane(next_v) != walked + i + 1 && __builtin_amdgcn_readfirstlane(next_k) != walked + i + 1;
-    __syncthreads();
-  }
-#pragma nounroll
-  for (; i < steps && good; ++i) {
-    const int me = here_only(lane), key0 = stage0 + i * kKeys;
-    rows.multiply(y, lds, keys(i) + kHalfKeys, me);
-    rows.mask(y, me, key0 + 32);
-    rows.finish(x, lds, values(i), me, c2);
-    if (i + 1 < steps) {
-      rows.multiply(x, lds, keys(i + 1), me);
-      rows.mask(x, me, key0 + kKeys);
-    }
-    rows.finish(y, lds, values(i) + kHalfVals, me, c2);
-    put<D, KEYS, kHalf>(raw, here_only(tid), target(i + kLead));
-    advance(i);
-    good = narrow(i + 1);
     __syncthreads();
   }
   if (__builtin_expect(i == steps, 1)) return;
@@ -863,10 +858,7 @@ __device__ __forceinline__ void work(const ChunkParams& p, Piece piece, int work
       rows.seen = s.seen(token0 + at);
       const uint16_t* src = p.q + (int64_t)(s.first + token0 + at) * p.q_stride + (head0 + r - at * heads) * D + half * 8;
 #pragma unroll
-      for (int st = 0; st < D / 16; ++st) {
-        rows.q[st] = *reinterpret_cast<const u32x4*>(src + st * 16);
-        if (p.negate) rows.q[st] ^= 0x80008000u;
-      }
+      for (int st = 0; st < D / 16; ++st) rows.q[st] = *reinterpret_cast<const u32x4*>(src + st * 16);
     }
     const int32_t* table = p.bt + (int64_t)piece.b * p.bt_stride;
     const uint32_t key_blocks = p.kv_heads * (D / 32);
@@ -879,8 +871,9 @@ __device__ __forceinline__ void work(const ChunkParams& p, Piece piece, int work
         held_head = kv_head;
         held_from = held_until = stage0;
       }
-      const int until = stage0 + steps * kKeys;
-      if (held_until < until) {
+      if (held_until < stage0 + steps * kKeys) {
+        // (at once for the sequence's later tiles)
+        const int until = max(stage0 + steps * kKeys, min(s.cap, window + kStage) & -kKeys);
         for (int key = held_until + tid * 16; key < until; key += kThreads * 16) {
           const int id = min(max(table[min(key, s.cap - 1) >> p.bs_shift], 0), p.num_blocks - 1);
           const uint32_t slot = ((uint32_t)id << p.bs_shift) + (key & (1 << p.bs_shift) - 1);
@@ -889,7 +882,8 @@ __device__ __forceinline__ void work(const ChunkParams& p, Piece piece, int work
         held_until = until;
         __syncthreads();
       }
-      walk<KEYS>(p, rows, stage, places + (stage0 - window) / 16, walked, stage0, steps, least, s.cap - stage0);
+      walk<KEYS>(p, rows, stage, places + (stage0 - window) / 16, walked, stage0, steps, least, s.cap - stage0,
+                 p.negate && stage0 == begin);
       walked += steps + 4;
       stage0 = stage_end;
     }
