@@ -954,6 +954,7 @@ mqa_status paged_kv_evict(const float* weights, int64_t weights_stride, const in
     return fail(MQA_ERR_UNSUPPORTED, "%s: pool of %d blocks too large", who, num_blocks);
   if (keep < 1 || recent < 0 || recent > keep)
     return fail(MQA_ERR_INVALID_ARG, "%s: keep=%d recent=%d: keep >= 1, recent in [0, keep]", who, keep, recent);
+  if (keep > (1 << 30)) return fail(MQA_ERR_UNSUPPORTED, "%s: keep=%d over 2^30", who, keep);
   if ((int64_t)batch * max_context_len >= 0x7fffffff || (int64_t)batch * keep >= 0x7fffffff ||
       (int64_t)max_context_len * 4 >= kMaxRangeBytes)
     return fail(MQA_ERR_UNSUPPORTED, "%s: batch * max_context_len or batch * keep too large", who);

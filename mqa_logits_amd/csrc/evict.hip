@@ -12,15 +12,15 @@
 //            workgroup.  Sources are only read, so nothing depends on the order.
 //
 // Bound by the bytes: a kept token is read once and written once, a row of weights
-// read three or four times (from the L2 after the first).  Chosen tokens lie apart,
-// so what a token has in a pool costs whole cache lines: with one KV head 64 bytes of
-// K, 64 of V, 64 of the indexer's keys and three scales of 4 cost about 430 bytes of
-// reads instead of 204.
-//   3 sequences of up to 600 tokens to 128: 18 us of kernels (bound by their four
-//     launches, and by the host, 30 us a call);
-//   64 of up to 32768 to 4096, one KV head and an index: 63 us (top-k 25, move 37:
-//     4.5 TB/s of lines);
-//   one of 131072 to 16384, eight KV heads: 40 us (selection 24, move 12.5).
+// read a few times (from the L2 after the first).  Chosen tokens lie apart, so what a
+// token has in a pool costs whole cache lines: with one KV head 64 bytes of K, 64 of
+// V, 128 of the indexer's keys and three scales of 4 cost about 430 bytes of reads
+// instead of 268.
+//   64 sequences of up to 32768 tokens to 4096, one KV head and an index: 61 us
+//     (top-k 25, plan 3, move 33: 178 MB of lines at 5 TB/s);
+//   one of 131072 to 16384, eight KV heads: 42 us a call from Python, which its eight
+//     launches bound (selection 24 us on the device, plan 3, move 9);
+//   3 of up to 600 to 128: 31 us a call, the same with four (15 on the device).
 #include <hip/hip_runtime.h>
 
 #include "launch.hpp"
@@ -34,6 +34,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 constexpr int kPlanThreads = 1024;
 constexpr int kThreads = 256;
 constexpr int kChunk = 128;                  // tokens a workgroup moves at most
+constexpr int kTail = 2048;                  // columns a workgroup writes down where no token stays
 constexpr int kAhead = 4;                    // pieces a thread has in flight
 
 __device__ __forceinline__ int length(const EvictParams& p, int b) { return min(max(p.ctx[b], 0), p.max_ctx); }
@@ -373,20 +374,25 @@ __device__ __forceinline__ void copy_rows(uint8_t* data, int64_t bytes, const in
   }
 }
 
-__global__ void __launch_bounds__(kThreads) move_kernel(const EvictParams p, int chunk) {
+// movers: workgroups of `chunk` tokens each, as far as tokens stay.  Those after them
+// have kTail columns each of what is only written down: weights, table, positions.
+__global__ void __launch_bounds__(kThreads) move_kernel(const EvictParams p, int chunk, int movers) {
   __shared__ int64_t from[kChunk], to[kChunk];
   const int b = blockIdx.y, tid = threadIdx.x;
+  const bool tail = (int)blockIdx.x >= movers, records = blockIdx.z == 0;
+  if (tail && !records) return;
+  const int first = tail ? movers * chunk + (blockIdx.x - movers) * kTail : blockIdx.x * chunk;
+  const int columns = tail ? kTail : chunk;
   const EvictPlan plan = p.plan[b];
   const int n = length(p, b);
-  const bool moved = plan.chosen >= 0, records = blockIdx.z == 0;
+  const bool moved = plan.chosen >= 0;
   const int left = moved ? plan.chosen + p.recent : n;       // tokens afterwards
   const int32_t* table = p.bt + (int64_t)b * p.bt_stride;
   const int mask = (1 << p.bs_shift) - 1;
-  const int first = blockIdx.x * chunk;
   // tokens, positions and weights
   int32_t* kept = p.kept + (int64_t)b * p.kept_stride;
-  if (tid < chunk) {
-    const int i = first + tid;
+  for (int c = tid; c < columns; c += kThreads) {
+    const int i = first + c;
     int64_t src = -1, dst = -1;
     if (i < left) {
       const int at = !moved ? i : i < plan.chosen ? kept[i] : n - p.recent + (i - plan.chosen);
@@ -404,12 +410,14 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const EvictParams p, int
       if (records && i < p.max_ctx) p.new_weights[b * p.new_weights_stride + i] = 0.f;
     }
     if (records && plan.cut && !moved && i < p.keep) kept[i] = -1;
-    from[tid] = src;
-    to[tid] = dst;
+    if (!tail) {
+      from[c] = src;
+      to[c] = dst;
+    }
   }
   __syncthreads();
-  // this chunk's entries of the table, of the freed blocks
-  const int width = blocks_of(p, p.max_ctx), entry = blocks_of(p, first), entries = blocks_of(p, first + chunk) - entry;
+  // these columns' entries of the table, of the freed blocks
+  const int width = blocks_of(p, p.max_ctx), entry = blocks_of(p, first), entries = blocks_of(p, first + columns) - entry;
   if (records && tid < entries) {
     const int e = entry + tid, held = blocks_of(p, n);
     if (e < width)
@@ -421,7 +429,7 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const EvictParams p, int
   const int64_t pad = p.counts[1] + (int64_t)blockIdx.y * width + entry + tid;
   if (records && tid < entries && entry + tid < width && pad < (int64_t)p.batch * width) p.freed[pad] = -1;
   const int tokens = min(left - first, chunk);
-  if (!moved || tokens <= 0) return;
+  if (tail || !moved || tokens <= 0) return;
   for (int i = blockIdx.z; i < p.num_pools; i += gridDim.z) {
     uint8_t* data = static_cast<uint8_t*>(p.pools[i].data);
     const int64_t bytes = p.pools[i].bytes;
@@ -495,7 +503,9 @@ hipError_t launch_evict(EvictParams p, hipStream_t s) {
   int chunk = kChunk;
   while (chunk > 32 && wanted(chunk) < 512) chunk /= 2;
   const bool apart = wanted(chunk) < 1024 && p.num_pools > 1;
-  move_kernel<<<dim3((rows + chunk - 1) / chunk, p.batch, apart ? p.num_pools : 1), kThreads, 0, s>>>(p, chunk);
+  const int movers = (tokens + chunk - 1) / chunk;
+  const int tails = rows > movers * chunk ? (rows - movers * chunk + kTail - 1) / kTail : 0;
+  move_kernel<<<dim3(movers + tails, p.batch, apart ? p.num_pools : 1), kThreads, 0, s>>>(p, chunk, movers);
   return hipGetLastError();
 }
 

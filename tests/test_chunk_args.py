@@ -95,6 +95,7 @@ def test_weights_refusals(change, expect):
     (dict(batch=4096, max_ctx=1 << 19, stride=1 << 19, new_weights_stride=1 << 19, table_stride=1 << 15, new_stride=1 << 15),
      UNSUPPORTED),
     (dict(batch=4096, keep=1 << 19, kept_stride=1 << 19), UNSUPPORTED),
+    (dict(batch=1, keep=(1 << 30) + 1, kept_stride=1 << 31), UNSUPPORTED),
 ])
 def test_evict_refusals(change, expect):
     assert call(lib.paged_kv_evict, EVICT, change) == expect
