@@ -441,7 +441,7 @@ mqa_status paged_chunk_attention(mqa_dtype dt, const void* q, mqa_float q_type, 
  *   out      [batch, out_stride] fp32; it may be `weights` itself.  Columns from
  *            max_context_len on are not written
  *   workspace of at least paged_attention_weights_workspace_size bytes for the
- *            same sizes (NULL if that is 0), 16-byte aligned.
+ *            same sizes (NULL if that is 0), 16-byte aligned, as paged_attention's.
  * Scores and sums are fp32, added in an order that only the sizes decide.
  * Requires what paged_chunk_attention does.
  */
@@ -474,8 +474,9 @@ typedef struct {
  *   weights  [batch, weights_stride] fp32, as paged_attention_weights gathers them
  *   context_lens [batch], block_table [batch, block_table_stride] int32: read
  *   free_blocks [num_free] int32: ids of free blocks, in the order to take them.
- *            A sequence that the list does not suffice for, after the longer ones
- *            before it, stays as it is, and so do the others behind the end
+ *            Sequences ask for blocks in their order; from the first on whose
+ *            blocks, with those asked for before, are more than num_free, longer
+ *            sequences stay as they are
  *   pools    [num_pools] (host memory, read before the call returns), at most 16
  *   new_context_lens [batch] int32: tokens afterwards
  *   new_block_table [batch, new_block_table_stride] int32: entries for them, and
@@ -492,12 +493,12 @@ typedef struct {
  *   counts   [2] int32: blocks asked of the free list (more than num_free: it did
  *            not suffice), blocks in freed_blocks
  *   workspace of at least paged_kv_evict_workspace_size bytes for the same sizes,
- *            16-byte aligned.
+ *            16-byte aligned, as paged_attention's.
  * Tokens whose old or new block id lies outside [0, num_blocks) are not copied.
- * Nothing that is written may overlap anything else, free blocks no block of a
- * sequence.  Requires 1 <= batch <= 8192, block_size in {16, 32, 64}, 1 <= keep,
- * 0 <= recent <= keep, batch * max_context_len and batch * keep below 2^31,
- * num_blocks * block_size < 2^31.
+ * Nothing that is written may overlap anything else (no output may be an input),
+ * free blocks no block of a sequence.  Requires 1 <= batch <= 8192, block_size in
+ * {16, 32, 64}, 1 <= keep <= 2^30, 0 <= recent <= keep, max_context_len < 2^29 - 2^18,
+ * batch * max_context_len and batch * keep below 2^31, num_blocks * block_size < 2^31.
  */
 int64_t paged_kv_evict_workspace_size(int32_t batch, int32_t max_context_len);  /* bytes; negative on error */
 mqa_status paged_kv_evict(const float* weights, int64_t weights_stride, const int32_t* context_lens,
