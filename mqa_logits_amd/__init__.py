@@ -879,8 +879,8 @@ def paged_kv_evict(weights, context_lens, block_table, free_blocks, pools, keep,
     paged_kv_evict_workspace_size bytes to keep between calls on one stream, or None."""
     if weights is None or context_lens is None or free_blocks is None or pools is None:
         _required(weights=weights, context_lens=context_lens, free_blocks=free_blocks, pools=pools)
-    if not pools:
-        raise ValueError("pools must hold at least one tensor")
+    if not pools or any([p is None for p in pools]):
+        raise ValueError("pools must hold tensors, at least one")
     if len(pools[0].shape) < 2:
         raise ValueError(f"pools must be [num_blocks, block_size, ...], got {tuple(pools[0].shape)}")
     lead = pools[0].shape[:2]

@@ -166,7 +166,7 @@ def test_cpu_tensors_and_sizes_are_refused(fn):
     dict(workspace=torch.zeros(64)))] + [(mq.paged_kv_evict, c) for c in (
         dict(weights=torch.zeros(2, 15)), dict(weights=torch.zeros(2, 16).double()), dict(weights=torch.zeros(16, 2).t()),
         dict(context_lens=i32(3)), dict(block_table=i32(2, 0)), dict(free_blocks=i32(3, 1)), dict(free_blocks=i32(3).long()),
-        dict(pools=[]), dict(pools=[u8(3)]), dict(pools=[u8(3, 8, 2)]), dict(pools=[u8(3, 16, 2), u8(4, 16, 2)]),
+        dict(pools=[]), dict(pools=[None]), dict(pools=[u8(3, 16, 2), None]), dict(pools=[u8(3)]), dict(pools=[u8(3, 8, 2)]), dict(pools=[u8(3, 16, 2), u8(4, 16, 2)]),
         dict(pools=[u8(3, 16, 4)[:, :, ::2]]), dict(keep=0), dict(recent=9), dict(recent=-1), dict(workspace=torch.zeros(64)),
         dict(out=(i32(2), i32(2, 1), torch.zeros(2, 16), i32(2, 8), i32(2), i32(3))),
         dict(out=(i32(2), i32(2, 0), torch.zeros(2, 16), i32(2, 8), i32(2), i32(2))))],

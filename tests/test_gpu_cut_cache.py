@@ -264,3 +264,37 @@ def test_fewer_candidates_than_stay_in_a_long_row():
     for name, g, r in zip(NAMES, got, ref):
         assert np.array_equal(g.cpu().numpy().view(np.int32), r.view(np.int32)), name
     assert got.context_lens.tolist() == [13, 19995 + 10]
+
+
+def test_nothing_to_do():
+    """No tokens, no context, or neither."""
+    import mqa_logits_amd as mq
+    c = Held([40, 7], [3, 2], 8, 2, 64, 16, "bf16", seed=1)
+    free, zero = spare(c, 4), torch.zeros(3, dtype=torch.int32, device="cuda")
+    q, sums = c.q.cuda(), torch.rand(2, c.max_ctx, device="cuda")
+    pools = [c.dk, c.dks, c.dv, c.dvs]
+    out, lse = mq.paged_chunk_attention("mxfp4", q[:0], *pools, c.dctx, zero, c.dtable, c.max_ctx, return_lse=True)
+    assert out.shape == (0, 8, 64) and lse.shape == (0, 8)
+    w = mq.paged_attention_weights("mxfp4", q[:0], lse, c.dk, c.dks, c.dctx, zero, c.dtable, c.max_ctx, weights=sums)
+    seen = torch.arange(c.max_ctx, device="cuda") < c.dctx[:, None]
+    assert torch.equal(w, torch.where(seen, sums, 0))
+    # a bound of no keys
+    out, lse = mq.paged_chunk_attention("mxfp4", q, *pools, c.dctx, c.doff, c.dtable[:, :0].contiguous(), 0, return_lse=True)
+    assert not out.any() and bool((lse == -float("inf")).all())
+    assert mq.paged_attention_weights("mxfp4", q, lse, c.dk, c.dks, c.dctx, c.doff, c.dtable, 0).shape == (2, 0)
+    e = mq.paged_kv_evict(sums, c.dctx, c.dtable, free, pools, 20, 5, 0)
+    assert e.context_lens.tolist() == [0, 0] and e.counts.tolist() == [0, 0] and bool((e.kept == -1).all())
+    # an empty free list
+    e = mq.paged_kv_evict(sums, c.dctx, c.dtable, free[:0], pools, 20, 5, c.max_ctx)
+    assert e.context_lens.tolist() == [40, 7] and e.counts.tolist() == [2, 0] and torch.equal(e.weights, w)
+
+
+def test_contexts_beyond_their_bound_and_of_negative_length():
+    for hq, hkv, new in ((8, 2, 3), (64, 1, 6)):
+        c = Held([300, 90, 500], [new] * 3, hq, hkv, 64, 16, "fp16", max_ctx=200, seed=3)
+        c.ctx[1] = -4
+        c.dctx = dev(c.ctx)
+        out, lse = c.check("bounded")
+        import mqa_logits_amd as mq
+        w = mq.paged_attention_weights("mxfp4", c.q.cuda(), lse, c.dk, c.dks, c.dctx, c.doff, c.dtable, 200, scale=c.scale)
+        assert not w[1].any() and bool((w[0] > 0).any()) and bool((w[2, -1:] > 0).all())
