@@ -14,7 +14,8 @@
 //
 // Few rows (weights_kernel): the cache's bytes, D/2 + D/32 for a key and KV head.
 // 32 sequences of 1024..32768 keys, 8 KV heads of 8 rows: 79 us, 3.7 TB/s; waves wait
-// for memory 56% of the time (two items ahead instead of one measured the same).
+// for memory 56% of the time.  Two items ahead instead of one, eight heads beside each
+// other, or whole lines handed over through LDS measured the same.
 // Many rows (weights_wide_kernel): matrix cores and vector ALU.  A tile of 32 rows x 64 keys
 // is 16 products (512 cycles) and, a lane, 32 exponentials, shifts and additions
 // (about 600), formed between the products of the tile that follows; two tiles of two
