@@ -841,6 +841,17 @@ mqa_status paged_chunk_attention(mqa_dtype dt, const void* q, mqa_float q_type, 
   p.members = a.members;
   p.workers = a.workers;
   p.whole = a.whole;
+  if (a.whole) {
+    // Few tiles (counting those that a sequence with all tokens would have): a workgroup
+    // knows its own without the others' lengths (a chunk of 17 tokens 12.5 us, by the
+    // lengths 14.1).
+    const int64_t most = ((token_offsets ? tokens : tokens / batch) + a.tile_tokens - 1) / a.tile_tokens;
+    const int64_t direct = most * batch * a.members;
+    if (direct <= mqa::kChunkResident) {
+      p.direct = (int32_t)most;
+      p.workers = (int32_t)direct;
+    }
+  }
   p.least = a.whole ? 1 : kChunkLeast;
   p.negate = scale < 0.f;
   p.c2 = positive_c2(scale);

@@ -228,6 +228,17 @@ struct Piece {
     return (int)(step < head ? step / (each + 1) : more + (step - head) / each);
   }
 
+  // One tile for each worker: no need to find out which.
+  __device__ __forceinline__ bool take(const ChunkParams& p, int worker) {
+    const int row = worker / p.direct;
+    tile = worker - row * p.direct;
+    member = row / p.batch;
+    b = row - member * p.batch;
+    begin = at = tile_begin = 0;
+    end = 1;
+    return tile < Seq::of<true>(p, b).tiles;
+  }
+
   __device__ __forceinline__ bool find(const ChunkParams& p, int worker, int64_t* sums, int64_t* found) {
     int64_t all = 0, part, mine = 0, before = 0;
     const auto weigh = [&](int i) {
@@ -999,8 +1010,8 @@ chunk_kernel(const ChunkParams p) {
   // neighbouring workers, which read the same keys, on one XCD
   const int worker = (blockIdx.x & 7) * ((p.workers + 7) / 8) + (blockIdx.x >> 3);
   if (tid < 8) stage.flags[tid >> 1][tid & 1] = -1;
-  Piece piece;                               // (find has barriers)
-  const bool any = worker < p.workers && piece.find(p, worker, sums, found);
+  Piece piece;
+  const bool any = worker < p.workers && (p.direct ? piece.take(p, worker) : piece.find(p, worker, sums, found));
   if (!any) {
     if (p.notes && tid == 0 && worker < p.workers) p.notes[worker].parts = 0;
     return;

@@ -154,13 +154,11 @@ struct ChunkParams {
   int32_t head_groups, members;      // tiles beside each other on a KV head; on all of them
   int32_t workers;           // workgroups
   int32_t whole;             // tiles are never cut
+  int32_t direct;            // whole, and a worker for each of so many tiles of every sequence (0: not so)
   int32_t least;             // steps that a worker takes at least, if there are that many
   int32_t negate;            // scale < 0: the queries' signs are flipped
   float c2;                  // |scale| * log2(e)
 };
-
-// Blocks of 64 keys that a wave of the weights kernel takes at most.
-
 
 struct WeightParams {
   const uint16_t* q;         // [tokens, Hq, D] bf16 or fp16 bits

@@ -178,3 +178,11 @@ def test_offsets_past_the_rows(dtype):
     assert torch.equal(out, whole[:50]) and torch.equal(part, lse[:50])
     c = Case([70, 300], [33, 33], 8, 2, 64, 32, dtype, seed=1)
     assert all(torch.equal(a, b) for a, b in zip(c.run(), c.run(token_offsets=None)))
+
+
+@pytest.mark.parametrize("batch", [5, 70])
+def test_small_contexts(batch):
+    """Tiles that are never cut, known to their workgroups or found by the lengths."""
+    rng = np.random.default_rng(batch)
+    ctx = rng.integers(0, 500, batch)
+    Case(ctx, np.minimum(ctx, rng.integers(0, 60, batch)), 16, 8, 64, 16, "fp16", max_ctx=500, seed=batch).check("small contexts")
