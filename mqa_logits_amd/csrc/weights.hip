@@ -20,7 +20,7 @@
 // is 16 products (512 cycles) and, a lane, 32 exponentials, shifts and additions
 // (about 600), formed between the products of the tile that follows; two tiles of two
 // waves of a SIMD take 2450 cycles.  64 sequences of 1024..32768 keys, 256 rows: 89 us,
-// 0.8 PFLOP/s; 2048 rows of each of 8 KV heads past 32768 keys: 152 us, 0.9.
+// 0.8 PFLOP/s; 2048 rows of each of 8 KV heads past 32768 keys: 139 us, 0.98.
 //
 // Workers, two workgroups for each CU, share the blocks of 64 keys evenly by what
 // they cost (Share); with a workgroup for each piece of a sequence instead, of 512
