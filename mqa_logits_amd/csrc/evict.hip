@@ -17,7 +17,7 @@
 // V, 128 of the indexer's keys and three scales of 4 cost about 430 bytes of reads
 // instead of 268.
 //   64 sequences of up to 32768 tokens to 4096, one KV head and an index: 61 us
-//     (top-k 25, plan 3, move 33: 178 MB of lines at 5 TB/s);
+//     (top-k 25, plan 3 to 5, move 32: 178 MB of lines at 5.5 TB/s);
 //   one of 131072 to 16384, eight KV heads: 42 us a call from Python, which its eight
 //     launches bound (selection 24 us on the device, plan 3, move 9);
 //   3 of up to 600 to 128: 31 us a call, the same with four (15 on the device).

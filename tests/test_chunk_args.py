@@ -108,6 +108,8 @@ def test_workspace_sizes():
     assert chunk(2, 0, 8, 2, 128, 100000) == 0 and chunk(1, 17, 16, 2, 128, 113) == 0
     assert chunk(1, 4096, 64, 8, 128, 65536) > 0
     assert weights(64, 256, 64, 1, 128, 32768) == 0 and weights(1, 256, 64, 8, 128, 32768) % (4 * 32768) == 0
+    # (64 parts of 256 rows, three padding rows behind them: as many splits; then 16)
+    assert weights(1, 259, 64, 8, 128, 32768) == 4 * 32768 * 64 and weights(1, 67, 64, 8, 128, 32768) == 4 * 32768 * 16
     assert weights(3, 0, 8, 2, 128, 1000) == 0 and weights(1, 4, 8, 2, 128, 0) >= 0
     assert evict(3, 600) < evict(64, 600) < 1 << 20 and evict(1, 131072) > 3 * 2048 * 4
     for fn, bad in ((chunk, (0, 1, 8, 1, 128, 1)), (chunk, (1, 1, 8, 3, 128, 1)), (chunk, (1, 1, 8, 1, 96, 1)),
