@@ -594,27 +594,9 @@ struct Rows {
     r += w.rounded;
   }
 
-  // The weights of 32 keys, and their V.
-  __device__ __forceinline__ void finish(f32x16& x, const char* lds, uint32_t values, int lane, float c2) {
-    const uint32_t v = value_at(values, lane);
-    Weights w;
-    form(x, w, c2);
-    check(x, w, c2);
-    u32x4 a[kAhead];
-#pragma unroll
-    for (int n = 0; n < kAhead; ++n) a[n] = value_operand(lds, v, n);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int n = 0; n < kValOps; ++n) {
-      o[n % kCols] = mma<true>(a[n % kAhead], w.w[n / kCols], o[n % kCols]);
-      if (n + kAhead < kValOps) a[n % kAhead] = value_operand(lds, v, n + kAhead);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
-
-  // The same for scores x, with the products of the next 32 keys between the
-  // weights, and other work (0 .. kValOps - 1) between V's: the matrix cores and the
-  // vector ALU work side by side.
+  // The weights of the 32 keys of scores x and their V, with the products of the next
+  // 32 keys between the weights, and other work (0 .. kValOps - 1) between V's: the
+  // matrix cores and the vector ALU work side by side.
   // a: the first operands of `keys`, and then of `then`.
   template <class Work>
   __device__ __forceinline__ void finish_and_multiply(f32x16& x, f32x16& next, u32x4 (&a)[kAhead], const char* lds, uint32_t values,

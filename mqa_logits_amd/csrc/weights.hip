@@ -362,9 +362,9 @@ struct Wave {
     for (int st = 0; st < kSteps; ++st) x.q[st] = *reinterpret_cast<const u32x4*>(src + st * 8);
   }
 
-  // rows: that the tile has (FULL: 32).  key0: the first of the keys (MASKED: some
+  // rows: that the tile has.  key0: the first of the keys (MASKED: some
   // row may not see all of them).
-  template <bool WIDE, bool MASKED, bool FULL, class Places>
+  template <bool WIDE, bool MASKED, class Places>
   __device__ __forceinline__ void add(const Tile& x, const Places& places, int tile, int rows, int key0, float c2) {
     const int lane = fresh(threadIdx.x & 63), half = lane >> 5;
     f32x4 shift[4];
@@ -417,7 +417,7 @@ struct Wave {
     // registers 4 a .. 4 a + 3: rows 8 a + 4 half ..
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
-      if (!FULL && 8 * a >= rows) break;
+      if (8 * a >= rows) break;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -592,11 +592,11 @@ weights_kernel(const WeightParams p) {
                 const int n = min(rows - t * 32, 32);
                 const bool masked = some_left_out || s.seen((int)((r0 + t * 32) / p.group)) < key0 + kKeys;
                 if (F16 && wide)
-                  w.template add<F16, true, false>(x, places, t, n, key0, p.c2);
+                  w.template add<F16, true>(x, places, t, n, key0, p.c2);
                 else if (masked)
-                  w.template add<false, true, false>(x, places, t, n, key0, p.c2);
+                  w.template add<false, true>(x, places, t, n, key0, p.c2);
                 else
-                  w.template add<false, false, false>(x, places, t, n, key0, p.c2);
+                  w.template add<false, false>(x, places, t, n, key0, p.c2);
               }
               sums[block * kKeys + lane] += w.take_sums();
             }
@@ -827,9 +827,9 @@ weights_wide_kernel(const WeightParams p) {
 #pragma unroll
               for (int st = 0; st < D / 16; ++st) tile.q[st] = *reinterpret_cast<const u32x4*>(q + st * 16);
               if (F16 && wide)
-                w.template add<F16, true, false>(tile, x, tile0 + t, n - t * 32, key0, p.c2);
+                w.template add<F16, true>(tile, x, tile0 + t, n - t * 32, key0, p.c2);
               else
-                w.template add<false, true, false>(tile, x, tile0 + t, n - t * 32, key0, p.c2);
+                w.template add<false, true>(tile, x, tile0 + t, n - t * 32, key0, p.c2);
             }
             pending[1].clear(none);
           }
