@@ -3,9 +3,8 @@
 // blocks from a free list.
 //
 //   ranges   which columns the choice is made from: [0, ctx - recent)
-//   (top-k)  the library's own, over the rows of weights; or, for a few rows that
-//            are longer than a workgroup holds, a radix selection over many
-//            workgroups (below)
+//   (top-k)  the library's own, over the rows of weights; or, for a few long rows, a
+//            radix selection over many workgroups (below)
 //   plan     one workgroup: new lengths, and where each sequence's blocks begin in
 //            the free list and in the list of freed ones
 //   move     tokens, weights, positions and tables, a chunk of a sequence per
@@ -114,8 +113,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const EvictParams p)
 // keys by 11, 11 and 10 bits of those that agree with what is known of it.  (Counts
 // of integers do not depend on the order in which they are added.)  Then every
 // workgroup counts what its columns give, and writes them behind the others'.
-// A workgroup per row, as in the top-k, takes 134 us for 15360 of 131072 columns;
-// these five launches 24.
+// Whole evictions in a graph, by the top-k's workgroup a row and by this, an eighth of
+// the columns kept: one row of 16384 columns 17 us against 27, of 32768 24 against 27,
+// of 40000 48 against 27, of 131072 124 against 29; 64 rows of 16384 21 against 35, of
+// 33000 47 against 48, of 65536 90 against 62; 96 of 40000 65 against 63, 256 95 against 115.
 constexpr int kSelectThreads = 256, kEach = 8, kColumns = kSelectThreads * kEach;   // of a workgroup
 constexpr int kBins = 2048;
 constexpr int kSelectRows = 64, kSelectFrom = 32768;   // rows at most, of more columns than that
