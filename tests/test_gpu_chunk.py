@@ -186,3 +186,10 @@ def test_small_contexts(batch):
     rng = np.random.default_rng(batch)
     ctx = rng.integers(0, 500, batch)
     Case(ctx, np.minimum(ctx, rng.integers(0, 60, batch)), 16, 8, 64, 16, "fp16", max_ctx=500, seed=batch).check("small contexts")
+
+
+def test_shortest_contexts():
+    """Tiles that are never cut, more than the chip holds."""
+    rng = np.random.default_rng(9)
+    ctx = rng.integers(0, 257, 90)
+    Case(ctx, np.minimum(ctx, rng.integers(0, 80, 90)), 24, 8, 128, 32, "bf16", max_ctx=256, seed=9).check("shortest contexts")
