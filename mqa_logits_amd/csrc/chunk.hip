@@ -816,6 +816,7 @@ __device__ __forceinline__ void walk(const ChunkParams& p, Rows<D, F16>& rows, S
   }
   if (__builtin_expect(i == steps, 1)) return;
   // from a step with unusual scales on, in bf16, NaN scales apart
+  held = -64;                                // (the loads were ahead, maybe in the next 64 steps)
   fetch(raw, i);
 #pragma nounroll
   for (; i < steps; ++i) {
