@@ -44,6 +44,7 @@
 #include <cstddef>
 #include <type_traits>
 
+#include "chunk_split.hpp"
 #include "launch.hpp"
 
 namespace mqa {
@@ -60,10 +61,9 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kKeys = 64;                    // of a step
+constexpr int kKeys = kChunkKeys;            // of a step
 constexpr int kStage = 16384;                // keys whose places LDS holds at a time
-// Steps that beginning and ending a tile takes as long as (about 8 us; a step 2).
-constexpr int kTileSteps = 4;
+constexpr int kTileSteps = kChunkTileSteps;  // that beginning and ending a tile counts for
 constexpr uint32_t kLastScale = 252;         // bytes above could overflow fp32: they count as NaN
 // Scale bytes (2^-22 .. 2^9) whose steps are worked on in fp16.  Every e2m1 value
 // under 2^-23 .. 2^13 is exact there; large ones are left out for what the weights'
@@ -125,15 +125,10 @@ __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
 // ---------------------------------------------------------------------------
 
 // Sequence b of the call.
-struct Seq {
-  int64_t base;            // keys before its first new token (may be negative)
-  int cap;                 // keys of the context
-  int first, n;            // its rows of q
-  int tiles;
+struct Seq : ChunkSeq {
   // UNIFORM: b is the same in every lane, and everything stays in scalar registers.
   template <bool UNIFORM>
   __device__ __forceinline__ static Seq of(const ChunkParams& p, int b) {
-    Seq s;
     const auto get = [](int x) { return UNIFORM ? __builtin_amdgcn_readfirstlane(x) : x; };
     int64_t lo, hi;
     if (p.offsets) {
@@ -143,48 +138,9 @@ struct Seq {
       lo = (int64_t)b * p.next_n;
       hi = lo + p.next_n;
     }
-    const int ctx = get(p.ctx[b]);
-    s.cap = min(max(ctx, 0), p.max_ctx);
-    const int64_t from = min(max(lo, (int64_t)0), (int64_t)p.tokens);
-    const int64_t to = min(max(hi, from), (int64_t)p.tokens);
-    s.base = (int64_t)ctx - (hi - lo) + (from - lo);   // (rows cut off in front: keys that stay)
-    s.first = (int)from;
-    s.n = (int)(to - from);
-    s.tiles = (s.n + p.tile_tokens - 1) / p.tile_tokens;
+    Seq s;
+    s.set(p, get(p.ctx[b]), lo, hi);
     return s;
-  }
-  // keys that its row t sees
-  __device__ __forceinline__ int seen(int64_t t) const {
-    return (int)min(max(base + 1 + t, (int64_t)0), (int64_t)cap);
-  }
-  __device__ __forceinline__ int tile_seen(const ChunkParams& p, int i) const {
-    return seen(min((int64_t)(i + 1) * p.tile_tokens, (int64_t)n) - 1);
-  }
-  // What a tile counts for in the split: its steps, and kTileSteps to begin and end it.
-  __device__ __forceinline__ int steps(const ChunkParams& p, int i) const {
-    return p.whole ? 1 : (tile_seen(p, i) + kKeys - 1) / kKeys + kTileSteps;
-  }
-  // The same for its first k tiles: none while no keys are seen, then the sum of
-  // floor((tile_tokens * i + c) / 64), then the context's.
-  __device__ __forceinline__ int64_t before(const ChunkParams& p, int k) const {
-    if (p.whole) return k;
-    const int a = p.tile_tokens;
-    const int64_t full = cap - base;
-    const int64_t none = base >= 0 ? 0 : -base / a;                 // tiles that see nothing
-    const int64_t until = full <= a ? 0 : (full + a - 1) / a - 1;   // tiles below the cap
-    const int64_t i1 = min(none, (int64_t)k), i2 = min(max(until, i1), (int64_t)k);
-    int64_t sum = (int64_t)k * kTileSteps + (k - i2) * (int64_t)((cap + kKeys - 1) / kKeys);
-    const int64_t m = i2 - i1, turns = m / kKeys;
-    if (m > 0) {
-      const int64_t c = base + (i1 + 1) * a + kKeys - 1;
-      const int d = a & -a & (kKeys - 1) ? a & -a : kKeys;          // gcd(a, 64)
-      const int64_t turn = ((int64_t)(a - 1) * (kKeys - 1) + d - 1) / 2 + c / d * d;
-      sum += turns * turn + (int64_t)a * kKeys * (turns * (turns - 1) / 2);
-      const int r = (int)(m - turns * kKeys);
-      sum += (int64_t)r * a * turns;
-      for (int i = 0; i < r; ++i) sum += (c + (int64_t)a * i) / kKeys;
-    }
-    return sum;
   }
 };
 
@@ -217,16 +173,10 @@ __device__ __forceinline__ int64_t scan(int64_t mine, int64_t* sums, int64_t& to
 }
 
 // A worker's piece of the steps of all members' sequences' tiles, laid end to end.
-struct Piece {
-  int64_t begin, end, each, more, at;
+struct Piece : ChunkBorders {
+  int64_t begin, end, at;
   int64_t tile_begin;      // where the tile at `at` begins
-  int workers, member, b, tile;
-
-  __device__ __forceinline__ int64_t border(int64_t j) const { return j * each + min(j, more); }
-  __device__ __forceinline__ int owner(int64_t step) const {
-    const int64_t head = more * (each + 1);
-    return (int)(step < head ? step / (each + 1) : more + (step - head) / each);
-  }
+  int member, b, tile;
 
   // One tile for each worker: no need to find out which.
   __device__ __forceinline__ bool take(const ChunkParams& p, int worker) {
@@ -252,10 +202,7 @@ struct Piece {
       all += part;
     }
     all = uniform(all);
-    const int64_t steps = all * p.members;
-    workers = (int)min((int64_t)p.workers, max(steps / p.least, (int64_t)1));
-    each = steps / workers;
-    more = steps - each * workers;
+    divide(all * p.members, p.workers, p.least);
     begin = at = border(worker);
     end = border(worker + 1);
     if (worker >= workers || begin >= end) return false;
@@ -973,10 +920,11 @@ __device__ __forceinline__ void work(const ChunkParams& p, Piece piece, int work
       do {
         if (++piece.b == p.batch) {
           piece.b = 0;
-          ++piece.member;
+          // (no tile is behind the last KV head, even if lengths change during the call)
+          if (++piece.member == p.members) piece.end = piece.at;
         }
         s = Seq::of<true>(p, piece.b);
-      } while (s.tiles == 0);
+      } while (s.tiles == 0 && piece.at < piece.end);
     }
   }
   if (p.notes && tid == 0) p.notes[worker] = note;
