@@ -657,7 +657,6 @@ weights_wide_kernel(const WeightParams p) {
     const int rows = s.n * p.group;          // of a head
     const int tiles_all = (rows + 31) / 32, heads = max(min(kTiles / max(tiles_all, 1), p.kv_heads), 1);   // of a unit
     const int groups = (p.kv_heads + heads - 1) / heads, units = (tiles_all + kTiles - 1) / kTiles * groups;
-    int staged = -1;                         // unit whose rows are in LDS
     // (the sums of one unit need not wait for another's: all blocks at once)
     const int spans = units - split > p.splits ? (to - from + kWideSpan - 1) / kWideSpan : 1;
     for (int span = 0; span < spans; ++span) {
@@ -701,8 +700,7 @@ weights_wide_kernel(const WeightParams p) {
         const int n_heads = min(heads, p.kv_heads - head0);
         const bool first_unit = unit == split, last_unit = unit + p.splits >= units;
         __syncthreads();                     // (the rows before are done with)
-        if (unit != staged) {
-          staged = unit;
+        {
           const int tid = fresh(threadIdx.x);
           // Quotients by products: of at most 7 by at most 8, and of less than 2^16
           // by a group of less than 2^16 (the factors too large by less than 1).
@@ -741,9 +739,6 @@ weights_wide_kernel(const WeightParams p) {
           x.seen[tid] = gives ? seen : 0;
           const bool left_out = __any(is && !gives);
           if (lane == 0) x.left_out[wave] = left_out;
-        } else if (first_unit && wave < here) {
-          next_block();
-          fetch(head0);
         }
         __syncthreads();
         const bool left_out = x.left_out[0] || x.left_out[1] || x.left_out[2] || x.left_out[3];
