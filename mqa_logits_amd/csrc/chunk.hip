@@ -19,9 +19,12 @@
 // are its operand of the second product as they stand, and V is stored with the keys
 // in that order.  e2m1 under its scale is exact in bf16 and, for the scales that
 // occur (2^-22 .. 2^9), in fp16: K takes q's type, V fp16, in which a weight keeps 2^-12
-// with one product, where bf16 took two.  A step with other scales, or with NaN ones,
-// leaves the loop for one in bf16 with the weights in two parts.  The sum that a result
-// is divided by is that of the rounded weights.
+// with one product, where bf16 took two.  At a step with other scales, or with NaN ones,
+// a workgroup leaves the loop for one in bf16 with the weights in two parts, up to the end
+// of the stretch (16384 keys at most).  That one takes 1.7 times as long (64 sequences as
+// below with such a scale in every block 1.93 ms, with one in the middle of each 1.56),
+// with D = 64 and fp16 queries 2.6 times.  The sum that a result is divided by is that of
+// the rounded weights.
 //
 // What bounds it: the matrix cores and the vector ALU, and beyond them power.  A step is 32
 // products (1024 cycles) a wave, two waves a SIMD, and 32 exponentials, scalings, sums
@@ -29,16 +32,19 @@
 // one wave in turn, so each half of a step (32 keys) is finished, weights and second
 // product, between the products of the scores that follow it; the order is fixed
 // by hand.  With everything in bf16 and one part after the other 4096 query tokens over
-// 65536 keys took 13.1 ms.  They take 8.3 now, 1.03 PFLOP/s (6.7 ms on a cache of
+// 65536 keys took 13.1 ms.  They take 8.4 now, 1.02 PFLOP/s (6.7 ms on a cache of
 // zeros: the rest is the clock, which goes down to 2.0 GHz under random data; matrix
 // cores busy 48%); 64 sequences of 1024..32768 keys, 32 query tokens of 64 heads,
-// 1.11 ms, 1.02 PFLOP/s.  Short prompts pay for tiles' beginnings and ends: 33 of
-// 1..1900 tokens take 471 us, of which about 7 us a tile (16 a workgroup, of ten steps)
+// 1.14 ms, 0.99 PFLOP/s.  Short prompts pay for tiles' beginnings and ends: 33 of
+// 1..1900 tokens take 480 us, of which about 7 us a tile (16 a workgroup, of ten steps)
 // are the latencies of its first loads and its last stores.
 //
 // Work is divided evenly: the steps of all tiles, and a few for what a tile costs
 // besides, lie end to end, and each of 256 workers takes as many.  A tile that a border
-// cuts is left in parts, that a second kernel joins (15 us for 256 of them).
+// cuts is left in parts, that a second kernel joins (15 us for 256 of them).  A tile
+// costs its steps whatever rows it has: single new tokens beside a long chunk are better
+// left to paged_attention (63 sequences of 1024..32768 keys, 64 heads on one KV head: 142 us
+// here, 78 there).
 #include <hip/hip_runtime.h>
 
 #include <cstddef>

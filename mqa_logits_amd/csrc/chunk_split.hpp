@@ -11,7 +11,7 @@
 namespace mqa {
 
 constexpr int kChunkKeys = 64;               // of a step
-// Steps that beginning and ending a tile takes as long as (about 8 us; a step 2).
+// Steps that beginning and ending a tile takes as long as (about 7 us; a step 2).
 constexpr int kChunkTileSteps = 4;
 
 // A sequence of the call.  (P: ChunkParams, or what a check has of it)

@@ -15,11 +15,12 @@
 // token has in a pool costs whole cache lines: with one KV head 64 bytes of K, 64 of
 // V, 128 of the indexer's keys and three scales of 4 cost about 430 bytes of reads
 // instead of 268.
-//   64 sequences of up to 32768 tokens to 4096, one KV head and an index: 61 us
+//   64 sequences of up to 32768 tokens to 4096, one KV head and an index: 75 us, 61 where
+//     the last-level cache still holds the pools from the call before
 //     (top-k 25, plan 3 to 5, move 32: 178 MB of lines at 5.5 TB/s);
-//   one of 131072 to 16384, eight KV heads: 42 us a call from Python, which its eight
+//   one of 131072 to 16384, eight KV heads: 40 us a call from Python, which its eight
 //     launches bound (selection 24 us on the device, plan 3, move 9);
-//   3 of up to 600 to 128: 31 us a call, the same with four (15 on the device).
+//   3 of up to 600 to 128: 28 us a call, the same with four (15 on the device).
 #include <hip/hip_runtime.h>
 
 #include "launch.hpp"

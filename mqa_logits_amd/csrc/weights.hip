@@ -13,14 +13,14 @@
 // Scores, weights and sums are fp32.
 //
 // Few rows (weights_kernel): the cache's bytes, D/2 + D/32 for a key and KV head.
-// 32 sequences of 1024..32768 keys, 8 KV heads of 8 rows: 79 us, 3.7 TB/s; waves wait
+// 32 sequences of 1024..32768 keys, 8 KV heads of 8 rows: 81 us, 3.6 TB/s; waves wait
 // for memory 56% of the time.  Two items ahead instead of one, eight heads beside each
 // other, or whole lines handed over through LDS measured the same.
 // Many rows (weights_wide_kernel): matrix cores and vector ALU.  A tile of 32 rows x 64 keys
 // is 16 products (512 cycles) and, a lane, 32 exponentials, shifts and additions
 // (about 600), formed between the products of the tile that follows; two tiles of two
-// waves of a SIMD take 2450 cycles.  64 sequences of 1024..32768 keys, 256 rows: 89 us,
-// 0.8 PFLOP/s; 2048 rows of each of 8 KV heads past 32768 keys: 139 us, 0.98.
+// waves of a SIMD take 2450 cycles.  64 sequences of 1024..32768 keys, 256 rows: 82 us,
+// 0.86 PFLOP/s; 2048 rows of each of 8 KV heads past 32768 keys: 138 us, 0.99.
 //
 // Workers, two workgroups for each CU, share the blocks of 64 keys evenly by what
 // they cost (Share); with a workgroup for each piece of a sequence instead, of 512
